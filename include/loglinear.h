@@ -371,6 +371,127 @@ size_t ssd_fwd_workspace_bytes(const ll_shape* shape);
 ll_status ssd_fwd(const ll_shape* shape, const void* q, const void* k, const void* v,
                   const float* a, void* o, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- linear attention with a decay per head ----------------------------------------------
+ * Where the forward above takes a decay per token and weighs each bucket, these take one
+ * constant decay per head and no weights: for every batch row b and head h, with group
+ * g = h / heads_per_group and gamma = exp(log_a[h]),
+ *     S_t = gamma S_{t-1} + k[b,t,g,:] v[b,t,h,:]ᵀ,     o[b,t,h,:] = S_tᵀ q[b,t,g,:],
+ * S_{-1} = state_in or 0.  (The state-space-duality article, section 狀態空間對偶性, with
+ * the decay held constant.)
+ *
+ * Shapes: ll_shape with any T >= 1 (2^30 at most); d_k and d_v multiples of 8 from 8 to 128;
+ * batch * heads <= 2^20; chunk and levels are ignored.  q, k, v, o and their gradients have
+ * shape->dtype; states (B, H, d_k, d_v), log_a (H) and their gradients are fp32.  bf16 runs
+ * on the tensor cores, fp32 on the CUDA cores.
+ *
+ * log_a is a constant of the model (no gradient is returned for it).  Values above 0 count
+ * as 0 (no decay), values below -1000 as -1000 (gamma is 0 in fp32).
+ *
+ * lengths: NULL, or (B) int32 on the device: row b holds lengths[b] tokens, clamped to
+ * [0, T].  What the tensors hold past them is not used, NaN included; the outputs there are
+ * written as zeros, and final states are those after lengths[b] tokens (state_in itself for
+ * length 0).  A NaN or infinity inside a row's length can reach every output of its
+ * 128-token chunk, earlier tokens included (0 times infinity in a masked product).
+ */
+
+/* Bytes of device workspace lindecay_fwd needs (0: invalid shape). */
+size_t lindecay_fwd_workspace_bytes(const ll_shape* shape);
+
+/*
+ * The whole sequence.
+ *   q, k (B, T, G, d_k), v (B, T, H, d_v)   dtype
+ *   log_a     (H) fp32
+ *   lengths   NULL or (B) int32
+ *   state_in  NULL or (B, H, d_k, d_v) fp32, the state before the first token
+ *   o         (B, T, H, d_v) dtype, written
+ *   state_out NULL or (B, H, d_k, d_v) fp32, written; may be state_in
+ *   workspace >= lindecay_fwd_workspace_bytes(shape) bytes; contents do not matter
+ */
+ll_status lindecay_fwd(const ll_shape* shape, const void* q, const void* k, const void* v, const float* log_a,
+                       const int* lengths, const float* state_in, void* o, float* state_out, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/* Bytes of device workspace lindecay_bwd needs (0: invalid shape). */
+size_t lindecay_bwd_workspace_bytes(const ll_shape* shape);
+
+/*
+ * Gradients of sum(dO * o) + sum(dstate_out * state_out), (o, state_out) = lindecay_fwd.
+ *   dO         (B, T, H, d_v) dtype; ignored past a row's length
+ *   state_in   as for the forward (NULL: zero)
+ *   dstate_out NULL (zero) or (B, H, d_k, d_v) fp32
+ *   dq, dk     (B, T, G, d_k) dtype, dv (B, T, H, d_v) dtype, written; the heads of a group
+ *              add up in fp32, in order (the result does not vary between calls)
+ *   dstate_in  NULL or (B, H, d_k, d_v) fp32, written; neither state_in nor dstate_out
+ */
+ll_status lindecay_bwd(const ll_shape* shape, const void* q, const void* k, const void* v, const float* log_a,
+                       const int* lengths, const float* state_in, const void* dO, const float* dstate_out, void* dq,
+                       void* dk, void* dv, float* dstate_in, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * One token for every (b, h): the recurrence itself.  shape->T is ignored.
+ *   q_t, k_t (B, G, d_k), v_t (B, H, d_v) dtype; log_a (H) fp32; o_t (B, H, d_v) dtype, written
+ *   states (B, H, d_k, d_v) fp32, read and updated in place; lindecay_fwd's state_out
+ *   continues here.
+ */
+ll_status lindecay_decode_step(const ll_shape* shape, const void* q_t, const void* k_t, const void* v_t,
+                               const float* log_a, void* o_t, float* states, void* stream);
+
+/* ---- norms around a block ----------------------------------------------------------------
+ * The norm after a block (of its output y, over groups of `group` values), its gate, the
+ * residual add with a scale per channel, and the norm before the next block, in one pass:
+ *     n  = y * rsqrt(mean over the group of y^2 + eps) * w_post
+ *     x' = x + scale * act(gate) * n
+ *     h  = x' * rsqrt(mean over the row of x'^2 + eps) * w_pre
+ * x, gate, w_post, scale and the pair (w_pre, h) may be left out (NULL): without x, x' is
+ * the gated norm alone (a norm per head before the output projection: group = d_v); without
+ * y, h is the norm of x alone (in front of the first block).
+ *   rows   >= 1, below 2^31
+ *   dim    1 to 16384 values per row; a multiple of 8 runs faster
+ *   group  divides dim into at most 4096 groups (dim: one norm per row); dim itself, or a
+ *          power of two from 8 to 256, runs faster
+ *   act    of the gate
+ *   eps    0 to 1
+ * Activations have `dtype`; weights and their gradients are fp32 (dim).  Sums are fp32.
+ */
+enum { BN_IDENTITY = 0, BN_SILU = 1, BN_SIGMOID = 2 };
+typedef struct {
+  long long rows;
+  int dim;
+  int group;
+  int act;
+  float eps;
+  ll_dtype dtype;
+} blocknorm_shape;
+
+/*
+ * Forward.  x, y, gate (rows, dim); x_new (rows, dim), written when y is given (NULL
+ * otherwise); h NULL or (rows, dim), written.  x_new may be x, y or gate, h too (not the
+ * same buffer as x_new).
+ */
+ll_status blocknorm_fwd(const blocknorm_shape* shape, const void* x, const void* y, const void* gate,
+                        const float* w_post, const float* scale, const float* w_pre, void* x_new, void* h,
+                        void* stream);
+
+/* Bytes of device workspace blocknorm_bwd needs (0: invalid shape). */
+size_t blocknorm_bwd_workspace_bytes(const blocknorm_shape* shape);
+
+/*
+ * Gradients of sum(dx_new * x') + sum(dh * h).
+ *   dx_new   NULL (zero) or (rows, dim);  dh NULL, or (rows, dim) together with x_new, the
+ *            forward's x' as stored (x itself without y)
+ *   y, gate, w_post, scale, w_pre as for the forward
+ *   dx       NULL, or (rows, dim): the gradient of x (and of x')
+ *   dy       (rows, dim), with y;  dgate (rows, dim), with gate
+ *   dw_post, dscale, dw_pre  NULL, or (dim) fp32, each with its weight; summed over the rows in a
+ *            fixed order (the result does not vary between calls)
+ *   workspace >= blocknorm_bwd_workspace_bytes(shape) bytes; contents do not matter
+ * No output may overlap an input.
+ */
+ll_status blocknorm_bwd(const blocknorm_shape* shape, const void* dx_new, const void* dh, const void* x_new,
+                        const void* y, const void* gate, const float* w_post, const float* scale,
+                        const float* w_pre, void* dx, void* dy, void* dgate, float* dw_post, float* dscale,
+                        float* dw_pre, void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---- diagnostics -------------------------------------------------------------------- */
 
 /* Same as loglinear_fwd, and records CUDA events on `stream` around its kernels:

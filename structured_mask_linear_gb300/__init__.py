@@ -14,6 +14,11 @@ Functions mirror the C names:
   a forward that starts from the bucket memories at a position T0, and the pieces that
   build those memories from whole earlier segments (see ``sharded`` for a sequence split
   over ranks)
+* ``lindecay_fwd``, ``lindecay_bwd``, ``lindecay_decode_step``: linear attention with one
+  constant decay per head, for prompts (ragged batches, carried states), its gradients and
+  its single-token form
+* ``blocknorm_fwd``, ``blocknorm_bwd``: the norms before and after a block fused with its
+  gate and the residual scale, and their gradients
 * ``loglinear_fwd_workspace_bytes``, ``loglinear_fwd_path``, ``loglinear_check_status``,
   ``loglinear_selftest_wait_timeout``, ``loglinear_status_string``
 """
@@ -22,6 +27,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -47,10 +53,16 @@ class LLShape(ctypes.Structure):
                 ("chunk", ctypes.c_int), ("levels", ctypes.c_int), ("dtype", ctypes.c_int)]
 
 
+class BlocknormShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_longlong), ("dim", ctypes.c_int), ("group", ctypes.c_int), ("act", ctypes.c_int),
+                ("eps", ctypes.c_float), ("dtype", ctypes.c_int)]
+
+
 _lock = threading.Lock()
 _lib = None
 _vp = ctypes.c_void_p
 _SP = ctypes.POINTER(LLShape)
+_BP = ctypes.POINTER(BlocknormShape)
 
 
 def lib() -> ctypes.CDLL:
@@ -118,6 +130,22 @@ def lib() -> ctypes.CDLL:
             L.loglinear_segment_total.argtypes = [_SP] + [_vp] * 4 + [ctypes.c_size_t, _vp, _vp, _vp]
             L.loglinear_prefix_states.restype = ctypes.c_int
             L.loglinear_prefix_states.argtypes = [_SP, ctypes.c_int] + [_vp] * 4 + [ctypes.c_int, _vp]
+            L.lindecay_fwd_workspace_bytes.restype = ctypes.c_size_t
+            L.lindecay_fwd_workspace_bytes.argtypes = [_SP]
+            L.lindecay_fwd.restype = ctypes.c_int
+            L.lindecay_fwd.argtypes = [_SP] + [_vp] * 9 + [ctypes.c_size_t, _vp]
+            L.lindecay_bwd_workspace_bytes.restype = ctypes.c_size_t
+            L.lindecay_bwd_workspace_bytes.argtypes = [_SP]
+            L.lindecay_bwd.restype = ctypes.c_int
+            L.lindecay_bwd.argtypes = [_SP] + [_vp] * 13 + [ctypes.c_size_t, _vp]
+            L.lindecay_decode_step.restype = ctypes.c_int
+            L.lindecay_decode_step.argtypes = [_SP] + [_vp] * 7
+            L.blocknorm_fwd.restype = ctypes.c_int
+            L.blocknorm_fwd.argtypes = [_BP] + [_vp] * 9
+            L.blocknorm_bwd_workspace_bytes.restype = ctypes.c_size_t
+            L.blocknorm_bwd_workspace_bytes.argtypes = [_BP]
+            L.blocknorm_bwd.restype = ctypes.c_int
+            L.blocknorm_bwd.argtypes = [_BP] + [_vp] * 15 + [ctypes.c_size_t, _vp]
             _lib = L
     return _lib
 
@@ -435,3 +463,214 @@ def loglinear_check_status(stream=None) -> int:
 def loglinear_selftest_wait_timeout(spins: int, stream=None) -> None:
     _check(lib().loglinear_selftest_wait_timeout(int(spins), _stream_ptr(stream)),
            "loglinear_selftest_wait_timeout")
+
+
+# ---- linear attention with a decay per head ------------------------------------------------
+def _expect(name, x, shape, dtype, device, optional=False):
+    """x is a contiguous tensor of this shape, type and device (or None where optional)."""
+    if x is None:
+        if optional:
+            return
+        raise ValueError(f"{name} is required")
+    if x.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
+    if x.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(x.shape)}")
+    if x.device != device:
+        raise ValueError(f"{name} is on {x.device}, the other tensors on {device}")
+    if not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+class _Device:
+    """Makes a CUDA device current for a call, where it is not already."""
+
+    def __init__(self, device):
+        if device.type != "cuda":
+            raise ValueError(f"tensors must be on a CUDA device, got {device}")
+        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _workspace(workspace, nbytes, device, where):
+    if nbytes == 0:
+        raise LogLinearError(2, where)
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace
+
+
+def _lindecay_check(q, k, v, log_a, lead):
+    """Checks q, k, v, log_a against each other; returns the shape and its parts."""
+    if q.dim() != lead + 2 or v.dim() != lead + 2:
+        raise ValueError(f"q and v must have {lead + 2} dimensions, got {q.dim()} and {v.dim()}")
+    B, G, dk, H, dv = q.shape[0], q.shape[lead], q.shape[lead + 1], v.shape[lead], v.shape[lead + 1]
+    T = q.shape[1] if lead == 2 else 1
+    if G == 0 or H % G:
+        raise ValueError(f"{H} heads do not divide into {G} groups")
+    dt, dev = q.dtype, q.device
+    code = _dtype_code(dt)
+    head = q.shape[:lead]
+    _expect("q", q, q.shape, dt, dev)
+    _expect("k", k, q.shape, dt, dev)
+    _expect("v", v, head + (H, dv), dt, dev)
+    _expect("log_a", log_a, (H,), torch.float32, dev)
+    return LLShape(B, T, H, H // G, dk, dv, 0, 0, code), (B, H, dk, dv), dt, dev
+
+
+def lindecay_fwd_workspace_bytes(shape: LLShape) -> int:
+    return int(lib().lindecay_fwd_workspace_bytes(ctypes.byref(shape)))
+
+
+def lindecay_bwd_workspace_bytes(shape: LLShape) -> int:
+    return int(lib().lindecay_bwd_workspace_bytes(ctypes.byref(shape)))
+
+
+def lindecay_fwd(q, k, v, log_a, lengths=None, state_in=None, state_out=None, o=None, workspace=None, stream=None):
+    """o of S_t = exp(log_a[h]) S_{t-1} + k_t v_tᵀ, o_t = S_tᵀ q_t.  q, k: (B, T, G, d_k);
+    v: (B, T, H, d_v), bf16 or fp32; log_a: (H,) fp32.  lengths: (B,) int32 tokens per row;
+    state_in, state_out: (B, H, d_k, d_v) fp32 states before the first and after the last
+    token (state_out is written; it may be state_in)."""
+    shape, st_shape, dt, dev = _lindecay_check(q, k, v, log_a, 2)
+    _expect("lengths", lengths, (shape.batch,), torch.int32, dev, True)
+    _expect("state_in", state_in, st_shape, torch.float32, dev, True)
+    _expect("state_out", state_out, st_shape, torch.float32, dev, True)
+    if o is None:
+        o = torch.empty_like(v)
+    else:
+        _expect("o", o, v.shape, dt, dev)
+    with _Device(dev):
+        workspace = _workspace(workspace, lindecay_fwd_workspace_bytes(shape), dev, "lindecay_fwd_workspace_bytes")
+        st = lib().lindecay_fwd(ctypes.byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(),
+                                _ptr(lengths), _ptr(state_in), o.data_ptr(), _ptr(state_out), workspace.data_ptr(),
+                                workspace.numel() * workspace.element_size(), _stream_ptr(stream))
+    _check(st, "lindecay_fwd")
+    return o
+
+
+def lindecay_bwd(q, k, v, log_a, dO, lengths=None, state_in=None, dstate_out=None, dstate_in=None, workspace=None,
+                 stream=None):
+    """Gradients of sum(dO * o) + sum(dstate_out * state_out) of lindecay_fwd: returns dq, dk
+    (B, T, G, d_k) and dv (B, T, H, d_v); dstate_in, where given, receives state_in's."""
+    shape, st_shape, dt, dev = _lindecay_check(q, k, v, log_a, 2)
+    _expect("dO", dO, v.shape, dt, dev)
+    _expect("lengths", lengths, (shape.batch,), torch.int32, dev, True)
+    _expect("state_in", state_in, st_shape, torch.float32, dev, True)
+    _expect("dstate_out", dstate_out, st_shape, torch.float32, dev, True)
+    _expect("dstate_in", dstate_in, st_shape, torch.float32, dev, True)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    with _Device(dev):
+        workspace = _workspace(workspace, lindecay_bwd_workspace_bytes(shape), dev, "lindecay_bwd_workspace_bytes")
+        st = lib().lindecay_bwd(ctypes.byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(),
+                                _ptr(lengths), _ptr(state_in), dO.data_ptr(), _ptr(dstate_out), dq.data_ptr(),
+                                dk.data_ptr(), dv.data_ptr(), _ptr(dstate_in), workspace.data_ptr(),
+                                workspace.numel() * workspace.element_size(), _stream_ptr(stream))
+    _check(st, "lindecay_bwd")
+    return dq, dk, dv
+
+
+def lindecay_decode_step(q_t, k_t, v_t, log_a, states, o_t=None, stream=None):
+    """One token: q_t, k_t (B, G, d_k); v_t (B, H, d_v); states (B, H, d_k, d_v) fp32, updated
+    in place.  Returns o_t (B, H, d_v)."""
+    shape, st_shape, dt, dev = _lindecay_check(q_t, k_t, v_t, log_a, 1)
+    _expect("states", states, st_shape, torch.float32, dev)
+    if o_t is None:
+        o_t = torch.empty_like(v_t)
+    else:
+        _expect("o_t", o_t, v_t.shape, dt, dev)
+    with _Device(dev):
+        st = lib().lindecay_decode_step(ctypes.byref(shape), q_t.data_ptr(), k_t.data_ptr(), v_t.data_ptr(),
+                                        log_a.data_ptr(), o_t.data_ptr(), states.data_ptr(), _stream_ptr(stream))
+    _check(st, "lindecay_decode_step")
+    return o_t
+
+
+# ---- norms around a block ------------------------------------------------------------------
+ACTS = {"identity": 0, "silu": 1, "sigmoid": 2}
+
+
+class BlocknormGrads(NamedTuple):
+    """Gradients of blocknorm_fwd's inputs; None for those it was not given."""
+
+    dx: Optional[torch.Tensor]
+    dy: Optional[torch.Tensor]
+    dgate: Optional[torch.Tensor]
+    dw_post: Optional[torch.Tensor]
+    dscale: Optional[torch.Tensor]
+    dw_pre: Optional[torch.Tensor]
+
+
+def _blocknorm_check(first, acts, weights, group, act, eps):
+    """Checks activations (name -> tensor or None) against `first` and weights (dim) fp32."""
+    shape, dt, dev = first.shape, first.dtype, first.device
+    code = _dtype_code(dt)
+    if not shape or shape[-1] == 0 or first.numel() == 0:
+        raise ValueError(f"activations must hold at least one row, got shape {tuple(shape)}")
+    D = shape[-1]
+    for name, x in acts:
+        _expect(name, x, shape, dt, dev, True)
+    for name, x in weights:
+        _expect(name, x, (D,), torch.float32, dev, True)
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
+    return BlocknormShape(first.numel() // D, D, D if group is None else int(group), ACTS[act], eps, code), dev
+
+
+def blocknorm_fwd(y=None, w_post=None, x=None, gate=None, scale=None, w_pre=None, group=None, act="silu", eps=1e-6,
+                  x_new=None, h=None, stream=None):
+    """x' = x + scale * act(gate) * norm_group(y) * w_post and h = norm(x') * w_pre, in one
+    pass; returns (x', h).  Activations (..., D) in bf16 or fp32, weights (D,) fp32.  Without x,
+    x' is the gated norm alone; h is computed where w_pre is given (else None); without y,
+    x' is x."""
+    first = y if y is not None else x
+    if first is None:
+        raise ValueError("y or x is required")
+    shape, dev = _blocknorm_check(first, (("y", y), ("x", x), ("gate", gate), ("x_new", x_new), ("h", h)),
+                                  (("w_post", w_post), ("scale", scale), ("w_pre", w_pre)), group, act, eps)
+    if y is None and x_new is not None:
+        raise ValueError("x_new is x itself without y")
+    if y is not None and x_new is None:
+        x_new = torch.empty_like(y)
+    if h is None and w_pre is not None:
+        h = torch.empty_like(first)
+    with _Device(dev):
+        st = lib().blocknorm_fwd(ctypes.byref(shape), _ptr(x), _ptr(y), _ptr(gate), _ptr(w_post), _ptr(scale),
+                                 _ptr(w_pre), _ptr(x_new), _ptr(h), _stream_ptr(stream))
+    _check(st, "blocknorm_fwd")
+    return (x if y is None else x_new), h
+
+
+def blocknorm_bwd(dx_new, y=None, w_post=None, dh=None, x_new=None, gate=None, scale=None, w_pre=None, group=None,
+                  act="silu", eps=1e-6, residual=None, workspace=None, stream=None):
+    """Gradients of sum(dx_new * x') + sum(dh * h) of blocknorm_fwd, from its x' (x_new, with
+    dh) and its inputs; dx_new or dh may be None (zero).  dx is returned where the forward
+    had a residual input x (`residual`; by default taken from scale or x_new being given)."""
+    first = dx_new if dx_new is not None else dh
+    if first is None:
+        raise ValueError("dx_new or dh is required")
+    shape, dev = _blocknorm_check(first, (("dh", dh), ("x_new", x_new), ("y", y), ("gate", gate)),
+                                  (("w_post", w_post), ("scale", scale), ("w_pre", w_pre)), group, act, eps)
+    _expect("dx_new", dx_new, first.shape, first.dtype, dev, True)
+    if residual is None:
+        residual = y is None or scale is not None or x_new is not None
+    like = lambda t: None if t is None else torch.empty_like(t)  # noqa: E731
+    g = BlocknormGrads(torch.empty_like(first) if residual else None, like(y), like(gate), like(w_post), like(scale),
+                       like(w_pre))
+    with _Device(dev):
+        nb = int(lib().blocknorm_bwd_workspace_bytes(ctypes.byref(shape)))
+        workspace = _workspace(workspace, nb, dev, "blocknorm_bwd_workspace_bytes")
+        st = lib().blocknorm_bwd(ctypes.byref(shape), _ptr(dx_new), _ptr(dh), _ptr(x_new), _ptr(y), _ptr(gate),
+                                 _ptr(w_post), _ptr(scale), _ptr(w_pre), _ptr(g.dx), _ptr(g.dy), _ptr(g.dgate),
+                                 _ptr(g.dw_post), _ptr(g.dscale), _ptr(g.dw_pre), workspace.data_ptr(),
+                                 workspace.numel() * workspace.element_size(), _stream_ptr(stream))
+    _check(st, "blocknorm_bwd")
+    return g

@@ -77,6 +77,7 @@ cudaError_t launch_tc_gdn_local(const ll_shape& s, const void* k, const void* v,
                                 void* u, char* ws, unsigned* status, cudaStream_t st);
 cudaError_t launch_tc_gdn_pass(const ll_shape& s, int b0, int nb, const void* k, const void* v, const float* a,
                                const float* beta, void* u, char* ws, unsigned* status, cudaStream_t st);
+unsigned* device_status_word() { return status_word(); }
 void note_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 void note_launch(const FwdArgs& a, int i, cudaStream_t st) {
   note_launch();

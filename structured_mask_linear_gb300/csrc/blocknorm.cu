@@ -1,0 +1,611 @@
+// The norms around a block, fused with its gate and the residual scale, and their gradients.
+//
+// Per row (token) of D values, rms over groups of `group` values for the block's output and
+// over the whole row for the residual stream:
+//     n  = y rsqrt(mean_group(y²) + eps) w_post
+//     x' = x + scale act(gate) n
+//     h  = x' rsqrt(mean(x'²) + eps) w_pre
+// with x, gate, w_post, scale and the (w_pre, h) pair each optional.  Gradients, given dx'
+// and dh (r1, r2 the two rsqrt):
+//     u   = dh w_pre,       dx = dx' + r2 (u - x' r2² mean(u x')),   dw_pre = sum dh x' r2
+//     dm  = dx scale,       dscale = sum dx act(gate) n,             dgate = dm n act'(gate)
+//     dn  = dm act(gate),   dw_post = sum dn y r1
+//     un  = dn w_post,      dy = r1 (un - y r1² mean_group(un y))
+// All sums are fp32; values are rounded once, where they are stored.  h is the norm of x'
+// before x' is rounded; the gradients take x' as stored.
+//
+// Both directions are bound by memory: each activation is read once and written once.
+#include <cuda_runtime.h>
+
+#include "blocknorm.cuh"
+#include "ptx.cuh"
+
+namespace ll {
+
+namespace {
+
+struct F8 {
+  float v[8];
+};
+__device__ __forceinline__ F8 unpack8(const uint4& x) {
+  F8 r;
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r.v[2 * i] = __uint_as_float(w[i] << 16);
+    r.v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+  return r;
+}
+__device__ __forceinline__ F8 load8(const float* p) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  return {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+}
+__device__ __forceinline__ F8 load8(const __nv_bfloat16* p) { return unpack8(*reinterpret_cast<const uint4*>(p)); }
+__device__ __forceinline__ void store8(float* p, const F8& x) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(x.v[0], x.v[1], x.v[2], x.v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x.v[4], x.v[5], x.v[6], x.v[7]);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const F8& x) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack2(x.v[0], x.v[1]), pack2(x.v[2], x.v[3]), pack2(x.v[4], x.v[5]),
+                                            pack2(x.v[6], x.v[7]));
+}
+__device__ __forceinline__ F8 fill8(float c) { return {{c, c, c, c, c, c, c, c}}; }
+__device__ __forceinline__ F8 weight8(const float* w, int c) { return w ? load8(w + c) : fill8(1.f); }
+
+__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + __expf(-x)); }
+__device__ __forceinline__ float act_of(int act, float g) {
+  return act == BN_SILU ? g * sigmoid(g) : act == BN_SIGMOID ? sigmoid(g) : g;
+}
+// act(g) and its derivative
+__device__ __forceinline__ float2 act_grad(int act, float g) {
+  if (act == BN_IDENTITY) return make_float2(g, 1.f);
+  const float s = sigmoid(g);
+  return act == BN_SILU ? make_float2(g * s, s * (1.f + g * (1.f - s))) : make_float2(s, s * (1.f - s));
+}
+
+// Sum over the aligned groups of `width` lanes (a power of two) that hold a value each.
+__device__ __forceinline__ float lanes_sum(float x, int width) {
+  for (int o = width >> 1; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+// Sums over the tpr threads of a row (tpr a power of two >= 32, rows aligned in the CTA).
+// `red` holds K floats a warp; the caller lets a barrier pass before using it again.
+template <int K>
+__device__ __forceinline__ void row_sum(float (&x)[K], int tpr, float* red) {
+#pragma unroll
+  for (int k = 0; k < K; ++k) x[k] = lanes_sum(x[k], 32);
+  if (tpr == 32) return;
+  const int warp = threadIdx.x >> 5, n = tpr >> 5, w0 = warp & ~(n - 1);
+  if ((threadIdx.x & 31) == 0)
+#pragma unroll
+    for (int k = 0; k < K; ++k) red[warp * K + k] = x[k];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    float s = 0.f;
+    for (int w = 0; w < n; ++w) s += red[(w0 + w) * K + k];
+    x[k] = s;
+  }
+}
+
+// ---------------------------------------------------------------------------------
+// bn_fwd: D a multiple of 8, up to 512 threads a row, each with NV vectors of 8 values
+// (column (i tpr + t) 8) that stay in registers between the two norms, so nothing is read
+// twice.  Small rows share a CTA.  gl: lanes per group of y's norm, 0: the whole row.
+// ---------------------------------------------------------------------------------
+template <typename T, int NV>
+__global__ void __launch_bounds__(512) bn_fwd_kernel(const __grid_constant__ BnArgs p, int tpr, int gl) {
+  __shared__ float red1[16], red2[16];
+  const int t = threadIdx.x & (tpr - 1);
+  const long long row = (long long)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
+  const bool live = row < p.rows;
+  const size_t base = (size_t)row * p.D;
+  const T* X = static_cast<const T*>(p.x);
+  const T* Y = static_cast<const T*>(p.y);
+  const T* Gt = static_cast<const T*>(p.gate);
+  F8 x[NV], y[NV], g[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * tpr + t) * 8;
+    const bool on = live && c < p.D;
+    y[i] = on && Y ? load8(Y + base + c) : fill8(0.f);
+    x[i] = on && X ? load8(X + base + c) : fill8(0.f);
+    g[i] = on && Gt ? load8(Gt + base + c) : fill8(0.f);
+  }
+  if (Y) {
+    float ss[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      ss[i] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss[i] += y[i].v[e] * y[i].v[e];
+    }
+    if (gl) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) ss[i] = lanes_sum(ss[i], gl);
+    } else {
+      float s[1] = {0.f};
+#pragma unroll
+      for (int i = 0; i < NV; ++i) s[0] += ss[i];
+      row_sum(s, tpr, red1);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) ss[i] = s[0];
+    }
+    T* XN = static_cast<T*>(p.x_new);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * tpr + t) * 8;
+      if (!live || c >= p.D) continue;
+      const float r = rsqrtf(ss[i] * p.inv_group + p.eps);
+      const F8 w = weight8(p.w_post, c), sc = weight8(p.scale, c);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        float m = y[i].v[e] * r * w.v[e];
+        if (Gt) m *= act_of(p.act, g[i].v[e]);
+        x[i].v[e] += sc.v[e] * m;
+      }
+      store8(XN + base + c, x[i]);
+    }
+  }
+  if (!p.h) return;
+  float s[1] = {0.f};
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s[0] += x[i].v[e] * x[i].v[e];
+  row_sum(s, tpr, red2);
+  const float r = rsqrtf(s[0] * p.inv_D + p.eps);
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * tpr + t) * 8;
+    if (!live || c >= p.D) continue;
+    const F8 w = weight8(p.w_pre, c);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[i].v[e] *= r * w.v[e];
+    store8(static_cast<T*>(p.h) + base + c, x[i]);
+  }
+}
+
+// ---------------------------------------------------------------------------------
+// bn_bwd: persistent CTAs of 512 threads, one per SM, 512 / tpr rows at a time.  Rows are
+// contiguous, so a step's rows of each input are one bulk copy into a ring of stages in
+// shared memory; the reductions of one step overlap the copies of the next ones.  The
+// weights' gradients stay in registers over a CTA's rows and go out once, as one partial
+// row per row slot combined in shared memory; bn_reduce adds the CTAs' partials in order.
+// ---------------------------------------------------------------------------------
+constexpr int kBwdT = 512;
+constexpr int kBwdMaxStages = 8;
+
+template <typename T, int NV>
+__global__ void __launch_bounds__(kBwdT, 1) bn_bwd_kernel(const __grid_constant__ BnArgs p, int tpr, int gl, int stages) {
+  extern __shared__ __align__(128) uint8_t sm[];
+  __shared__ __align__(8) uint64_t full[kBwdMaxStages];
+  __shared__ float red1[3 * (kBwdT / 32)], red2[kBwdT / 32];
+  const int tid = threadIdx.x, t = tid & (tpr - 1), slot = tid / tpr, R = kBwdT / tpr;
+  const T* in[5] = {static_cast<const T*>(p.dh), static_cast<const T*>(p.x), static_cast<const T*>(p.dx_new),
+                    static_cast<const T*>(p.y), static_cast<const T*>(p.gate)};
+  const size_t arr = (size_t)R * p.D * sizeof(T);  // one array of a stage
+  int nin = 0, at[5];
+#pragma unroll
+  for (int k = 0; k < 5; ++k) at[k] = in[k] ? nin++ : 0;
+  const long long steps = (p.rows + R - 1) / R;
+  auto load = [&](long long step, int st) {
+    const long long r0 = step * R;
+    const int n = (int)(p.rows - r0 < R ? p.rows - r0 : R);
+    const uint32_t bytes = (uint32_t)(n * (size_t)p.D * sizeof(T));
+    ptx::mbar_arrive_expect_tx(&full[st], bytes * nin);
+#pragma unroll
+    for (int k = 0; k < 5; ++k)
+      if (in[k]) ptx::bulk_load(sm + ((size_t)st * nin + at[k]) * arr, in[k] + (size_t)r0 * p.D, bytes, &full[st]);
+  };
+  if (tid == 0) {
+    for (int i = 0; i < stages; ++i) ptx::mbar_init(&full[i], 1);
+    ptx::fence_mbar_init();
+    for (int i = 0; i < stages; ++i)
+      if ((long long)blockIdx.x + (long long)i * gridDim.x < steps)
+        load((long long)blockIdx.x + (long long)i * gridDim.x, i);
+  }
+  __syncthreads();
+  float apre[NV][8], apost[NV][8], ascale[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) apre[i][e] = apost[i][e] = ascale[i][e] = 0.f;
+  long long it = 0;
+  for (long long step = blockIdx.x; step < steps; step += gridDim.x, ++it) {
+    const int st = (int)(it % stages);
+    const long long row = step * R + slot;
+    const bool live = row < p.rows;
+    bool ok = bn_wait(&full[st], (uint32_t)(it / stages) & 1);
+    if (!ok) atomicExch(p.status, (unsigned)LL_ERR_TIMEOUT);
+    if (!__syncthreads_and(ok)) {
+      if (tid == 0)  // let the other copies in flight land (bounded)
+        for (int i = 0; i < stages; ++i) bn_wait(&full[i], (uint32_t)((it + (i - st + stages) % stages) / stages) & 1);
+      return;
+    }
+    const T* a = reinterpret_cast<const T*>(sm + (size_t)st * nin * arr) + (size_t)slot * p.D;
+    const size_t arre = arr / sizeof(T);
+    const T *aH = a + at[0] * arre, *aX = a + at[1] * arre, *aD = a + at[2] * arre, *aY = a + at[3] * arre,
+            *aG = a + at[4] * arre;
+    float s3[3] = {0.f, 0.f, 0.f}, sg[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * tpr + t) * 8;
+      sg[i] = 0.f;
+      if (!live || c >= p.D) continue;
+      if (in[0]) {
+        const F8 x = load8(aX + c), dh = load8(aH + c), w = weight8(p.w_pre, c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          s3[0] += x.v[e] * x.v[e];
+          s3[1] += dh.v[e] * w.v[e] * x.v[e];
+        }
+      }
+      if (in[3]) {
+        const F8 y = load8(aY + c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sg[i] += y.v[e] * y.v[e];
+        s3[2] += sg[i];
+      }
+    }
+    if (gl) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) sg[i] = lanes_sum(sg[i], gl);
+    }
+    row_sum(s3, tpr, red1);
+    const float r2 = rsqrtf(s3[0] * p.inv_D + p.eps), c2 = r2 * r2 * s3[1] * p.inv_D;
+    float se[NV], r1[NV];
+    F8 un[NV], yy[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * tpr + t) * 8;
+      se[i] = 0.f;
+      r1[i] = rsqrtf((gl ? sg[i] : s3[2]) * p.inv_group + p.eps);
+      un[i] = yy[i] = fill8(0.f);
+      if (!live || c >= p.D) continue;
+      F8 dx = in[2] ? load8(aD + c) : fill8(0.f);
+      if (in[0]) {
+        const F8 x = load8(aX + c), dh = load8(aH + c), w = weight8(p.w_pre, c);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          apre[i][e] += dh.v[e] * x.v[e] * r2;
+          dx.v[e] += r2 * (dh.v[e] * w.v[e] - x.v[e] * c2);
+        }
+      }
+      if (p.dx) store8(static_cast<T*>(p.dx) + (size_t)row * p.D + c, dx);
+      if (in[3]) {
+        const F8 w = weight8(p.w_post, c), sc = weight8(p.scale, c);
+        yy[i] = load8(aY + c);
+        F8 dg;
+        F8 g = in[4] ? load8(aG + c) : fill8(0.f);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float yn = yy[i].v[e] * r1[i], n = yn * w.v[e];
+          const float2 a = in[4] ? act_grad(p.act, g.v[e]) : make_float2(1.f, 0.f);
+          ascale[i][e] += dx.v[e] * a.x * n;
+          const float dm = dx.v[e] * sc.v[e];
+          dg.v[e] = dm * n * a.y;
+          const float dn = dm * a.x;
+          apost[i][e] += dn * yn;
+          un[i].v[e] = dn * w.v[e];
+          se[i] += un[i].v[e] * yy[i].v[e];
+        }
+        if (in[4]) store8(static_cast<T*>(p.dgate) + (size_t)row * p.D + c, dg);
+      }
+    }
+    if (gl) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) se[i] = lanes_sum(se[i], gl);
+    } else {
+      float s[1] = {0.f};
+#pragma unroll
+      for (int i = 0; i < NV; ++i) s[0] += se[i];
+      row_sum(s, tpr, red2);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) se[i] = s[0];
+    }
+    __syncthreads();  // every thread has read the stage (and red1, red2)
+    if (tid == 0 && step + (long long)stages * gridDim.x < steps) load(step + (long long)stages * gridDim.x, st);
+    if (in[3]) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * tpr + t) * 8;
+        if (!live || c >= p.D) continue;
+        const float k = r1[i] * r1[i] * se[i] * p.inv_group;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) un[i].v[e] = r1[i] * (un[i].v[e] - yy[i].v[e] * k);
+        store8(static_cast<T*>(p.dy) + (size_t)row * p.D + c, un[i]);
+      }
+    }
+  }
+  // partial sums of this CTA, the row slots combined in slot order
+  float* part = p.part + (size_t)blockIdx.x * 3 * p.D;
+  float* acc = reinterpret_cast<float*>(sm);  // 3 x D: the ring is free (every copy was waited for)
+  for (int s = 0; s < R; ++s) {
+    __syncthreads();
+    if (slot != s) continue;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * tpr + t) * 8;
+      if (c >= p.D) continue;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float a0 = s ? acc[c + e] : 0.f, a1 = s ? acc[p.D + c + e] : 0.f, a2 = s ? acc[2 * p.D + c + e] : 0.f;
+        acc[c + e] = a0 + apre[i][e];
+        acc[p.D + c + e] = a1 + apost[i][e];
+        acc[2 * p.D + c + e] = a2 + ascale[i][e];
+      }
+    }
+  }
+  __syncthreads();
+  for (int c = tid; c < 3 * p.D; c += kBwdT) part[c] = acc[c];
+}
+
+// Sums of the CTAs' partials, in order: 32 columns x 8 slices of the parts per CTA.
+__global__ void __launch_bounds__(256) bn_reduce_kernel(const __grid_constant__ BnArgs p, int nparts) {
+  __shared__ float red[8][32];
+  const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane, which = blockIdx.y;
+  float* out = which == 0 ? p.dw_pre : which == 1 ? p.dw_post : p.dscale;
+  if (!out) return;
+  const int per = (nparts + 7) / 8, p0 = sl * per, p1 = min(nparts, p0 + per);
+  float s = 0.f;
+  if (c < p.D)
+#pragma unroll 8
+    for (int i = p0; i < p1; ++i) s += p.part[((size_t)i * 3 + which) * p.D + c];
+  red[sl][lane] = s;
+  __syncthreads();
+  if (sl == 0 && c < p.D) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i) s += red[i][lane];
+    out[c] = s;
+  }
+}
+
+// ---------------------------------------------------------------------------------
+// Any D up to kBnMaxD and any group that divides it: a CTA per row, values one by one.
+// The rsqrt of each group stays in shared memory; inputs are read again for each step
+// (from L1 or L2).
+// ---------------------------------------------------------------------------------
+constexpr int kAny = 256;
+
+__device__ __forceinline__ float block_sum(float x, float* red) {
+  x = lanes_sum(x, 32);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+  __syncthreads();
+  float s = 0.f;
+#pragma unroll
+  for (int w = 0; w < kAny / 32; ++w) s += red[w];
+  return s;
+}
+// out[k] = sum over group k of f(column), for every group of the row: by the whole CTA for
+// one group, else a warp per group.
+template <typename F>
+__device__ __forceinline__ void group_sums(int D, int group, float* out, float* red, F f) {
+  const int n = D / group;
+  if (n == 1) {
+    float s = 0.f;
+    for (int c = threadIdx.x; c < D; c += kAny) s += f(c);
+    s = block_sum(s, red);
+    if (threadIdx.x == 0) out[0] = s;
+  } else {
+    for (int k = threadIdx.x >> 5; k < n; k += kAny / 32) {
+      float s = 0.f;
+      for (int c = threadIdx.x & 31; c < group; c += 32) s += f(k * group + c);
+      s = lanes_sum(s, 32);
+      if ((threadIdx.x & 31) == 0) out[k] = s;
+    }
+  }
+  __syncthreads();
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kAny) bn_fwd_any_kernel(const __grid_constant__ BnArgs p) {
+  extern __shared__ float s_grp[];
+  __shared__ float red[kAny / 32];
+  const size_t base = (size_t)blockIdx.x * p.D;
+  const T *X = static_cast<const T*>(p.x), *Y = static_cast<const T*>(p.y), *Gt = static_cast<const T*>(p.gate);
+  if (Y)
+    group_sums(p.D, p.group, s_grp, red, [&](int c) {
+      const float y = ll_load(Y, base + c);
+      return y * y;
+    });
+  auto value = [&](int c) {
+    float x = X ? ll_load(X, base + c) : 0.f;
+    if (Y) {
+      float m = ll_load(Y, base + c) * rsqrtf(s_grp[c / p.group] * p.inv_group + p.eps);
+      if (p.w_post) m *= p.w_post[c];
+      if (Gt) m *= act_of(p.act, ll_load(Gt, base + c));
+      x += p.scale ? p.scale[c] * m : m;
+    }
+    return x;
+  };
+  float s = 0.f;
+  // x' may be written over x or y only after h has been formed: the values are read again
+  for (int c = threadIdx.x; c < p.D; c += kAny) {
+    const float x = value(c);
+    s += x * x;
+  }
+  s = block_sum(s, red);
+  const float r = rsqrtf(s * p.inv_D + p.eps);
+  for (int c = threadIdx.x; c < p.D; c += kAny) {
+    const float x = value(c);
+    if (Y) ll_store(static_cast<T*>(p.x_new), base + c, x);
+    if (p.h) ll_store(static_cast<T*>(p.h), base + c, p.w_pre ? x * r * p.w_pre[c] : x * r);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kAny) bn_bwd_any_kernel(const __grid_constant__ BnArgs p) {
+  extern __shared__ float s_dyn[];
+  __shared__ float red[kAny / 32];
+  const int ng = p.D / p.group;
+  float *acc = s_dyn;                       // 3 x D weight gradients of this CTA's rows
+  float *s_y = acc + 3 * p.D, *s_e = s_y + ng;  // per group: sum y², sum un y
+  const T *H = static_cast<const T*>(p.dh), *X = static_cast<const T*>(p.x), *Dn = static_cast<const T*>(p.dx_new),
+          *Y = static_cast<const T*>(p.y), *Gt = static_cast<const T*>(p.gate);
+  for (int c = threadIdx.x; c < 3 * p.D; c += kAny) acc[c] = 0.f;
+  for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    const size_t base = (size_t)row * p.D;
+    __syncthreads();
+    float a = 0.f, b = 0.f;
+    if (H)
+      for (int c = threadIdx.x; c < p.D; c += kAny) {
+        const float x = ll_load(X, base + c), u = ll_load(H, base + c) * (p.w_pre ? p.w_pre[c] : 1.f);
+        a += x * x;
+        b += u * x;
+      }
+    a = block_sum(a, red);
+    b = block_sum(b, red);
+    const float r2 = rsqrtf(a * p.inv_D + p.eps), c2 = r2 * r2 * b * p.inv_D;
+    if (Y)
+      group_sums(p.D, p.group, s_y, red, [&](int c) {
+        const float y = ll_load(Y, base + c);
+        return y * y;
+      });
+    auto dx_of = [&](int c) {
+      float dx = Dn ? ll_load(Dn, base + c) : 0.f;
+      if (H) dx += r2 * (ll_load(H, base + c) * (p.w_pre ? p.w_pre[c] : 1.f) - ll_load(X, base + c) * c2);
+      return dx;
+    };
+    auto un_of = [&](int c) {
+      float d = dx_of(c) * (p.scale ? p.scale[c] : 1.f);
+      if (Gt) d *= act_of(p.act, ll_load(Gt, base + c));
+      return p.w_post ? d * p.w_post[c] : d;
+    };
+    if (Y) group_sums(p.D, p.group, s_e, red, [&](int c) { return un_of(c) * ll_load(Y, base + c); });
+    for (int c = threadIdx.x; c < p.D; c += kAny) {
+      const float dx = dx_of(c);
+      if (H) acc[c] += ll_load(H, base + c) * ll_load(X, base + c) * r2;
+      float dy = 0.f, dg = 0.f;
+      if (Y) {
+        const int k = c / p.group;
+        const float r1 = rsqrtf(s_y[k] * p.inv_group + p.eps), y = ll_load(Y, base + c), yn = y * r1;
+        const float n = p.w_post ? yn * p.w_post[c] : yn;
+        const float2 ac = Gt ? act_grad(p.act, ll_load(Gt, base + c)) : make_float2(1.f, 0.f);
+        const float dm = p.scale ? dx * p.scale[c] : dx;
+        acc[p.D + c] += dm * ac.x * yn;
+        acc[2 * p.D + c] += dx * ac.x * n;
+        dg = dm * n * ac.y;
+        dy = r1 * (un_of(c) - y * r1 * r1 * s_e[k] * p.inv_group);
+      }
+      if (p.dx) ll_store(static_cast<T*>(p.dx), base + c, dx);
+      if (Gt) ll_store(static_cast<T*>(p.dgate), base + c, dg);
+      if (Y) ll_store(static_cast<T*>(p.dy), base + c, dy);
+    }
+  }
+  __syncthreads();
+  float* part = p.part + (size_t)blockIdx.x * 3 * p.D;
+  for (int c = threadIdx.x; c < 3 * p.D; c += kAny) part[c] = acc[c];
+}
+
+int ceil_pow2(int x) {
+  int r = 1;
+  while (r < x) r <<= 1;
+  return r;
+}
+// Lanes per group of y's norm when groups lie inside a warp's vectors; 0: the whole row is
+// one group; -1: neither.
+int group_lanes(const BnArgs& p) {
+  if (!p.y || p.group == p.D) return 0;
+  const int n = p.group / 8;
+  return p.group % 8 == 0 && n <= 32 && (n & (n - 1)) == 0 ? n : -1;
+}
+
+template <typename T>
+cudaError_t fwd(const BnArgs& p, cudaStream_t st) {
+  const int gl = group_lanes(p), nvec = p.D / 8;
+  if (p.D % 8 || gl < 0) {
+    const int smem = p.y ? p.D / p.group * 4 : 0;
+    cudaError_t e = cudaFuncSetAttribute(bn_fwd_any_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kBnMaxGroups * 4);
+    if (e != cudaSuccess) return e;
+    bn_fwd_any_kernel<T><<<(unsigned)p.rows, kAny, smem, st>>>(p);
+    return cudaGetLastError();
+  }
+  // one vector a thread up to 512 threads a row, then two or four
+  const int nv = nvec <= 512 ? 1 : nvec <= 1024 ? 2 : 4;
+  int tpr = ceil_pow2((nvec + nv - 1) / nv);
+  tpr = tpr < 32 ? 32 : tpr;
+  const int threads = tpr < 128 ? 128 : tpr, R = threads / tpr;
+  const unsigned grid = (unsigned)((p.rows + R - 1) / R);
+  if (nv == 1) bn_fwd_kernel<T, 1><<<grid, threads, 0, st>>>(p, tpr, gl);
+  else if (nv == 2) bn_fwd_kernel<T, 2><<<grid, threads, 0, st>>>(p, tpr, gl);
+  else bn_fwd_kernel<T, 4><<<grid, threads, 0, st>>>(p, tpr, gl);
+  return cudaGetLastError();
+}
+
+constexpr int kBwdSmem = 220 * 1024;
+
+template <typename T, int NV>
+cudaError_t bwd_fast(const BnArgs& p, int tpr, int gl, int ctas, cudaStream_t st) {
+  const int nin = (p.dh ? 2 : 0) + (p.dx_new ? 1 : 0) + (p.y ? 1 : 0) + (p.gate ? 1 : 0);
+  const size_t stage = (size_t)nin * (kBwdT / tpr) * p.D * sizeof(T), acc = (size_t)3 * p.D * 4;
+  int stages = (int)(kBwdSmem / stage);
+  stages = stages > kBwdMaxStages ? kBwdMaxStages : stages;
+  const size_t smem = stage * stages > acc ? stage * stages : acc;
+  cudaError_t e = cudaFuncSetAttribute(bn_bwd_kernel<T, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
+  if (e != cudaSuccess) return e;
+  bn_bwd_kernel<T, NV><<<ctas, kBwdT, smem, st>>>(p, tpr, gl, stages);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t bwd(const BnArgs& p, cudaStream_t st) {
+  const int gl = group_lanes(p), nvec = p.D / 8;
+  const BnBwdPlan pl = bn_bwd_plan(p, sizeof(T) == 2);
+  cudaError_t e;
+  if (!pl.fast) {
+    const int smem = (3 * p.D + 2 * (p.D / p.group)) * 4;
+    e = cudaFuncSetAttribute(bn_bwd_any_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (3 * kBnMaxD + 2 * kBnMaxGroups) * 4);
+    if (e != cudaSuccess) return e;
+    bn_bwd_any_kernel<T><<<pl.ctas, kAny, smem, st>>>(p);
+    e = cudaGetLastError();
+  } else {
+    int tpr = ceil_pow2(nvec > 512 ? nvec / 2 + nvec % 2 : nvec);
+    tpr = tpr < 32 ? 32 : tpr;
+    e = nvec <= 512 ? bwd_fast<T, 1>(p, tpr, gl, pl.ctas, st) : bwd_fast<T, 2>(p, tpr, gl, pl.ctas, st);
+  }
+  if (e != cudaSuccess) return e;
+  note_launch();
+  if (p.dw_pre || p.dw_post || p.dscale) {
+    bn_reduce_kernel<<<dim3((p.D + 31) / 32, 3), 256, 0, st>>>(p, pl.ctas);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    note_launch();
+  }
+  return cudaSuccess;
+}
+
+}  // namespace
+
+// Which backward kernel runs and on how many CTAs (each leaves a partial of the weights'
+// gradients in the workspace).
+BnBwdPlan bn_bwd_plan(const BnArgs& p, bool bf16) {
+  BnBwdPlan pl;
+  const int nvec = p.D / 8, e = bf16 ? 2 : 4;
+  int tpr = ceil_pow2(nvec > 512 ? nvec / 2 + nvec % 2 : nvec);
+  tpr = tpr < 32 ? 32 : tpr;
+  // the widest rows that leave room for one step of rows of all five inputs
+  pl.fast = p.D % 8 == 0 && nvec <= 1024 && group_lanes(p) >= 0 && (long long)5 * (kBwdT / tpr) * p.D * e <= kBwdSmem;
+  const long long steps = pl.fast ? (p.rows + kBwdT / tpr - 1) / (kBwdT / tpr) : p.rows;
+  pl.ctas = (int)(steps < 152 ? steps : 152);
+  return pl;
+}
+
+cudaError_t launch_bn_fwd(const BnArgs& p, bool bf16, cudaStream_t st) {
+  const cudaError_t e = bf16 ? fwd<__nv_bfloat16>(p, st) : fwd<float>(p, st);
+  if (e == cudaSuccess) note_launch();
+  return e;
+}
+cudaError_t launch_bn_bwd(const BnArgs& p, bool bf16, cudaStream_t st) {
+  return bf16 ? bwd<__nv_bfloat16>(p, st) : bwd<float>(p, st);
+}
+
+}  // namespace ll

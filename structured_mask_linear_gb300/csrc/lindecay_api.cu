@@ -1,0 +1,249 @@
+// Entry points of the linear attention with a decay per head: argument checks, how a call
+// is split into units of work, workspace layout.  Contracts are in include/loglinear.h.
+#include <cuda_runtime.h>
+
+#include "lindecay.cuh"
+
+namespace {
+
+using ll::LinArgs;
+using ll::LinProb;
+
+constexpr int kSms = 152;  // CTAs of a persistent launch: one per SM
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+size_t a256(size_t x) { return (x + 255) & ~size_t(255); }
+
+ll_status check_shape(const ll_shape* s) {
+  if (!s) return LL_ERR_NULL;
+  if (s->dtype != LL_F32 && s->dtype != LL_BF16) return LL_ERR_DTYPE;
+  if (s->batch < 1 || s->heads < 1 || s->heads_per_group < 1 || s->heads % s->heads_per_group) return LL_ERR_SHAPE;
+  if (s->d_k < 8 || s->d_k > 128 || s->d_k % 8 || s->d_v < 8 || s->d_v > 128 || s->d_v % 8) return LL_ERR_SHAPE;
+  if ((long long)s->batch * s->heads > (1 << 20)) return LL_ERR_SHAPE;
+  return LL_OK;
+}
+ll_status check_seq_shape(const ll_shape* s) {
+  const ll_status st = check_shape(s);
+  if (st != LL_OK) return st;
+  return s->T < 1 || s->T > (1 << 30) ? LL_ERR_SHAPE : LL_OK;
+}
+
+// How many chunks a segment holds.  One segment per head needs no state pass but leaves
+// SMs idle when there are few heads; more segments cost a pass over Y and Z (kState of an
+// output chunk's time each) and two more launches (kLaunch chunks).  Estimated in units of
+// one output chunk on one SM; measured at the shapes of the comments in lindecay_tc.cu.
+int segment_chunks(const LinArgs& p, int max_chunks) {
+  constexpr double kState = 0.5, kLaunch = 8.0;
+  long long units = 0, sunits = 0, weight = 0;
+  int nh_max = 1;
+  for (int i = 0; i < p.nprob; ++i) {
+    const LinProb& r = p.pr[i];
+    const int nh = r.oh == p.H ? 1 : p.hpg;
+    units += (long long)p.B * r.oh * r.tiles;
+    weight += (long long)p.B * r.oh * r.tiles * nh;
+    sunits += (long long)p.B * p.H * r.tiles;
+    nh_max = nh > nh_max ? nh : nh_max;
+  }
+  const bool even = weight == units * nh_max;
+  double best = 0;
+  int best_l = 0;
+  for (int n = 1; n <= 256 && n <= p.NC; ++n) {
+    const int l = (p.NC + n - 1) / n, nseg = (p.NC + l - 1) / l;
+    if (l > max_chunks) continue;
+    double c = even ? (double)((units * nseg + kSms - 1) / kSms) * l * nh_max
+                    : (double)weight * p.NC / kSms + 0.5 * l * nh_max;
+    if (nseg > 1) c += (double)((sunits * (nseg - 1) + kSms - 1) / kSms) * l * kState + kLaunch;
+    if (best_l == 0 || c < best) {
+      best = c;
+      best_l = l;
+    }
+  }
+  return best_l ? best_l : max_chunks;
+}
+
+struct Plan {
+  LinArgs args;
+  size_t off_seg[ll::kLinProbs], off_scratch, bytes;
+};
+
+// Completes a plan whose scans' head counts, widths and directions are set.
+void finish_plan(const ll_shape* s, Plan* pl, size_t off) {
+  LinArgs& p = pl->args;
+  const bool bf16 = s->dtype == LL_BF16;
+  p.B = s->batch;
+  p.T = s->T;
+  p.H = s->heads;
+  p.hpg = s->heads_per_group;
+  p.chunk = bf16 ? ll::kLinChunk : ll::kLinChunk32;
+  p.NC = (s->T + p.chunk - 1) / p.chunk;
+  bool grouped = false;
+  for (int i = 0; i < p.nprob; ++i) {
+    p.pr[i].tiles = (p.pr[i].b + ll::kLinTile - 1) / ll::kLinTile;
+    grouped = grouped || p.pr[i].oh != p.H;
+  }
+  // A group's heads are summed in a buffer of one segment per CTA: 16 chunks of 32 KB on
+  // 152 CTAs stay in the 126 MB L2.
+  p.L = segment_chunks(p, bf16 && grouped ? 16 : p.NC);
+  p.nseg = (p.NC + p.L - 1) / p.L;
+  p.units = p.sunits = 0;
+  for (int i = 0; i < p.nprob; ++i) {
+    LinProb& r = p.pr[i];
+    r.unit0 = p.units;
+    r.sunit0 = p.sunits;
+    p.units += p.B * r.oh * r.tiles * p.nseg;
+    p.sunits += p.B * p.H * r.tiles * (p.nseg - 1);
+    pl->off_seg[i] = off;
+    if (p.nseg > 1) off += a256((size_t)p.B * p.H * r.tiles * p.nseg * r.a * ll::kLinTile * 4);
+  }
+  pl->off_scratch = off;
+  if (bf16 && grouped) off += a256((size_t)kSms * p.L * ll::kLinChunk * ll::kLinTile * 4);
+  pl->bytes = off;
+}
+
+LinProb scan(const void* X, int xh, const void* Y, int yh, const void* Z, int zh, void* out, int oh, int a, int b,
+             int rev) {
+  LinProb r{};
+  r.X = X;
+  r.Y = Y;
+  r.Z = Z;
+  r.out = out;
+  r.xh = xh;
+  r.yh = yh;
+  r.zh = zh;
+  r.oh = oh;
+  r.a = a;
+  r.b = b;
+  r.rev = rev;
+  return r;
+}
+
+void plan_fwd(const ll_shape* s, const void* q, const void* k, const void* v, void* o, Plan* pl) {
+  const int H = s->heads, G = H / s->heads_per_group;
+  pl->args = LinArgs{};
+  pl->args.nprob = 1;
+  pl->args.pr[0] = scan(q, G, k, G, v, H, o, H, s->d_k, s->d_v, 0);
+  finish_plan(s, pl, 0);
+}
+
+// The gradients' three scans, in one launch, or in two on the tensor cores where d_k and
+// d_v are padded to different widths (the kernel's).
+int plan_bwd(const ll_shape* s, const void* q, const void* k, const void* v, const void* dO, void* dq, void* dk,
+             void* dv, Plan* pl) {
+  const int H = s->heads, G = H / s->heads_per_group;
+  const bool split = s->dtype == LL_BF16 && ll::lin_is_wide(s->d_k) != ll::lin_is_wide(s->d_v);
+  const LinProb pq = scan(dO, H, v, H, k, G, dq, G, s->d_v, s->d_k, 0);
+  const LinProb pk = scan(v, H, dO, H, q, G, dk, G, s->d_v, s->d_k, 1);
+  const LinProb pv = scan(k, G, q, G, dO, H, dv, H, s->d_k, s->d_v, 1);
+  pl[0].args = LinArgs{};
+  pl[0].args.pr[0] = pq;
+  pl[0].args.pr[1] = pk;
+  pl[0].args.nprob = split ? 2 : 3;
+  if (!split) pl[0].args.pr[2] = pv;
+  finish_plan(s, &pl[0], 0);
+  if (!split) return 1;
+  pl[1].args = LinArgs{};
+  pl[1].args.pr[0] = pv;
+  pl[1].args.nprob = 1;
+  finish_plan(s, &pl[1], 0);  // the launches run one after the other and share the workspace
+  return 2;
+}
+
+ll_status run(const ll_shape* s, Plan* pl, const float* log_a, const int* lengths, void* workspace, void* stream) {
+  LinArgs& p = pl->args;
+  p.log_a = log_a;
+  p.lengths = lengths;
+  p.status = ll::device_status_word();
+  if (!p.status) return LL_ERR_CUDA;
+  char* ws = static_cast<char*>(workspace);
+  for (int i = 0; i < p.nprob; ++i) p.pr[i].seg = p.nseg > 1 ? reinterpret_cast<float*>(ws + pl->off_seg[i]) : nullptr;
+  p.scratch = reinterpret_cast<float*>(ws + pl->off_scratch);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = s->dtype == LL_BF16 ? ll::launch_lin_tc(p, kSms, st) : ll::launch_lin_f32(p, st);
+  return e == cudaSuccess ? LL_OK : LL_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t lindecay_fwd_workspace_bytes(const ll_shape* s) {
+  if (check_seq_shape(s) != LL_OK) return 0;
+  Plan pl;
+  plan_fwd(s, nullptr, nullptr, nullptr, nullptr, &pl);
+  return pl.bytes + 256;
+}
+
+ll_status lindecay_fwd(const ll_shape* s, const void* q, const void* k, const void* v, const float* log_a,
+                       const int* lengths, const float* state_in, void* o, float* state_out, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  const ll_status st = check_seq_shape(s);
+  if (st != LL_OK) return st;
+  if (!q || !k || !v || !log_a || !o) return LL_ERR_NULL;
+  for (const void* x : {q, k, v, (const void*)o, (const void*)state_in, (const void*)state_out})
+    if (!aligned16(x)) return LL_ERR_ALIGN;
+  Plan pl;
+  plan_fwd(s, q, k, v, o, &pl);
+  if (!workspace || workspace_bytes < pl.bytes) return LL_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return LL_ERR_ALIGN;
+  LinProb& r = pl.args.pr[0];
+  r.init = state_in;
+  r.init_rs = s->d_v;
+  r.init_cs = 1;
+  r.fin = state_out;
+  return run(s, &pl, log_a, lengths, workspace, stream);
+}
+
+size_t lindecay_bwd_workspace_bytes(const ll_shape* s) {
+  if (check_seq_shape(s) != LL_OK) return 0;
+  Plan pl[2];
+  const int n = plan_bwd(s, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, pl);
+  size_t b = pl[0].bytes;
+  if (n == 2 && pl[1].bytes > b) b = pl[1].bytes;
+  return b + 256;
+}
+
+ll_status lindecay_bwd(const ll_shape* s, const void* q, const void* k, const void* v, const float* log_a,
+                       const int* lengths, const float* state_in, const void* dO, const float* dstate_out, void* dq,
+                       void* dk, void* dv, float* dstate_in, void* workspace, size_t workspace_bytes, void* stream) {
+  ll_status st = check_seq_shape(s);
+  if (st != LL_OK) return st;
+  if (!q || !k || !v || !log_a || !dO || !dq || !dk || !dv) return LL_ERR_NULL;
+  for (const void* x : {q, k, v, dO, (const void*)dq, (const void*)dk, (const void*)dv, (const void*)state_in,
+                        (const void*)dstate_out, (const void*)dstate_in})
+    if (!aligned16(x)) return LL_ERR_ALIGN;
+  // the scans run side by side: one may still read the states that another's end writes
+  if (dstate_in && (dstate_in == state_in || dstate_in == dstate_out)) return LL_ERR_SHAPE;
+  Plan pl[2];
+  const int n = plan_bwd(s, q, k, v, dO, dq, dk, dv, pl);
+  size_t need = pl[0].bytes;
+  if (n == 2 && pl[1].bytes > need) need = pl[1].bytes;
+  if (!workspace || workspace_bytes < need) return LL_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return LL_ERR_ALIGN;
+  LinProb& pq = pl[0].args.pr[0];
+  LinProb& pk = pl[0].args.pr[1];
+  LinProb& pv = n == 2 ? pl[1].args.pr[0] : pl[0].args.pr[2];
+  pq.init = state_in;
+  pk.init = pv.init = dstate_out;
+  pq.init_rs = pk.init_rs = 1;  // dq and dk run over the transposed states
+  pq.init_cs = pk.init_cs = s->d_v;
+  pv.init_rs = s->d_v;
+  pv.init_cs = 1;
+  pv.fin = dstate_in;
+  for (int i = 0; i < n; ++i)
+    if ((st = run(s, &pl[i], log_a, lengths, workspace, stream)) != LL_OK) return st;
+  return LL_OK;
+}
+
+ll_status lindecay_decode_step(const ll_shape* s, const void* q_t, const void* k_t, const void* v_t,
+                               const float* log_a, void* o_t, float* states, void* stream) {
+  const ll_status st = check_shape(s);
+  if (st != LL_OK) return st;
+  if (!q_t || !k_t || !v_t || !log_a || !o_t || !states) return LL_ERR_NULL;
+  for (const void* x : {q_t, k_t, v_t, (const void*)o_t, (const void*)states})
+    if (!aligned16(x)) return LL_ERR_ALIGN;
+  const ll::LinStepArgs d{s->batch, s->heads, s->heads_per_group, s->d_k, s->d_v, q_t, k_t, v_t, log_a, o_t, states};
+  const cudaError_t e = ll::launch_lin_step(d, s->dtype == LL_BF16, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? LL_OK : LL_ERR_CUDA;
+}
+
+}  // extern "C"

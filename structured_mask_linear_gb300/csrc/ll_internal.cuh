@@ -58,6 +58,8 @@ struct FwdArgs {
 // Counts a kernel launch and records the profiling event that follows kernel `i`.
 void note_launch(const FwdArgs& a, int i, cudaStream_t st);
 void note_launch();
+// Address of the current device's status word (NULL: a CUDA call failed).
+unsigned* device_status_word();
 
 
 cudaError_t launch_generic_fwd(const GenPlan& p, bool bf16, const FwdArgs& a, cudaStream_t st);
