@@ -11,23 +11,25 @@ namespace {
 // ---------------------------------------------------------------------------------
 // lin_scan: segment totals -> the state at each segment's start, in place, in scan order:
 // prefix_{s+1} = g^(tokens of s) prefix_s + total_s, prefix_0 = the start state or 0.  One
-// thread per float4 of a (head, column tile); nseg loads of a thread are independent of
-// the running sum, so they are issued four at a time.
+// thread per float4 of a (head, column tile); its loads do not depend on the running sum
+// and are issued eight at a time, a batch ahead.
 // ---------------------------------------------------------------------------------
 __global__ void __launch_bounds__(256) lin_scan_kernel(const __grid_constant__ LinArgs p) {
   const LinProb& r = p.pr[blockIdx.y];
   const int n4 = r.a * (kLinTile / 4);
-  const long long total = (long long)p.B * p.H * r.tiles * n4;
   const long long e = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (e >= total) return;
-  const int q = (int)(e % n4);
-  const int tile = (int)(e / n4 % r.tiles);
-  const int bh = (int)(e / n4 / r.tiles);
-  const int b = bh / p.H, h = bh % p.H;
+  if (e >= (long long)r.nsplit * r.nh * n4) return;
+  const int q = (int)(e % n4), uh = (int)(e / n4);
+  LinItem x;
+  x.prob = blockIdx.y;
+  x.unit = r.split0 + uh / r.nh;
+  x.seg = 0;
+  lin_locate(p, x);
+  const int tile = x.tile, b = x.b, h = x.oh * r.nh + uh % r.nh, bh = b * p.H + h;
   const int row = q / (kLinTile / 4), c = q % (kLinTile / 4) * 4;
   const int len = lin_len(p, b), span = p.L * p.chunk;
   const float l2 = lin_log2_decay(p.log_a, h);
-  float4* s4 = reinterpret_cast<float4*>(r.seg) + (size_t)(e / n4) * p.nseg * n4 + q;
+  float4* s4 = reinterpret_cast<float4*>(r.seg) + (size_t)uh * p.nseg * n4 + q;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   if (r.init && kLinTile * tile + c < r.b) {  // b is a multiple of 8: whole float4s
     const float* in =
@@ -35,24 +37,29 @@ __global__ void __launch_bounds__(256) lin_scan_kernel(const __grid_constant__ L
     acc = make_float4(in[0], in[r.init_cs], in[2 * (size_t)r.init_cs], in[3 * (size_t)r.init_cs]);
   }
   const int last = p.nseg - 1;
-  for (int i0 = 0; i0 < p.nseg; i0 += 4) {
-    float4 x[4];
+  constexpr int kBatch = 8;
+  float4 now[kBatch], next[kBatch];
+  auto fetch = [&](int i0, float4(&to)[kBatch]) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (i0 + k < last) x[k] = s4[(size_t)(r.rev ? last - i0 - k : i0 + k) * n4];
+    for (int k = 0; k < kBatch; ++k)
+      if (i0 + k < last) to[k] = s4[(size_t)(r.rev ? last - i0 - k : i0 + k) * n4];
+  };
+  fetch(0, now);
+  for (int i0 = 0; i0 <= last; i0 += kBatch) {
+    fetch(i0 + kBatch, next);
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < kBatch; ++k) {
       const int i = i0 + k;
-      if (i > last) break;
-      const int s = r.rev ? last - i : i;
-      s4[(size_t)s * n4] = acc;
-      if (i == last) break;
-      const int tok = max(0, min(len - s * span, span));
-      const float d = exp2f(l2 * (float)tok);
-      acc.x = d * acc.x + x[k].x;
-      acc.y = d * acc.y + x[k].y;
-      acc.z = d * acc.z + x[k].z;
-      acc.w = d * acc.w + x[k].w;
+      if (i <= last) {
+        const int s = r.rev ? last - i : i;
+        s4[(size_t)s * n4] = acc;
+        const float d = exp2f(l2 * (float)max(0, min(len - s * span, span)));
+        acc.x = d * acc.x + now[k].x;
+        acc.y = d * acc.y + now[k].y;
+        acc.z = d * acc.z + now[k].z;
+        acc.w = d * acc.w + now[k].w;
+      }
+      now[k] = next[k];
     }
   }
 }
@@ -80,32 +87,33 @@ __global__ void __launch_bounds__(kF, 1) lin_f32_kernel(const __grid_constant__ 
   extern __shared__ float4 smem4[];
   F32Smem& sm = *reinterpret_cast<F32Smem*>(smem4);
   const int tid = threadIdx.x;
-  const LinUnit x = kStateOnly ? lin_state_unit(p, (int)blockIdx.x) : lin_unit(p, (int)blockIdx.x);
+  int head0 = 0;
+  const LinItem x =
+      kStateOnly ? lin_state_item(p, (int)blockIdx.x, &head0) : lin_item(p, (int)blockIdx.x);
   const LinProb& r = p.pr[x.prob];
-  const bool rev = r.rev != 0;
+  const bool rev = r.rev != 0, split = lin_is_split(p, x);
   const int sh = rev ? 0 : 1;
-  const int nh = (kStateOnly || r.oh == p.H) ? 1 : p.hpg;
   const int a = r.a, b = r.b, c0 = kLinTile * x.tile, nc = min(kLinTile, b - c0);
   const int ldx = a + 4;
   const int len = lin_len(p, x.b);
-  const int lo = x.seg * p.L, hi = min(min(lo + p.L, p.NC), (len + kC32 - 1) / kC32);
+  const int lo = x.lo, hi = min(x.hi, (len + kC32 - 1) / kC32);
   const int n = max(0, hi - lo);
   const float* Xg = static_cast<const float*>(r.X);
   const float* Yg = static_cast<const float*>(r.Y);
   const float* Zg = static_cast<const float*>(r.Z);
   float* out = static_cast<float*>(r.out);
-  for (int hi_h = 0; hi_h < nh; ++hi_h) {
-    const int h = x.oh * nh + hi_h, g = h / p.hpg;
+  for (int hi_h = head0; hi_h < (kStateOnly ? head0 + 1 : r.nh); ++hi_h) {
+    const int h = x.oh * r.nh + hi_h, g = h / p.hpg;
     const int hx = r.xh == p.H ? h : g, hy = r.yh == p.H ? h : g, hz = r.zh == p.H ? h : g;
     const size_t bh = (size_t)x.b * p.H + h;
     const float l2 = lin_log2_decay(p.log_a, h);
-    float* seg = r.seg ? r.seg + ((bh * r.tiles + x.tile) * p.nseg + x.seg) * (size_t)a * kLinTile : nullptr;
+    float* seg = split ? lin_seg(p, x, hi_h) : nullptr;
     __syncthreads();
     for (int e = tid; e < a * kLinTile; e += kF) {
       const int i = e / kLinTile, j = e % kLinTile;
       float v = 0.f;
       if (!kStateOnly) {
-        if (p.nseg > 1) v = seg[e];
+        if (split) v = seg[e];
         else if (r.init && j < nc) v = r.init[bh * a * b + (size_t)i * r.init_rs + (size_t)(c0 + j) * r.init_cs];
       }
       sm.R[i * kLd + j] = v;
@@ -203,15 +211,15 @@ __global__ void __launch_bounds__(kF, 1) lin_f32_kernel(const __grid_constant__ 
     __syncthreads();
     if (kStateOnly) {
       for (int e = tid; e < a * kLinTile; e += kF) seg[e] = sm.R[e / kLinTile * kLd + e % kLinTile];
-    } else if (r.fin && x.seg == (rev ? 0 : p.nseg - 1)) {
+    } else if (r.fin && lin_is_last(p, x)) {
       for (int e = tid; e < a * nc; e += kF)
         r.fin[(bh * a + e / nc) * b + c0 + e % nc] = sm.R[e / nc * kLd + e % nc];
     }
   }
   if (!kStateOnly) {  // chunks past the row's length: zeros
-    const int t1 = min(p.T, min((x.seg + 1) * p.L, p.NC) * kC32);
+    const int t1 = min(p.T, x.hi * kC32);
     const int n4 = nc / 4;
-    for (int e = tid; ; e += kF) {
+    for (int e = tid;; e += kF) {
       const int t = (lo + n) * kC32 + e / n4;
       if (t >= t1) break;
       *reinterpret_cast<float4*>(out + (((size_t)x.b * p.T + t) * r.oh + x.oh) * b + c0 + e % n4 * 4) =
@@ -309,7 +317,7 @@ __global__ void __launch_bounds__(kStepT) lin_step_kernel(LinStepArgs d) {
 cudaError_t launch_lin_scan(const LinArgs& p, cudaStream_t st) {
   long long most = 0;
   for (int i = 0; i < p.nprob; ++i) {
-    const long long n = (long long)p.B * p.H * p.pr[i].tiles * p.pr[i].a * (kLinTile / 4);
+    const long long n = (long long)p.pr[i].nsplit * p.pr[i].nh * p.pr[i].a * (kLinTile / 4);
     most = n > most ? n : most;
   }
   lin_scan_kernel<<<dim3((unsigned)((most + 255) / 256), p.nprob), 256, 0, st>>>(p);
@@ -325,7 +333,7 @@ cudaError_t launch_lin_f32(LinArgs& p, cudaStream_t st) {
     if ((e = cudaFuncSetAttribute(lin_f32_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) !=
         cudaSuccess)
       return e;
-    lin_f32_kernel<true><<<p.sunits, kF, smem, st>>>(p);
+    lin_f32_kernel<true><<<p.sitems, kF, smem, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     note_launch();
     if ((e = launch_lin_scan(p, st)) != cudaSuccess) return e;
@@ -333,7 +341,7 @@ cudaError_t launch_lin_f32(LinArgs& p, cudaStream_t st) {
   if ((e = cudaFuncSetAttribute(lin_f32_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) !=
       cudaSuccess)
     return e;
-  lin_f32_kernel<false><<<p.units, kF, smem, st>>>(p);
+  lin_f32_kernel<false><<<p.items, kF, smem, st>>>(p);
   if ((e = cudaGetLastError()) == cudaSuccess) note_launch();
   return e;
 }

@@ -39,21 +39,29 @@ struct LinProb {
   const float* init;         // NULL (zero), or start states: element (i, j) of head bh at
   int init_rs, init_cs;      // init[bh * a * b + i * init_rs + j * init_cs]
   float* fin;                // NULL, or end states (B*H, a, b)
-  float* seg;                // (B*H, tiles, nseg, a, 64) segment totals, then start states
   int tiles;                 // ceil(b / 64)
-  int unit0, sunit0;         // first unit of this scan in the output and the state pass
+  int nh;                    // heads summed into one output head (1 or hpg)
+  int unit0;                 // units of the scans before this one
+  int split0, nsplit;        // first unit (of this scan) that is cut into segments, their number
+  int sunit0;                // work items of the state pass before this scan's
+  float* seg;                // (nsplit, nh, nseg, a, 64): segment totals, then start states
 };
 
+// A unit is the 64 output columns of a tile, for one output head and batch row, over the
+// whole sequence.  The first `nwhole` units (over all scans) are one work item each; the
+// others are cut into nseg segments of L chunks, whose start states a pass over Y and Z
+// and a prefix over the segments provide.
 struct LinArgs {
   int B, T, H, hpg;
-  int chunk;        // tokens per chunk
-  int NC;           // chunks over T
-  int nseg, L;      // segments per head, chunks per segment
+  int chunk;            // tokens per chunk
+  int NC;               // chunks over T
+  int nseg, L;
+  int nwhole, items, sitems;  // work items of the output and of the state pass
+  int sub;              // grouped outputs: chunks that one head runs before the next one does
   int nprob;
-  int units, sunits;
   const float* log_a;   // (H)
   const int* lengths;   // NULL or (B)
-  float* scratch;       // per CTA: sums over a group's heads, L * 128 * 64 fp32
+  float* scratch;       // grouped outputs, per CTA: sub * 128 * 64 sums, hpg * 128 * 64 states
   unsigned* status;
   LinProb pr[kLinProbs];
 };
@@ -72,38 +80,56 @@ __device__ __forceinline__ int lin_len(const LinArgs& p, int b) {
   return n < 0 ? 0 : n > p.T ? p.T : n;
 }
 
-// A unit of work: columns 64 tile .. of out head oh of batch row b over one segment.
-struct LinUnit {
-  int prob, b, oh, tile, seg;
+// A work item: columns 64 tile .. of out head oh of batch row b over chunks [lo, hi).
+struct LinItem {
+  int prob, unit, b, oh, tile;
+  int seg, lo, hi;
 };
-__device__ __forceinline__ LinUnit lin_unit(const LinArgs& p, int u) {
-  LinUnit x;
+__device__ __forceinline__ void lin_locate(const LinArgs& p, LinItem& x) {
+  const LinProb& r = p.pr[x.prob];
+  x.tile = x.unit % r.tiles;
+  x.oh = x.unit / r.tiles % r.oh;
+  x.b = x.unit / r.tiles / r.oh;
+  x.lo = x.seg * p.L;
+  x.hi = min(x.lo + p.L, p.NC);
+}
+__device__ __forceinline__ LinItem lin_item(const LinArgs& p, int u) {
+  LinItem x;
+  const bool whole = u < p.nwhole;
+  x.seg = whole ? 0 : (u - p.nwhole) % p.nseg;
+  if (!whole) u = p.nwhole + (u - p.nwhole) / p.nseg;
   x.prob = 0;
   while (x.prob + 1 < p.nprob && u >= p.pr[x.prob + 1].unit0) ++x.prob;
-  const LinProb& r = p.pr[x.prob];
-  u -= r.unit0;
-  x.seg = u % p.nseg;
-  u /= p.nseg;
-  x.tile = u % r.tiles;
-  u /= r.tiles;
-  x.oh = u % r.oh;
-  x.b = u / r.oh;
+  x.unit = u - p.pr[x.prob].unit0;
+  lin_locate(p, x);
+  if (whole) x.hi = p.NC;
   return x;
 }
-// The state pass runs over single heads and every segment but the scan's last.
-__device__ __forceinline__ LinUnit lin_state_unit(const LinArgs& p, int u) {
-  LinUnit x;
+// An item of the state pass: one head `hi` of a unit, one segment (all but the scan's last).
+__device__ __forceinline__ LinItem lin_state_item(const LinArgs& p, int u, int* head) {
+  LinItem x;
   x.prob = 0;
   while (x.prob + 1 < p.nprob && u >= p.pr[x.prob + 1].sunit0) ++x.prob;
   const LinProb& r = p.pr[x.prob];
   u -= r.sunit0;
   x.seg = u % (p.nseg - 1) + (r.rev ? 1 : 0);
   u /= p.nseg - 1;
-  x.tile = u % r.tiles;
-  u /= r.tiles;
-  x.oh = u % p.H;
-  x.b = u / p.H;
+  *head = u % r.nh;
+  x.unit = r.split0 + u / r.nh;
+  lin_locate(p, x);
   return x;
+}
+// Where head `hi` (of the output's group) of a unit keeps its segment's state.
+__device__ __forceinline__ float* lin_seg(const LinArgs& p, const LinItem& x, int hi) {
+  const LinProb& r = p.pr[x.prob];
+  return r.seg + (((size_t)(x.unit - r.split0) * r.nh + hi) * p.nseg + x.seg) * r.a * kLinTile;
+}
+__device__ __forceinline__ bool lin_is_split(const LinArgs& p, const LinItem& x) {
+  return x.unit >= p.pr[x.prob].split0;
+}
+// Whether the item reaches the scan's end (and so leaves the end state).
+__device__ __forceinline__ bool lin_is_last(const LinArgs& p, const LinItem& x) {
+  return p.pr[x.prob].rev ? x.lo == 0 : x.hi == p.NC;
 }
 
 bool lin_is_wide(int a);  // the tensor-core kernels pad a to 64 or 128

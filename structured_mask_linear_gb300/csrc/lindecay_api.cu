@@ -28,46 +28,62 @@ ll_status check_seq_shape(const ll_shape* s) {
   return s->T < 1 || s->T > (1 << 30) ? LL_ERR_SHAPE : LL_OK;
 }
 
-// How many chunks a segment holds.  One segment per head needs no state pass but leaves
-// SMs idle when there are few heads; more segments cost a pass over Y and Z (kState of an
-// output chunk's time each) and two more launches (kLaunch chunks).  Estimated in units of
-// one output chunk on one SM; measured at the shapes of the comments in lindecay_tc.cu.
-int segment_chunks(const LinArgs& p, int max_chunks) {
-  constexpr double kState = 0.5, kLaunch = 8.0;
-  long long units = 0, sunits = 0, weight = 0;
-  int nh_max = 1;
-  for (int i = 0; i < p.nprob; ++i) {
-    const LinProb& r = p.pr[i];
-    const int nh = r.oh == p.H ? 1 : p.hpg;
-    units += (long long)p.B * r.oh * r.tiles;
-    weight += (long long)p.B * r.oh * r.tiles * nh;
-    sunits += (long long)p.B * p.H * r.tiles;
-    nh_max = nh > nh_max ? nh : nh_max;
-  }
-  const bool even = weight == units * nh_max;
-  double best = 0;
-  int best_l = 0;
-  for (int n = 1; n <= 256 && n <= p.NC; ++n) {
-    const int l = (p.NC + n - 1) / n, nseg = (p.NC + l - 1) / l;
-    if (l > max_chunks) continue;
-    double c = even ? (double)((units * nseg + kSms - 1) / kSms) * l * nh_max
-                    : (double)weight * p.NC / kSms + 0.5 * l * nh_max;
-    if (nseg > 1) c += (double)((sunits * (nseg - 1) + kSms - 1) / kSms) * l * kState + kLaunch;
-    if (best_l == 0 || c < best) {
-      best = c;
-      best_l = l;
-    }
-  }
-  return best_l ? best_l : max_chunks;
-}
-
 struct Plan {
   LinArgs args;
   size_t off_seg[ll::kLinProbs], off_scratch, bytes;
 };
 
+// How the units become work items.  Persistent CTAs take whole units in turn, one per SM;
+// the units of the last, incomplete turn (all of them when there are fewer units than SMs)
+// may be cut into segments, which costs them a pass over Y and Z first (kState of an
+// output chunk's time per chunk), two more launches (kLaunch chunks), a start per item
+// (kItem) and the prefix over the segments (kSeg each).  The cut with the least estimated
+// time wins, no cut included; in units of one output chunk on one SM, about 2 us.
+void cut_units(LinArgs& p) {
+  constexpr double kState = 0.6, kLaunch = 4.0, kItem = 1.0, kSeg = 0.1;
+  int units = 0, nh_tail = 1;
+  for (int i = 0; i < p.nprob; ++i) {
+    p.pr[i].unit0 = units;
+    units += p.B * p.pr[i].oh * p.pr[i].tiles;
+  }
+  const int whole = units / kSms * kSms, rest = units - whole;
+  for (int i = 0; i < p.nprob; ++i)
+    if (p.pr[i].unit0 + p.B * p.pr[i].oh * p.pr[i].tiles > whole && p.pr[i].nh > nh_tail) nh_tail = p.pr[i].nh;
+  p.nwhole = units;
+  p.nseg = 1;
+  p.L = p.NC;
+  if (rest > 0) {
+    double best = (double)p.NC * nh_tail;
+    for (int n = 2; n <= 256 && n <= p.NC; ++n) {
+      const int l = (p.NC + n - 1) / n, nseg = (p.NC + l - 1) / l;
+      const long long items = (long long)rest * nseg, sitems = (long long)rest * nh_tail * (nseg - 1);
+      const double c = (double)((items + kSms - 1) / kSms) * (l * nh_tail + kItem) +
+                       (double)((sitems + kSms - 1) / kSms) * (l * kState + kItem) + kLaunch + kSeg * nseg;
+      if (c < best) {
+        best = c;
+        p.nwhole = whole;
+        p.nseg = nseg;
+        p.L = l;
+      }
+    }
+  }
+  p.items = p.nwhole + (units - p.nwhole) * p.nseg;
+  p.sitems = 0;
+  for (int i = 0; i < p.nprob; ++i) {
+    LinProb& r = p.pr[i];
+    const int n = p.B * r.oh * r.tiles, w = p.nwhole - r.unit0;
+    r.split0 = w < 0 ? 0 : w > n ? n : w;
+    r.nsplit = n - r.split0;
+    r.sunit0 = p.sitems;
+    p.sitems += r.nsplit * r.nh * (p.nseg - 1);
+  }
+}
+
 // Completes a plan whose scans' head counts, widths and directions are set.
-void finish_plan(const ll_shape* s, Plan* pl, size_t off) {
+void finish_plan(const ll_shape* s, Plan* pl) {
+  // A group's heads take turns of 16 chunks, so that their fp32 sums (16 x 32 KB a CTA, 80
+  // MB on 152 SMs) stay in the 126 MB L2.
+  constexpr int kSub = 16;
   LinArgs& p = pl->args;
   const bool bf16 = s->dtype == LL_BF16;
   p.B = s->batch;
@@ -76,27 +92,22 @@ void finish_plan(const ll_shape* s, Plan* pl, size_t off) {
   p.hpg = s->heads_per_group;
   p.chunk = bf16 ? ll::kLinChunk : ll::kLinChunk32;
   p.NC = (s->T + p.chunk - 1) / p.chunk;
+  p.sub = kSub < p.NC ? kSub : p.NC;
   bool grouped = false;
   for (int i = 0; i < p.nprob; ++i) {
     p.pr[i].tiles = (p.pr[i].b + ll::kLinTile - 1) / ll::kLinTile;
-    grouped = grouped || p.pr[i].oh != p.H;
+    p.pr[i].nh = p.pr[i].oh == p.H ? 1 : p.hpg;
+    grouped = grouped || p.pr[i].nh > 1;
   }
-  // A group's heads are summed in a buffer of one segment per CTA: 16 chunks of 32 KB on
-  // 152 CTAs stay in the 126 MB L2.
-  p.L = segment_chunks(p, bf16 && grouped ? 16 : p.NC);
-  p.nseg = (p.NC + p.L - 1) / p.L;
-  p.units = p.sunits = 0;
+  cut_units(p);
+  size_t off = 0;
   for (int i = 0; i < p.nprob; ++i) {
-    LinProb& r = p.pr[i];
-    r.unit0 = p.units;
-    r.sunit0 = p.sunits;
-    p.units += p.B * r.oh * r.tiles * p.nseg;
-    p.sunits += p.B * p.H * r.tiles * (p.nseg - 1);
+    const LinProb& r = p.pr[i];
     pl->off_seg[i] = off;
-    if (p.nseg > 1) off += a256((size_t)p.B * p.H * r.tiles * p.nseg * r.a * ll::kLinTile * 4);
+    off += a256((size_t)r.nsplit * r.nh * p.nseg * r.a * ll::kLinTile * 4);
   }
   pl->off_scratch = off;
-  if (bf16 && grouped) off += a256((size_t)kSms * p.L * ll::kLinChunk * ll::kLinTile * 4);
+  if (bf16 && grouped) off += a256((size_t)kSms * (p.sub + p.hpg) * ll::kLinChunk * ll::kLinTile * 4);
   pl->bytes = off;
 }
 
@@ -122,7 +133,7 @@ void plan_fwd(const ll_shape* s, const void* q, const void* k, const void* v, vo
   pl->args = LinArgs{};
   pl->args.nprob = 1;
   pl->args.pr[0] = scan(q, G, k, G, v, H, o, H, s->d_k, s->d_v, 0);
-  finish_plan(s, pl, 0);
+  finish_plan(s, pl);
 }
 
 // The gradients' three scans, in one launch, or in two on the tensor cores where d_k and
@@ -139,12 +150,12 @@ int plan_bwd(const ll_shape* s, const void* q, const void* k, const void* v, con
   pl[0].args.pr[1] = pk;
   pl[0].args.nprob = split ? 2 : 3;
   if (!split) pl[0].args.pr[2] = pv;
-  finish_plan(s, &pl[0], 0);
+  finish_plan(s, &pl[0]);
   if (!split) return 1;
   pl[1].args = LinArgs{};
   pl[1].args.pr[0] = pv;
   pl[1].args.nprob = 1;
-  finish_plan(s, &pl[1], 0);  // the launches run one after the other and share the workspace
+  finish_plan(s, &pl[1]);  // the launches run one after the other and share the workspace
   return 2;
 }
 
@@ -155,7 +166,7 @@ ll_status run(const ll_shape* s, Plan* pl, const float* log_a, const int* length
   p.status = ll::device_status_word();
   if (!p.status) return LL_ERR_CUDA;
   char* ws = static_cast<char*>(workspace);
-  for (int i = 0; i < p.nprob; ++i) p.pr[i].seg = p.nseg > 1 ? reinterpret_cast<float*>(ws + pl->off_seg[i]) : nullptr;
+  for (int i = 0; i < p.nprob; ++i) p.pr[i].seg = reinterpret_cast<float*>(ws + pl->off_seg[i]);
   p.scratch = reinterpret_cast<float*>(ws + pl->off_scratch);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = s->dtype == LL_BF16 ? ll::launch_lin_tc(p, kSms, st) : ll::launch_lin_f32(p, st);

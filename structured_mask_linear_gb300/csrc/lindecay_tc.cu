@@ -20,12 +20,16 @@
 // significant bits, relative error below 2^-17): the states are fp32 outputs, and an error
 // made in one chunk stays in them.  R itself is carried in fp32.
 //
-// Warp roles (512 threads, 16 warps; 128 registers a thread):
-//   warp 0      one thread issues the TMA loads, kStages chunks ahead
-//   warp 1      one thread issues the MMAs, S one chunk ahead of the rest
-//   warps 4-7   P: reads S, writes P over it in tensor memory (bf16, row t in lane t)
-//   warps 8-11  state: w Z hi / lo, R's update, R's bf16 image for the next Ob
-//   warps 12-15 output: Oa, Ob -> out, staged and stored by TMA
+// Warp roles (640 threads, five warpgroups; each keeps to one part of the chain, so that the
+// parts of consecutive chunks overlap):
+//   warps 0-3   P: reads S, writes P over it in tensor memory (bf16, row t in lane t)
+//   warps 4-7   state: R's update from D, R's bf16 image for Ob
+//   warps 8-11  output: Oa, Ob -> out, staged and stored by TMA
+//   warps 12-15 w Z: the high and low parts, in two halves of 64 tokens
+//   warp 16     TMA loads, kStages chunks ahead
+//   warp 17     the MMAs of S, one chunk ahead of
+//   warp 18     the MMAs of D, Ob and Oa
+// The launch gives 96 registers a thread; the last two groups hand 32 each to the others.
 // Every mbarrier wait is bounded (wait_bar); one that runs out records LL_ERR_TIMEOUT and
 // ends its role, the others follow by their own limits.
 #include "lindecay.cuh"
@@ -35,7 +39,7 @@ namespace ll {
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr int kC = kLinChunk;
 constexpr int kZBytes = kC * kLinTile * 2;  // 16 KB: 128 tokens x 64 columns, bf16
 constexpr int kMisc = 1024;
@@ -58,41 +62,60 @@ struct LinMaps {
 };
 
 // Tensor-memory columns: S of even and odd chunks (P over their first 64, Oa in the last
-// 64), Ob of even and odd chunks, D.
+// 64), Ob of even and odd chunks, D (its high and low part side by side).
 constexpr uint32_t kColS = 0, kColOb = 256, kColD = 384;
 
-// The chunks a CTA works on, in order; every role walks the same sequence.
+// The chunks a CTA works on, in runs of one head each; every role walks the same sequence.
+// An item whose heads are summed is cut into blocks of p.sub chunks, the heads taking turns
+// block by block; otherwise the item is one run.
 struct Walk {
   const LinArgs& p;
   bool state_only;
-  int u;             // unit
-  LinUnit x;
-  int nh, hi;        // heads of the unit, current one
-  int lo, hi_c, n;   // valid chunks [lo, hi_c) of the segment, their number
+  int u;             // item
+  LinItem x;
+  int nh, hi;        // heads of the item (first and current one)
+  int h0;
+  int lo, n;         // first valid chunk, number of valid chunks
   int len;           // valid tokens of the batch row
-  int k;             // index of the current chunk in scan order
+  int k0, k, k1;     // the run's chunks in scan order: k0 .. k1 - 1, k the current one
+  int c0, dc;        // chunk k is c0 + dc k
+  bool rev;
   __device__ __forceinline__ Walk(const LinArgs& a, bool s) : p(a), state_only(s), u((int)blockIdx.x) { enter(); }
-  __device__ __forceinline__ int total() const { return state_only ? p.sunits : p.units; }
-  __device__ __forceinline__ bool live() const { return u < total(); }
+  __device__ __forceinline__ bool live() const { return u < (state_only ? p.sitems : p.items); }
+  __device__ __forceinline__ const LinProb& prob() const { return p.pr[x.prob]; }
   __device__ __forceinline__ void enter() {
     if (!live()) return;
-    x = state_only ? lin_state_unit(p, u) : lin_unit(p, u);
-    const LinProb& r = p.pr[x.prob];
-    nh = (state_only || r.oh == p.H) ? 1 : p.hpg;
-    hi = 0;
+    h0 = 0;
+    x = state_only ? lin_state_item(p, u, &h0) : lin_item(p, u);
+    nh = state_only ? 1 : prob().nh;
+    hi = h0;
     len = lin_len(p, x.b);
-    lo = x.seg * p.L;
-    hi_c = min(min(lo + p.L, p.NC), (len + kC - 1) / kC);
-    n = max(0, hi_c - lo);
-    k = 0;
+    lo = x.lo;
+    n = max(0, min(x.hi, (len + kC - 1) / kC) - lo);
+    rev = prob().rev != 0;
+    c0 = rev ? lo + n - 1 : lo;
+    dc = rev ? -1 : 1;
+    block(0);
   }
-  __device__ __forceinline__ int head() const { return x.oh * nh + hi; }
-  __device__ __forceinline__ int chunk() const { return p.pr[x.prob].rev ? hi_c - 1 - k : lo + k; }
+  __device__ __forceinline__ void block(int first) {
+    k0 = k = first;
+    k1 = nh > 1 ? min(n, first + p.sub) : n;
+  }
+  __device__ __forceinline__ int head() const { return x.oh * prob().nh + hi; }
+  __device__ __forceinline__ int chunk() const { return c0 + dc * k; }
   __device__ __forceinline__ int valid() const { return min(kC, len - chunk() * kC); }
-  // one (unit, head) at a time: the chunks of a run are k = 0 .. n - 1
+  __device__ __forceinline__ bool first_head() const { return hi == h0; }
+  __device__ __forceinline__ bool last_head() const { return hi == h0 + nh - 1; }
+  __device__ __forceinline__ bool first_block() const { return k0 == 0; }
+  __device__ __forceinline__ bool last_block() const { return k1 == n; }
   __device__ __forceinline__ void next_run() {
-    k = 0;
-    if (++hi == nh) {
+    if (!last_head()) {
+      ++hi;
+      k = k0;
+    } else if (!last_block()) {
+      hi = h0;
+      block(k1);
+    } else {
       u += (int)gridDim.x;
       enter();
     }
@@ -101,11 +124,16 @@ struct Walk {
 
 // Per-CTA barriers (in shared memory)
 struct Bars {
-  uint64_t full[3], empty[3], s_full[2], p_ready[2], o_full[2], o_empty[2], z_ready, r_ready, d_full, fin;
+  uint64_t xy_full[3], xy_empty[3], z_full[3], z_empty[3], s_full[2], p_ready[2], o_full[2], o_empty[2], z_ready[2], z_free[2], r_ready, q_full,
+      d_full, d_free, fin[2];
   uint32_t tmem;
 };
 
+// A bounded wait; %globaltimer is slow to read, so only waits that last come to it.
 __device__ __forceinline__ bool lin_wait(uint64_t* bar, uint32_t parity, const LinArgs& p) {
+#pragma unroll 1
+  for (int i = 0; i < 1024; ++i)
+    if (__builtin_expect(ptx::mbar_try_wait(bar, parity), 1)) return true;
   if (wait_bar(bar, parity)) return true;
   atomicExch(p.status, kStatusTimeout);
   return false;
@@ -115,35 +143,47 @@ __device__ __forceinline__ bool lin_wait_warp(uint64_t* bar, uint32_t parity, co
   return __all_sync(0xffffffffu, lin_wait(bar, parity, p));
 }
 
-template <int KA, bool kStateOnly>
+__device__ __forceinline__ bool lin_failed(const LinArgs& p) {
+  return __any_sync(0xffffffffu, *reinterpret_cast<volatile unsigned*>(p.status) == kStatusTimeout);
+}
+
+template <int KA, bool kStateOnly, bool kGrouped>
 __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_constant__ LinMaps maps,
                                                              const __grid_constant__ LinArgs p) {
   using S = Lay<KA>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Bars& bars = *reinterpret_cast<Bars*>(smem + S::kMiscOff);
-  float* s_cf = reinterpret_cast<float*>(smem + S::kMiscOff + 256);  // 32
-  float* s_dt = s_cf + 32;                                           // 64
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  float* s_cf = reinterpret_cast<float*>(smem + S::kMiscOff + 512);  // 32
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform to the compiler too
+  const int row = tid & 127, quad = warp & 3;
+  const uint32_t loff = (uint32_t)(quad * 32) << 16;  // tensor-memory lanes of this warp
 
-  if (tid == 0) {
+  if (tid == 512) {
     for (int i = 0; i < 3; ++i) {
-      ptx::mbar_init(&bars.full[i], 1);
-      ptx::mbar_init(&bars.empty[i], 1);
+      ptx::mbar_init(&bars.xy_full[i], 1);
+      ptx::mbar_init(&bars.xy_empty[i], kStateOnly ? 1 : 2);
+      ptx::mbar_init(&bars.z_full[i], 1);
+      ptx::mbar_init(&bars.z_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(&bars.s_full[i], 1);
       ptx::mbar_init(&bars.p_ready[i], 128);
       ptx::mbar_init(&bars.o_full[i], 1);
       ptx::mbar_init(&bars.o_empty[i], 128);
+      ptx::mbar_init(&bars.z_ready[i], 128);
+      ptx::mbar_init(&bars.z_free[i], 1);
     }
-    ptx::mbar_init(&bars.z_ready, 128);
     ptx::mbar_init(&bars.r_ready, 128);
+    ptx::mbar_init(&bars.q_full, 1);
     ptx::mbar_init(&bars.d_full, 1);
-    ptx::mbar_init(&bars.fin, 1);
+    ptx::mbar_init(&bars.d_free, 128);
+    ptx::mbar_init(&bars.fin[0], 1);
+    ptx::mbar_init(&bars.fin[1], 1);
     ptx::fence_mbar_init();
   }
-  if (warp == 1) {
+  if (warp == 18) {
     ptx::tmem_alloc(&bars.tmem, 512);
     ptx::tmem_relinquish();
   }
@@ -152,121 +192,182 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
   ptx::tc_fence_after();
   const uint32_t tb = bars.tmem;
 
-  if (tid == 0) {
+  const int group = warp >> 2;
+  if (group == 4) {
+    ptx::regs_dec<64>();
+  if (warp == 16) {
     // ---- loads --------------------------------------------------------------------------
     uint32_t it = 0;
     bool ok = true;
     for (Walk w(p, kStateOnly); ok && w.live(); w.next_run()) {
-      const LinProb& r = p.pr[w.x.prob];
+      const LinProb& r = w.prob();
       const CUtensorMap* m = maps.m[w.x.prob];
       const int h = w.head(), g = h / p.hpg;
       const int hx = r.xh == p.H ? h : g, hy = r.yh == p.H ? h : g, hz = r.zh == p.H ? h : g;
-      for (; w.k < w.n; ++w.k, ++it) {
-        const uint32_t s = it % S::kStages;
-        if (it >= (uint32_t)S::kStages && !lin_wait(&bars.empty[s], ((it / S::kStages) & 1) ^ 1, p)) {
-          ok = false;
-          break;
-        }
+      for (; w.k < w.k1; ++w.k, ++it) {
+        const uint32_t s = it % S::kStages, par = ((it / S::kStages) & 1) ^ 1;
+        const bool again = it >= (uint32_t)S::kStages;
         uint8_t* st = smem + s * S::kStage;
         const int t0 = w.chunk() * kC;
-        ptx::mbar_arrive_expect_tx(&bars.full[s], kStateOnly ? S::kX + kZBytes : S::kStage);
+        ok = !again || lin_wait_warp(&bars.xy_empty[s], par, p);
+        if (!ok) break;
+        if (ptx::elect_one()) {
+          ptx::mbar_arrive_expect_tx(&bars.xy_full[s], kStateOnly ? S::kX : 2 * S::kX);
 #pragma unroll
-        for (int c = 0; c < KA / 64; ++c) {
-          if (!kStateOnly) ptx::tma_load_4d(st + c * 16384, &m[0], &bars.full[s], 64 * c, hx, t0, w.x.b);
-          ptx::tma_load_4d(st + S::kX + c * 16384, &m[1], &bars.full[s], 64 * c, hy, t0, w.x.b);
+          for (int c = 0; c < KA / 64; ++c) {
+            ptx::tma_load_4d(st + S::kX + c * 16384, &m[1], &bars.xy_full[s], 64 * c, hy, t0, w.x.b);
+            if (!kStateOnly) ptx::tma_load_4d(st + c * 16384, &m[0], &bars.xy_full[s], 64 * c, hx, t0, w.x.b);
+          }
         }
-        ptx::tma_load_4d(st + 2 * S::kX, &m[2], &bars.full[s], kLinTile * w.x.tile, hz, t0, w.x.b);
+        ok = !again || lin_wait_warp(&bars.z_empty[s], par, p);
+        if (!ok) {  // X and Y of this chunk are on their way
+          wait_bar(&bars.xy_full[s], par ^ 1);
+          break;
+        }
+        if (ptx::elect_one()) {
+          ptx::mbar_arrive_expect_tx(&bars.z_full[s], kZBytes);
+          ptx::tma_load_4d(st + 2 * S::kX, &m[2], &bars.z_full[s], kLinTile * w.x.tile, hz, t0, w.x.b);
+        }
       }
     }
     if (!ok)  // let the copies in flight land before the CTA ends (bounded)
-      for (uint32_t j = it >= (uint32_t)S::kStages ? it - S::kStages : 0; j < it; ++j)
-        wait_bar(&bars.full[j % S::kStages], (j / S::kStages) & 1);
-  } else if (tid == 32) {
-    // ---- MMAs ---------------------------------------------------------------------------
-    uint32_t n = 0;  // chunks of this CTA
-    for (Walk w(p, kStateOnly); w.live(); w.next_run()) n += w.n;
-    const uint32_t s0 = ptx::smem_u32(smem);
-    const uint32_t img = s0 + S::kImg, zt = s0 + S::kZt;
-    auto issue_s = [&](uint32_t it) -> bool {
-      const uint32_t st = it % S::kStages, bf = it & 1;
-      if (!lin_wait(&bars.full[st], (it / S::kStages) & 1, p)) return false;
-      if (it >= 2 && !lin_wait(&bars.o_empty[bf], ((it >> 1) & 1) ^ 1, p)) return false;
-      ptx::tc_fence_after();
-      const uint32_t x0 = s0 + st * S::kStage, y0 = x0 + S::kX;
-      const uint32_t idesc = ptx::idesc_bf16_f32(128, 128, 0, 0);
-#pragma unroll
-      for (int kk = 0; kk < KA / 16; ++kk) {
-        const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-        ptx::umma_f16(tb + kColS + 128 * bf, ptx::smem_desc_sw128(x0 + off, 16, 1024),
-                      ptx::smem_desc_sw128(y0 + off, 16, 1024), idesc, kk > 0);
+      for (uint32_t j = it >= (uint32_t)S::kStages ? it - S::kStages : 0; j < it; ++j) {
+        wait_bar(&bars.xy_full[j % S::kStages], (j / S::kStages) & 1);
+        wait_bar(&bars.z_full[j % S::kStages], (j / S::kStages) & 1);
       }
-      ptx::umma_commit(&bars.s_full[bf]);
-      return true;
-    };
-    bool ok = kStateOnly || n == 0 || issue_s(0);
-    for (uint32_t it = 0; ok && it < n; ++it) {
-      const uint32_t st = it % S::kStages, bf = it & 1, par = it & 1;
-      const uint32_t x0 = s0 + st * S::kStage, y0 = x0 + S::kX, z0 = x0 + 2 * S::kX;
-      if (!kStateOnly) {
-        if (it + 1 < n && !issue_s(it + 1)) break;
-        if (!lin_wait(&bars.r_ready, par, p)) break;
-        ptx::tc_fence_after();
-        const uint32_t idesc = ptx::idesc_bf16_f32(128, 64, 0, 1);
+  } else if (!kStateOnly && warp == 17) {
+    // ---- MMAs of S: the whole warp walks, one lane issues --------------------------------------
+    uint32_t n = 0;  // chunks of this CTA
+    for (Walk w(p, false); w.live(); w.next_run()) n += w.k1 - w.k0;
+    // descriptors at the start of shared memory; their low 14 bits count 16-byte units, so
+    // an offset is added there (addresses stay below 2^18)
+    const uint64_t kmaj = ptx::smem_desc_sw128(ptx::smem_u32(smem), 16, 1024);
+    for (uint32_t it = 0; it < n; ++it) {
+      const uint32_t st = it % S::kStages, bf = it & 1;
+      if (it >= 2 && !lin_wait_warp(&bars.o_empty[bf], ((it >> 1) & 1) ^ 1, p)) break;
+      if (!lin_wait_warp(&bars.xy_full[st], (it / S::kStages) & 1, p)) break;
+      ptx::tc_fence_after();
+      if (ptx::elect_one()) {
+        const uint32_t idesc = ptx::idesc_bf16_f32(128, 128, 0, 0);
+        const uint64_t dx = kmaj + ((st * S::kStage) >> 4), dy = dx + (S::kX >> 4);
 #pragma unroll
         for (int kk = 0; kk < KA / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * 16384 + (kk & 3) * 32;
-          ptx::umma_f16(tb + kColOb + 64 * bf, ptx::smem_desc_sw128(x0 + off, 16, 1024),
-                        ptx::smem_desc_sw128(img + kk * 2048, 1024, 1024), idesc, kk > 0);
+          const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+          ptx::umma_f16(tb + kColS + 128 * bf, dx + off, dy + off, idesc, kk > 0);
         }
+        ptx::umma_commit(&bars.s_full[bf]);
+        ptx::umma_commit(&bars.xy_empty[st]);
       }
-      if (!lin_wait(&bars.z_ready, par, p)) break;
-      ptx::tc_fence_after();
-      // D: A = Yᵀ (M = 128, both MN-major).  With a padded to 64 the second 64 rows of A
-      // read Z's tile that follows Y (LBO 16 KB): lanes 64..127 of D are never read.
-      const uint32_t idesc_d = ptx::idesc_bf16_f32(128, 64, 1, 1);
-#pragma unroll
-      for (int part = 0; part < 2; ++part)
-#pragma unroll
-        for (int kk = 0; kk < kC / 16; ++kk)
-          ptx::umma_f16(tb + kColD, ptx::smem_desc_sw128(y0 + kk * 2048, 16384, 1024),
-                        ptx::smem_desc_sw128(zt + part * kZBytes + kk * 2048, 1024, 1024), idesc_d, part + kk > 0);
-      ptx::umma_commit(&bars.d_full);
-      if (!kStateOnly) {
-        if (!lin_wait(&bars.p_ready[bf], (it >> 1) & 1, p)) break;
-        ptx::tc_fence_after();
-        const uint32_t idesc = ptx::idesc_bf16_f32(128, 64, 0, 1);
-        const uint32_t tp = tb + kColS + 128 * bf;
-#pragma unroll
-        for (int kk = 0; kk < kC / 16; ++kk)
-          ptx::umma_f16_tmem_a(tp + 64, tp + kk * 8, ptx::smem_desc_sw128(z0 + kk * 2048, 1024, 1024), idesc, kk > 0);
-        ptx::umma_commit(&bars.o_full[bf]);
-      }
-      ptx::umma_commit(&bars.empty[st]);
+      __syncwarp();
     }
-  } else if (!kStateOnly && warp >= 4 && warp < 8) {
+    if (lin_failed(p)) {  // the MMAs issued may still run: give them a bounded wait
+      if (ptx::elect_one()) ptx::umma_commit(&bars.fin[0]);
+      wait_bar(&bars.fin[0], 0);
+    }
+  } else if (warp == 18) {
+    // ---- MMAs of D, Ob, Oa ------------------------------------------------------------------
+    uint32_t n = 0;
+    for (Walk w(p, kStateOnly); w.live(); w.next_run()) n += w.k1 - w.k0;
+    const uint32_t s0 = ptx::smem_u32(smem);
+    const uint64_t kmaj = ptx::smem_desc_sw128(s0, 16, 1024);       // X of Ob
+    const uint64_t zmaj = ptx::smem_desc_sw128(s0, 1024, 1024);     // Z and R's image, N = 64
+    const uint64_t amaj = ptx::smem_desc_sw128(s0, 16384, 1024);    // Yᵀ and [Zhi | Zlo] of D
+    static_assert(kZBytes == 16384, "one LBO for both operands of D");
+    const uint32_t idesc = ptx::idesc_bf16_f32(128, 64, 0, 1);
+    auto issue_oa = [&](uint32_t it) -> bool {
+      const uint32_t st = it % S::kStages, bf = it & 1;
+      if (!lin_wait_warp(&bars.p_ready[bf], (it >> 1) & 1, p)) return false;
+      ptx::tc_fence_after();
+      if (ptx::elect_one()) {
+        const uint32_t zo = (st * S::kStage + 2 * S::kX) >> 4, tp = tb + kColS + 128 * bf;
+#pragma unroll
+        for (int kk = 0; kk < kC / 16; ++kk)
+          ptx::umma_f16_tmem_a(tp + 64, tp + kk * 8, zmaj + zo + kk * 128, idesc, kk > 0);
+        ptx::umma_commit(&bars.o_full[bf]);
+        ptx::umma_commit(&bars.z_empty[st]);
+      }
+      __syncwarp();
+      return true;
+    };
+    bool ok = true;
+    for (uint32_t it = 0; ok && it < n; ++it) {
+      const uint32_t st = it % S::kStages, bf = it & 1, par = it & 1;
+      const uint32_t xo = (st * S::kStage) >> 4, yo = xo + (S::kX >> 4);
+      // D = Yᵀ [Zhi | Zlo], by halves of 64 tokens: A is MN-major with M = 128 (with a padded
+      // to 64 its second 64 rows read Z's tile that follows Y, LBO 16 KB: lanes 64..127 of D
+      // are never read), B two 64-wide atoms 16 KB apart.
+      if (!lin_wait_warp(&bars.xy_full[st], (it / S::kStages) & 1, p)) break;
+      if (it > 0 && !lin_wait_warp(&bars.d_free, par ^ 1, p)) break;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        ok = ok && lin_wait_warp(&bars.z_ready[half], par, p);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        if (ptx::elect_one()) {
+          const uint32_t idesc_d = ptx::idesc_bf16_f32(128, 128, 1, 1);
+#pragma unroll
+          for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+            ptx::umma_f16(tb + kColD, amaj + yo + kk * 128, amaj + (S::kZt >> 4) + kk * 128, idesc_d, kk > 0);
+          ptx::umma_commit(&bars.z_free[half]);
+          if (half == 1) {
+            ptx::umma_commit(&bars.d_full);
+            if (kStateOnly) {
+              ptx::umma_commit(&bars.xy_empty[st]);
+              ptx::umma_commit(&bars.z_empty[st]);
+            }
+          }
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      if (!kStateOnly) {
+        // Ob's columns have been read two chunks ago
+        if (it >= 2 && !lin_wait_warp(&bars.o_empty[bf], ((it >> 1) & 1) ^ 1, p)) break;
+        if (!lin_wait_warp(&bars.r_ready, par, p)) break;
+        ptx::tc_fence_after();
+        if (ptx::elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < KA / 16; ++kk) {
+            const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+            ptx::umma_f16(tb + kColOb + 64 * bf, kmaj + xo + off, zmaj + (S::kImg >> 4) + kk * 128, idesc, kk > 0);
+          }
+          ptx::umma_commit(&bars.q_full);
+          ptx::umma_commit(&bars.xy_empty[st]);
+        }
+        __syncwarp();
+        ok = issue_oa(it);
+      }
+    }
+    if (lin_failed(p)) {
+      if (ptx::elect_one()) ptx::umma_commit(&bars.fin[1]);
+      wait_bar(&bars.fin[1], 0);
+    }
+  }
+  } else if (group == 0) {
+    ptx::regs_inc<104>();
+    if (!kStateOnly) {
     // ---- P ------------------------------------------------------------------------------
-    const int quad = warp - 4;
-    const uint32_t loff = (uint32_t)(quad * 32) << 16;
     uint32_t it = 0;
     bool ok = true;
     for (Walk w(p, false); ok && w.live(); w.next_run()) {
-      if (w.n == 0) continue;
-      const bool rev = p.pr[w.x.prob].rev != 0;
+      if (w.k0 == w.k1) continue;
+      const bool rev = w.rev;
       const float l2 = lin_log2_decay(p.log_a, w.head());
-      // g^(j - i) tables over 32 keys: off the diagonal 32-group g^|i-j| is the product of a
-      // factor of the row and group (to the group's nearest key) and one of the key, both
-      // <= 1; on it the power of the lag itself, 0 where the lag is negative.
-      ptx::named_bar_sync(1, 128);
-      if (quad == 0) {
-        s_cf[lane] = exp2f(l2 * (float)(rev ? lane : 31 - lane));
-      } else if (quad < 3) {
-        const int x = (quad - 1) * 32 + lane;  // key - row + 31
-        const int d = rev ? x - 31 : 31 - x;
-        s_dt[x] = d < 0 ? 0.f : exp2f(l2 * (float)d);
+      // Weights g^|i-j| of row i = 32 quad + lane.  Against its own 32-group of keys: in
+      // registers, 0 where the lag is negative.  Against a group behind it in scan order:
+      // the product of a factor of the row and group (up to the group's nearest key) and one
+      // of the key (from there, s_cf), both <= 1.
+      float2 wd[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const int d0 = rev ? 2 * j - lane : lane - 2 * j, d1 = rev ? d0 + 1 : d0 - 1;
+        wd[j] = make_float2(d0 < 0 ? 0.f : exp2f(l2 * (float)d0), d1 < 0 ? 0.f : exp2f(l2 * (float)d1));
       }
       ptx::named_bar_sync(1, 128);
-      const float* dt = s_dt + 31 - lane;
-      for (; w.k < w.n; ++w.k, ++it) {
+      if (quad == 0) s_cf[lane] = exp2f(l2 * (float)(rev ? lane : 31 - lane));
+      ptx::named_bar_sync(1, 128);
+      const float g32 = exp2f(l2 * 32.f), near = exp2f(l2 * (float)(rev ? 32 - lane : lane + 1));
+      for (; w.k < w.k1; ++w.k, ++it) {
         const uint32_t bf = it & 1;
         const int nv = w.valid();
         if (!lin_wait_warp(&bars.s_full[bf], (it >> 1) & 1, p)) {
@@ -275,59 +376,59 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         }
         ptx::tc_fence_after();
         const uint32_t ts = tb + kColS + 128 * bf + loff;
+        // Group cg's packed columns 16 cg .. 16 cg + 15 lie over S of groups cg / 2 and, for
+        // cg = 0, over the first half of its own: groups are done in ascending order, each
+        // read before it is written.
 #pragma unroll 1
         for (int cg = 0; cg < 4; ++cg) {
+          float2 sv[16];
           uint32_t pk[16];
-          if (cg == quad || (cg < quad) != rev) {
-            float sv[32];
-            ptx::tmem_ld32(ts + cg * 32, sv);
-            if (cg == quad) {
+          const int back = rev ? cg - quad : quad - cg;  // 32-groups behind the row's own
+          if (back >= 0) {
+            ptx::tmem_ld32(ts + 32 * cg, reinterpret_cast<float*>(sv));
+            if (back == 0) {
               ptx::tmem_ld_wait();
 #pragma unroll
-              for (int j = 0; j < 32; ++j) {
-                const float f = dt[j];
-                sv[j] = f != 0.f ? sv[j] * f : 0.f;
-              }
+              for (int j = 0; j < 16; ++j) sv[j] = ptx::mul2(sv[j], wd[j]);
             } else {
-              const float rf = exp2f(l2 * (float)(rev ? 32 * (cg - quad) - lane : 32 * (quad - cg) + lane - 31));
+              float f = near;
+              for (int i = 1; i < back; ++i) f *= g32;
               const float4* c4 = reinterpret_cast<const float4*>(s_cf);
               ptx::tmem_ld_wait();
 #pragma unroll
-              for (int j4 = 0; j4 < 8; ++j4) {
-                const float4 c = c4[j4];
-                sv[4 * j4] *= rf * c.x;
-                sv[4 * j4 + 1] *= rf * c.y;
-                sv[4 * j4 + 2] *= rf * c.z;
-                sv[4 * j4 + 3] *= rf * c.w;
+              for (int j = 0; j < 8; ++j) {
+                const float4 c = c4[j];
+                sv[2 * j] = ptx::mul2(sv[2 * j], ptx::mul2(make_float2(f, f), make_float2(c.x, c.y)));
+                sv[2 * j + 1] = ptx::mul2(sv[2 * j + 1], ptx::mul2(make_float2(f, f), make_float2(c.z, c.w)));
               }
             }
-            if (rev && nv < 32 * cg + 32) {  // keys past the row's length (warp-uniform)
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (32 * cg + j >= nv) sv[j] = 0.f;
+            for (int j = 0; j < 16; ++j) pk[j] = pack_bf16(sv[j].x, sv[j].y);
+            if (nv < 32 * cg + 32) {  // keys past the row's length (warp-uniform): P = 0
+              const int keep = nv - 32 * cg;
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                pk[j] = 2 * j + 1 < keep ? pk[j] : 2 * j < keep ? pk[j] & 0xffffu : 0u;
             }
-#pragma unroll
-            for (int j = 0; j < 16; ++j) pk[j] = pack_bf16(sv[2 * j], sv[2 * j + 1]);
           } else {
 #pragma unroll
             for (int j = 0; j < 16; ++j) pk[j] = 0u;
           }
-          // packed columns 16 cg ..: they held S of keys below 32 cg, all read before
-          ptx::tmem_st16(ts + cg * 16, pk);
+          ptx::tmem_st16(ts + 16 * cg, pk);
         }
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
         ptx::mbar_arrive(&bars.p_ready[bf]);
       }
     }
-  } else if (warp >= 8 && warp < 12) {
-    // ---- state --------------------------------------------------------------------------
-    // Thread r of the role: token r of the chunk for w Z, row r of R.
-    const int row = tid - 256, quad = warp - 8, rot = row & 7;
-    const uint32_t td = tb + kColD + ((uint32_t)(quad * 32) << 16);
-    uint8_t* zhi = smem + S::kZt + row * 128;
+    }
+  } else if (group == 1) {
+    ptx::regs_inc<128>();
+    // ---- state: thread `row` holds row `row` of R ------------------------------------------
+    const uint32_t td = tb + kColD + loff;
+    const int rot = row & 7;
     uint8_t* img = smem + S::kImg + row * 128;
-    const bool holds = row < KA;  // warp-uniform: this thread has a row of R
+    const bool holds = row < KA;  // warp-uniform
     uint32_t it = 0;
     bool ok = true;
     float R[kLinTile];
@@ -343,25 +444,34 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
       ptx::mbar_arrive(&bars.r_ready);
     };
     for (Walk w(p, kStateOnly); ok && w.live(); w.next_run()) {
-      const LinProb& r = p.pr[w.x.prob];
-      const bool rev = r.rev != 0;
+      const LinProb& r = w.prob();
       const int h = w.head();
       const size_t bh = (size_t)w.x.b * p.H + h;
       const int c0 = kLinTile * w.x.tile;
       const int nc = min(kLinTile, r.b - c0);  // columns of this tile, a multiple of 8
       const float l2 = lin_log2_decay(p.log_a, h);
-      float* seg = r.seg ? r.seg + (((bh * r.tiles + w.x.tile) * p.nseg + w.x.seg) * r.a + row) * kLinTile : nullptr;
+      // the states of the heads that wait for their turn, 16 float4s a row
+      float4* keep = reinterpret_cast<float4*>(p.scratch) +
+                     ((size_t)blockIdx.x * (p.sub + p.hpg) + p.sub + w.hi) * (kC * kLinTile / 4) + row;
 #pragma unroll
       for (int j = 0; j < kLinTile; ++j) R[j] = 0.f;
       if (!kStateOnly && row < r.a) {
-        if (p.nseg > 1) {
+        const float4* from = nullptr;
+        int step = 1;
+        if (!w.first_block()) {
+          from = keep;
+          step = kC;
+        } else if (lin_is_split(p, w.x)) {
+          from = reinterpret_cast<const float4*>(lin_seg(p, w.x, w.hi) + (size_t)row * kLinTile);
+        }
+        if (from) {
 #pragma unroll
-          for (int j = 0; j < kLinTile; j += 4) {
-            const float4 x = *reinterpret_cast<const float4*>(seg + j);
-            R[j] = x.x;
-            R[j + 1] = x.y;
-            R[j + 2] = x.z;
-            R[j + 3] = x.w;
+          for (int j = 0; j < kLinTile / 4; ++j) {
+            const float4 x = from[j * step];
+            R[4 * j] = x.x;
+            R[4 * j + 1] = x.y;
+            R[4 * j + 2] = x.z;
+            R[4 * j + 3] = x.w;
           }
         } else if (r.init) {
           const float* in = r.init + bh * r.a * r.b + (size_t)row * r.init_rs + (size_t)c0 * r.init_cs;
@@ -370,76 +480,49 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
             if (j < nc) R[j] = in[(size_t)j * r.init_cs];
         }
       }
-      if (!kStateOnly && w.n > 0) write_image();
-      for (; w.k < w.n; ++w.k, ++it) {
-        const uint32_t s = it % S::kStages;
-        const int nv = w.valid();
-        uint8_t* y0 = smem + s * S::kStage + S::kX + row * 128;
-        uint8_t* z0 = smem + s * S::kStage + 2 * S::kX + row * 128;
-        if (!lin_wait_warp(&bars.full[s], (it / S::kStages) & 1, p)) {
-          ok = false;
-          break;
-        }
-        if (row < nv) {
-          const float wt = exp2f(l2 * (float)(rev ? row + 1 : nv - 1 - row));
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            const int off = (c ^ rot) << 4;
-            uint4 x = *reinterpret_cast<const uint4*>(z0 + off), y;
-            __nv_bfloat162* hx = reinterpret_cast<__nv_bfloat162*>(&x);
-            __nv_bfloat162* hy = reinterpret_cast<__nv_bfloat162*>(&y);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float2 f = __bfloat1622float2(hx[e]);
-              f.x *= wt;
-              f.y *= wt;
-              hx[e] = __floats2bfloat162_rn(f.x, f.y);
-              const float2 rr = __bfloat1622float2(hx[e]);
-              hy[e] = __floats2bfloat162_rn(f.x - rr.x, f.y - rr.y);
-            }
-            *reinterpret_cast<uint4*>(zhi + off) = x;
-            *reinterpret_cast<uint4*>(zhi + kZBytes + off) = y;
+      for (; w.k < w.k1; ++w.k, ++it) {
+        if (!kStateOnly) {
+          if (it > 0 && !lin_wait_warp(&bars.q_full, (it & 1) ^ 1, p)) {  // the image is free
+            ok = false;
+            break;
           }
-        } else {
-          // past the row's length: whatever the padding holds must not reach a product
-          const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            *reinterpret_cast<uint4*>(zhi + (c << 4)) = zero;
-            *reinterpret_cast<uint4*>(zhi + kZBytes + (c << 4)) = zero;
-            *reinterpret_cast<uint4*>(z0 + (c << 4)) = zero;
-#pragma unroll
-            for (int d = 0; d < KA / 64; ++d) *reinterpret_cast<uint4*>(y0 + d * 16384 + (c << 4)) = zero;
-          }
+          write_image();
         }
-        ptx::fence_proxy_async_smem();
-        ptx::mbar_arrive(&bars.z_ready);
+        const float dec = exp2f(l2 * (float)w.valid());
         if (!lin_wait_warp(&bars.d_full, it & 1, p)) {
           ok = false;
           break;
         }
         if (holds) {
           ptx::tc_fence_after();
-          const float dec = exp2f(l2 * (float)nv);
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            float d[32];
-            ptx::tmem_ld32(td + 32 * q, d);
+          for (int q = 0; q < 4; ++q) {
+            float dh[16], dl[16];
+            ptx::tmem_ld16(td + 16 * q, dh);
+            ptx::tmem_ld16(td + 64 + 16 * q, dl);
             ptx::tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) R[32 * q + j] = dec * R[32 * q + j] + d[j];
+            for (int j = 0; j < 16; j += 2) {
+              float2& x = *reinterpret_cast<float2*>(R + 16 * q + j);
+              x = ptx::fma2(make_float2(dec, dec), x, make_float2(dh[j] + dl[j], dh[j + 1] + dl[j + 1]));
+            }
           }
           ptx::tc_fence_before();
         }
-        if (!kStateOnly && w.k + 1 < w.n) write_image();  // Ob of this chunk has completed (before D)
+        ptx::mbar_arrive(&bars.d_free);
       }
       if (!ok) break;
       if (row < r.a) {
         if (kStateOnly) {
+          float* seg = lin_seg(p, w.x, w.hi) + (size_t)row * kLinTile;
 #pragma unroll
           for (int j = 0; j < kLinTile; j += 4)
             *reinterpret_cast<float4*>(seg + j) = make_float4(R[j], R[j + 1], R[j + 2], R[j + 3]);
-        } else if (r.fin && w.x.seg == (rev ? 0 : p.nseg - 1)) {
+        } else if (!w.last_block()) {
+#pragma unroll
+          for (int j = 0; j < kLinTile / 4; ++j)
+            keep[j * kC] = make_float4(R[4 * j], R[4 * j + 1], R[4 * j + 2], R[4 * j + 3]);
+        } else if (r.fin && lin_is_last(p, w.x)) {
           float* out = r.fin + (bh * r.a + row) * r.b + c0;
 #pragma unroll
           for (int j = 0; j < kLinTile; j += 4)
@@ -447,71 +530,87 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         }
       }
     }
-  } else if (!kStateOnly && warp >= 12) {
+  } else if (group == 2) {
+    ptx::regs_inc<120>();
+    if (!kStateOnly) {
     // ---- output -------------------------------------------------------------------------
-    const int row = tid - 384, quad = warp - 12, rot = row & 7;
-    const uint32_t loff = (uint32_t)(quad * 32) << 16;
+    const int rot = row & 7;
     uint8_t* stage = smem + S::kOut;
-    float4* scr = reinterpret_cast<float4*>(p.scratch) + (size_t)blockIdx.x * p.L * (kC * kLinTile / 4) + row;
+    float4* scr = reinterpret_cast<float4*>(p.scratch) +
+                  (size_t)blockIdx.x * (p.sub + p.hpg) * (kC * kLinTile / 4) + row;
     uint32_t it = 0;
     bool ok = true;
     for (Walk w(p, false); ok && w.live(); w.next_run()) {
-      const LinProb& r = p.pr[w.x.prob];
-      const bool rev = r.rev != 0;
+      const LinProb& r = w.prob();
+      const bool rev = w.rev;
       const float l2 = lin_log2_decay(p.log_a, w.head());
-      const bool first = w.hi == 0, last = w.hi + 1 == w.nh;
+      const bool first = w.first_head(), last = w.last_head();
       const int c0 = kLinTile * w.x.tile;
-      for (; w.k < w.n; ++w.k, ++it) {
+      for (; w.k < w.k1; ++w.k, ++it) {
         const uint32_t bf = it & 1;
         const int nv = w.valid(), ch = w.chunk();
         // sums over a group's heads: 16 float4 per row, consecutive rows side by side
-        float4* sc = scr + (size_t)w.k * (kC * kLinTile / 4);
-        const bool in = row < nv;
+        float4* sc = scr + (size_t)(w.k - w.k0) * (kC * kLinTile / 4);
         const float wo = exp2f(l2 * (float)(rev ? nv - 1 - row : row + 1));
+        float4 sum[kGrouped ? kLinTile / 4 : 1];  // the heads before this one (on its way from L2 during the wait)
+        if (kGrouped && !first) {
+#pragma unroll
+          for (int j = 0; j < kLinTile / 4; ++j) sum[kGrouped ? j : 0] = sc[j * kC];
+        }
         if (!lin_wait_warp(&bars.o_full[bf], (it >> 1) & 1, p)) {
           ok = false;
           break;
         }
         ptx::tc_fence_after();
-        if (last) {
+        if (!kGrouped || last) {
           if (row == 0) ptx::bulk_wait_read_all();  // the previous tile has left the staging area
           ptx::named_bar_sync(2, 128);
         }
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          float oa[32], ob[32];
-          ptx::tmem_ld32(tb + kColS + 128 * bf + 64 + 32 * q + loff, oa);
-          ptx::tmem_ld32(tb + kColOb + 64 * bf + 32 * q + loff, ob);
+        auto quarter = [&](int q, const float4* s4) {
+          float oa[16], ob[16];
+          ptx::tmem_ld16(tb + kColS + 128 * bf + 64 + 16 * q + loff, oa);
+          ptx::tmem_ld16(tb + kColOb + 64 * bf + 16 * q + loff, ob);
           ptx::tmem_ld_wait();
-          if (q == 1) {
-            ptx::tc_fence_before();
-            ptx::mbar_arrive(&bars.o_empty[bf]);
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            float2& x = *reinterpret_cast<float2*>(oa + j);
+            x = ptx::fma2(make_float2(wo, wo), make_float2(ob[j], ob[j + 1]), x);
           }
+          if (nv < kC && row >= nv) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) oa[j] = in ? oa[j] + wo * ob[j] : 0.f;
-          if (!first) {
+            for (int j = 0; j < 16; ++j) oa[j] = 0.f;
+          }
+          if (kGrouped && !first) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float4 y = sc[(8 * q + j) * kC];
-              oa[4 * j] += y.x;
-              oa[4 * j + 1] += y.y;
-              oa[4 * j + 2] += y.z;
-              oa[4 * j + 3] += y.w;
+            for (int j = 0; j < 4; ++j) {
+              oa[4 * j] += s4[j].x;
+              oa[4 * j + 1] += s4[j].y;
+              oa[4 * j + 2] += s4[j].z;
+              oa[4 * j + 3] += s4[j].w;
             }
           }
-          if (!last) {
+          if (kGrouped && !last) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              sc[(8 * q + j) * kC] = make_float4(oa[4 * j], oa[4 * j + 1], oa[4 * j + 2], oa[4 * j + 3]);
+            for (int j = 0; j < 4; ++j)
+              sc[(4 * q + j) * kC] = make_float4(oa[4 * j], oa[4 * j + 1], oa[4 * j + 2], oa[4 * j + 3]);
           } else {
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              *reinterpret_cast<uint4*>(stage + row * 128 + (((4 * q + c) ^ rot) << 4)) =
+            for (int c = 0; c < 2; ++c)
+              *reinterpret_cast<uint4*>(stage + row * 128 + (((2 * q + c) ^ rot) << 4)) =
                   make_uint4(pack_bf16(oa[8 * c], oa[8 * c + 1]), pack_bf16(oa[8 * c + 2], oa[8 * c + 3]),
                              pack_bf16(oa[8 * c + 4], oa[8 * c + 5]), pack_bf16(oa[8 * c + 6], oa[8 * c + 7]));
           }
+        };
+        if (kGrouped) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) quarter(q, sum + 4 * q);
+        } else {
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) quarter(q, nullptr);
         }
-        if (last) {
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(&bars.o_empty[bf]);
+        if (!kGrouped || last) {
           ptx::fence_proxy_async_smem();
           ptx::named_bar_sync(2, 128);
           if (row == 0) {
@@ -520,58 +619,117 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
           }
         }
       }
-      if (ok && last) {  // chunks past the row's length: zeros
-        const int t1 = min(p.T, min((w.x.seg + 1) * p.L, p.NC) * kC);
-        const int nv8 = min(kLinTile, r.b - c0) / 8;
-        for (int t = max(w.lo, w.lo + w.n) * kC + row; t < t1; t += kC) {
+      if (ok && last && w.last_block()) {  // chunks past the row's length: zeros
+        const int t1 = min(p.T, w.x.hi * kC);
+        const int n8 = min(kLinTile, r.b - c0) / 8;
+        for (int t = (w.lo + w.n) * kC + row; t < t1; t += kC) {
           uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(r.out) +
                                               (((size_t)w.x.b * p.T + t) * r.oh + w.x.oh) * r.b + c0);
-          for (int c = 0; c < nv8; ++c) o[c] = make_uint4(0u, 0u, 0u, 0u);
+          for (int c = 0; c < n8; ++c) o[c] = make_uint4(0u, 0u, 0u, 0u);
         }
       }
     }
     if (row == 0) ptx::bulk_wait_read_all();
+    }
+  } else if (group == 3) {
+    ptx::regs_dec<64>();
+    // ---- w Z: two threads a token, 32 columns each, 64 tokens at a time --------------------
+    const int part = (row & 1) * 4;
+    uint32_t it = 0;
+    bool ok = true;
+    for (Walk w(p, kStateOnly); ok && w.live(); w.next_run()) {
+      const bool rev = w.rev;
+      const float l2 = lin_log2_decay(p.log_a, w.head());
+      for (; ok && w.k < w.k1; ++w.k, ++it) {
+        const uint32_t s = it % S::kStages;
+        const int nv = w.valid();
+        ok = lin_wait_warp(&bars.z_full[s], (it / S::kStages) & 1, p);
+        // rows of Y past the row's length are overwritten below: after their copy has landed
+        if (ok && nv < kC) ok = lin_wait_warp(&bars.xy_full[s], (it / S::kStages) & 1, p);
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          const int t = 64 * half + (row >> 1), rot = t & 7;
+          uint8_t* z0 = smem + s * S::kStage + 2 * S::kX + t * 128;
+          uint8_t* zhi = smem + S::kZt + t * 128;
+          uint4 x[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) x[c] = *reinterpret_cast<const uint4*>(z0 + (((part + c) ^ rot) << 4));
+          const float wt = exp2f(l2 * (float)(rev ? t + 1 : nv - 1 - t));
+          const __nv_bfloat16 w1 = __float2bfloat16_rn(wt), w2 = __float2bfloat16_rn(wt - __bfloat162float(w1));
+          const __nv_bfloat162 wh = __halves2bfloat162(w1, w1), wl = __halves2bfloat162(w2, w2);
+          // the products over the previous chunk's half have read it
+          if (ok && it > 0) ok = lin_wait_warp(&bars.z_free[half], (it & 1) ^ 1, p);
+          if (!ok) break;
+          if (t < nv) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int off = ((part + c) ^ rot) << 4;
+              uint4 y;
+              __nv_bfloat162* hx = reinterpret_cast<__nv_bfloat162*>(&x[c]);
+              __nv_bfloat162* hy = reinterpret_cast<__nv_bfloat162*>(&y);
+              // high part: bf16(wh z); low part: bf16(wl z + (wh z - high)), whose bracket
+              // is exact in bf16 (a product of two 8-bit significands less its first 8 bits)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 z = hx[e];
+                hx[e] = __hmul2(wh, z);
+                hy[e] = __hfma2(wl, z, __hfma2(wh, z, __hneg2(hx[e])));
+              }
+              *reinterpret_cast<uint4*>(zhi + off) = x[c];
+              *reinterpret_cast<uint4*>(zhi + kZBytes + off) = y;
+            }
+          } else {
+            // past the row's length: whatever the padding holds must not reach a product
+            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+            uint8_t* y0 = smem + s * S::kStage + S::kX + t * 128;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              const int off = (part + c) << 4;
+              *reinterpret_cast<uint4*>(zhi + off) = zero;
+              *reinterpret_cast<uint4*>(zhi + kZBytes + off) = zero;
+              *reinterpret_cast<uint4*>(z0 + off) = zero;
+#pragma unroll
+              for (int d = 0; d < KA / 64; ++d) *reinterpret_cast<uint4*>(y0 + d * 16384 + off) = zero;
+            }
+          }
+          ptx::fence_proxy_async_smem();
+          ptx::mbar_arrive(&bars.z_ready[half]);
+        }
+      }
+    }
   }
-  // join; on a timeout the MMAs issued may still run: give them a bounded wait
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  if (warp == 1) {
-    if (*reinterpret_cast<volatile unsigned*>(p.status) == kStatusTimeout) {
-      if (lane == 0) {
-        ptx::umma_commit(&bars.fin);
-        wait_bar(&bars.fin, 0);
-      }
-      __syncwarp();
-    }
-    ptx::tmem_dealloc(tb, 512);
-  }
+  if (warp == 18) ptx::tmem_dealloc(tb, 512);
 }
 
 bool lin_map(CUtensorMap* m, const void* base, int inner, int count, int T, int B) {
   return make_map(m, base, inner, count, T, B);
 }
 
-template <int KA>
-cudaError_t launch_ka(LinArgs& p, const LinMaps& maps, int ctas, cudaStream_t st) {
+template <int KA, bool kStateOnly, bool kGrouped>
+cudaError_t launch_one(const LinArgs& p, const LinMaps& maps, int items, int ctas, cudaStream_t st) {
   constexpr int smem = Lay<KA>::kBytes;
+  cudaError_t e = cudaFuncSetAttribute(lin_tc_kernel<KA, kStateOnly, kGrouped>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  lin_tc_kernel<KA, kStateOnly, kGrouped><<<min(ctas, items), kThreads, smem, st>>>(maps, p);
+  if ((e = cudaGetLastError()) == cudaSuccess) note_launch();
+  return e;
+}
+
+template <int KA>
+cudaError_t launch_ka(const LinArgs& p, const LinMaps& maps, int ctas, cudaStream_t st) {
   cudaError_t e;
+  bool grouped = false;
+  for (int i = 0; i < p.nprob; ++i) grouped = grouped || p.pr[i].nh > 1;
   if (p.nseg > 1) {
-    if ((e = cudaFuncSetAttribute(lin_tc_kernel<KA, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) !=
-        cudaSuccess)
-      return e;
-    lin_tc_kernel<KA, true><<<min(ctas, p.sunits), kThreads, smem, st>>>(maps, p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    note_launch();
+    if ((e = launch_one<KA, true, false>(p, maps, p.sitems, ctas, st)) != cudaSuccess) return e;
     if ((e = launch_lin_scan(p, st)) != cudaSuccess) return e;
   }
-  if ((e = cudaFuncSetAttribute(lin_tc_kernel<KA, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) !=
-      cudaSuccess)
-    return e;
-  lin_tc_kernel<KA, false><<<min(ctas, p.units), kThreads, smem, st>>>(maps, p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  note_launch();
-  return cudaSuccess;
+  return grouped ? launch_one<KA, false, true>(p, maps, p.items, ctas, st)
+                 : launch_one<KA, false, false>(p, maps, p.items, ctas, st);
 }
 
 }  // namespace
