@@ -68,6 +68,8 @@ _BP = ctypes.POINTER(BlocknormShape)
 def lib() -> ctypes.CDLL:
     """The loaded C library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(_LIB_PATH):
@@ -466,65 +468,114 @@ def loglinear_selftest_wait_timeout(spins: int, stream=None) -> None:
 
 
 # ---- linear attention with a decay per head ------------------------------------------------
-def _expect(name, x, shape, dtype, device, optional=False):
-    """x is a contiguous tensor of this shape, type and device (or None where optional)."""
+# These calls take a few microseconds on the GPU at their smallest, so the checks are kept
+# short: what follows from the sizes alone (the C shape, the sizes of the other tensors, the
+# workspace) is worked out once per combination of sizes.
+try:  # the current stream's handle without building a Stream object
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+except AttributeError:
+    def _raw_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
+
+
+def _bad(name, x, shape, dtype, index):
+    """Raises for a tensor that _ok refused."""
     if x is None:
-        if optional:
-            return
         raise ValueError(f"{name} is required")
     if x.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
     if x.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(x.shape)}")
-    if x.device != device:
-        raise ValueError(f"{name} is on {x.device}, the other tensors on {device}")
-    if not x.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if x.get_device() != index:
+        raise ValueError(f"{name} is on {x.device}, the first tensor on CUDA device {index}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-class _Device:
-    """Makes a CUDA device current for a call, where it is not already."""
-
-    def __init__(self, device):
-        if device.type != "cuda":
-            raise ValueError(f"tensors must be on a CUDA device, got {device}")
-        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _ok(x, shape, dtype, index):
+    return (x is not None and x.shape == shape and x.dtype is dtype and x.get_device() == index and
+            x.is_contiguous())
 
 
-def _workspace(workspace, nbytes, device, where):
-    if nbytes == 0:
-        raise LogLinearError(2, where)
+def _cuda_index(x):
+    index = x.get_device()
+    if index < 0:
+        raise ValueError(f"tensors must be on a CUDA device, got {x.device}")
+    return index
+
+
+def _call(fn, index, stream, args, where):
+    """fn(*args, stream) with the CUDA device `index` current; raises on an error status."""
+    if torch.cuda.current_device() == index:
+        st = fn(*args, _raw_stream(index) if stream is None else _stream_ptr(stream))
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, _stream_ptr(stream))
+    if st != LL_OK:
+        raise LogLinearError(st, where)
+
+
+def _workspace(workspace, nbytes, index):
     if workspace is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+        return torch.empty(nbytes, dtype=torch.uint8, device=index)
+    if workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on CUDA device {index}")
     return workspace
 
 
-def _lindecay_check(q, k, v, log_a, lead):
-    """Checks q, k, v, log_a against each other; returns the shape and its parts."""
-    if q.dim() != lead + 2 or v.dim() != lead + 2:
-        raise ValueError(f"q and v must have {lead + 2} dimensions, got {q.dim()} and {v.dim()}")
-    B, G, dk, H, dv = q.shape[0], q.shape[lead], q.shape[lead + 1], v.shape[lead], v.shape[lead + 1]
-    T = q.shape[1] if lead == 2 else 1
-    if G == 0 or H % G:
-        raise ValueError(f"{H} heads do not divide into {G} groups")
-    dt, dev = q.dtype, q.device
-    code = _dtype_code(dt)
-    head = q.shape[:lead]
-    _expect("q", q, q.shape, dt, dev)
-    _expect("k", k, q.shape, dt, dev)
-    _expect("v", v, head + (H, dv), dt, dev)
-    _expect("log_a", log_a, (H,), torch.float32, dev)
-    return LLShape(B, T, H, H // G, dk, dv, 0, 0, code), (B, H, dk, dv), dt, dev
+class _LinPlan:
+    """What follows from the sizes of q and v alone."""
+
+    __slots__ = ("shape", "ref", "states", "heads", "rows", "fwd_bytes", "bwd_bytes")
+
+    def __init__(self, q, v, dtype, lead):
+        if len(q) != lead + 2 or len(v) != lead + 2:
+            raise ValueError(f"q and v must have {lead + 2} dimensions, got {len(q)} and {len(v)}")
+        (G, dk), (H, dv) = q[lead:], v[lead:]
+        if q[:lead] != v[:lead]:
+            raise ValueError(f"q and v must agree in their first {lead} sizes, got {tuple(q)} and {tuple(v)}")
+        if G == 0 or H % G:
+            raise ValueError(f"{H} heads do not divide into {G} groups")
+        self.shape = LLShape(q[0], q[1] if lead == 2 else 1, H, H // G, dk, dv, 0, 0, _dtype_code(dtype))
+        self.ref = ctypes.byref(self.shape)
+        self.states = torch.Size((q[0], H, dk, dv))
+        self.heads = torch.Size((H,))
+        self.rows = torch.Size((q[0],))
+        self.fwd_bytes = lindecay_fwd_workspace_bytes(self.shape)
+        self.bwd_bytes = lindecay_bwd_workspace_bytes(self.shape)
+        if self.fwd_bytes == 0:
+            raise LogLinearError(2, "lindecay")
+
+
+_lin_plans = {}
+
+
+def _lin_plan(q, v, dtype, lead):
+    key = (q, v, dtype, lead)
+    plan = _lin_plans.get(key)
+    if plan is None:
+        if len(_lin_plans) >= 4096:
+            _lin_plans.clear()
+        plan = _lin_plans[key] = _LinPlan(q, v, dtype, lead)
+    return plan
+
+
+def _lin_checked(q, k, v, log_a, lead):
+    """Checks q, k, v, log_a against each other; returns the plan and the CUDA device."""
+    shape, dtype, index = q.shape, q.dtype, _cuda_index(q)
+    plan = _lin_plan(shape, v.shape, dtype, lead)
+    if not (_ok(k, shape, dtype, index) and _ok(v, v.shape, dtype, index) and q.is_contiguous() and
+            _ok(log_a, plan.heads, torch.float32, index)):
+        for name, x, want, dt in (("q", q, shape, dtype), ("k", k, shape, dtype), ("v", v, v.shape, dtype),
+                                  ("log_a", log_a, plan.heads, torch.float32)):
+            if not _ok(x, want, dt, index):
+                _bad(name, x, want, dt, index)
+    return plan, index
+
+
+def _lin_states(plan, index, **states):
+    for name, x in states.items():
+        if x is not None and not _ok(x, plan.states, torch.float32, index):
+            _bad(name, x, plan.states, torch.float32, index)
 
 
 def lindecay_fwd_workspace_bytes(shape: LLShape) -> int:
@@ -540,20 +591,18 @@ def lindecay_fwd(q, k, v, log_a, lengths=None, state_in=None, state_out=None, o=
     v: (B, T, H, d_v), bf16 or fp32; log_a: (H,) fp32.  lengths: (B,) int32 tokens per row;
     state_in, state_out: (B, H, d_k, d_v) fp32 states before the first and after the last
     token (state_out is written; it may be state_in)."""
-    shape, st_shape, dt, dev = _lindecay_check(q, k, v, log_a, 2)
-    _expect("lengths", lengths, (shape.batch,), torch.int32, dev, True)
-    _expect("state_in", state_in, st_shape, torch.float32, dev, True)
-    _expect("state_out", state_out, st_shape, torch.float32, dev, True)
+    plan, index = _lin_checked(q, k, v, log_a, 2)
+    if lengths is not None and not _ok(lengths, plan.rows, torch.int32, index):
+        _bad("lengths", lengths, plan.rows, torch.int32, index)
+    _lin_states(plan, index, state_in=state_in, state_out=state_out)
     if o is None:
         o = torch.empty_like(v)
-    else:
-        _expect("o", o, v.shape, dt, dev)
-    with _Device(dev):
-        workspace = _workspace(workspace, lindecay_fwd_workspace_bytes(shape), dev, "lindecay_fwd_workspace_bytes")
-        st = lib().lindecay_fwd(ctypes.byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(),
-                                _ptr(lengths), _ptr(state_in), o.data_ptr(), _ptr(state_out), workspace.data_ptr(),
-                                workspace.numel() * workspace.element_size(), _stream_ptr(stream))
-    _check(st, "lindecay_fwd")
+    elif not _ok(o, v.shape, v.dtype, index):
+        _bad("o", o, v.shape, v.dtype, index)
+    ws = _workspace(workspace, plan.fwd_bytes, index)
+    _call(lib().lindecay_fwd, index, stream,
+          (plan.ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), _ptr(lengths), _ptr(state_in),
+           o.data_ptr(), _ptr(state_out), ws.data_ptr(), ws.numel() * ws.element_size()), "lindecay_fwd")
     return o
 
 
@@ -561,36 +610,34 @@ def lindecay_bwd(q, k, v, log_a, dO, lengths=None, state_in=None, dstate_out=Non
                  stream=None):
     """Gradients of sum(dO * o) + sum(dstate_out * state_out) of lindecay_fwd: returns dq, dk
     (B, T, G, d_k) and dv (B, T, H, d_v); dstate_in, where given, receives state_in's."""
-    shape, st_shape, dt, dev = _lindecay_check(q, k, v, log_a, 2)
-    _expect("dO", dO, v.shape, dt, dev)
-    _expect("lengths", lengths, (shape.batch,), torch.int32, dev, True)
-    _expect("state_in", state_in, st_shape, torch.float32, dev, True)
-    _expect("dstate_out", dstate_out, st_shape, torch.float32, dev, True)
-    _expect("dstate_in", dstate_in, st_shape, torch.float32, dev, True)
+    plan, index = _lin_checked(q, k, v, log_a, 2)
+    if not _ok(dO, v.shape, v.dtype, index):
+        _bad("dO", dO, v.shape, v.dtype, index)
+    if lengths is not None and not _ok(lengths, plan.rows, torch.int32, index):
+        _bad("lengths", lengths, plan.rows, torch.int32, index)
+    _lin_states(plan, index, state_in=state_in, dstate_out=dstate_out, dstate_in=dstate_in)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    with _Device(dev):
-        workspace = _workspace(workspace, lindecay_bwd_workspace_bytes(shape), dev, "lindecay_bwd_workspace_bytes")
-        st = lib().lindecay_bwd(ctypes.byref(shape), q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(),
-                                _ptr(lengths), _ptr(state_in), dO.data_ptr(), _ptr(dstate_out), dq.data_ptr(),
-                                dk.data_ptr(), dv.data_ptr(), _ptr(dstate_in), workspace.data_ptr(),
-                                workspace.numel() * workspace.element_size(), _stream_ptr(stream))
-    _check(st, "lindecay_bwd")
+    ws = _workspace(workspace, plan.bwd_bytes, index)
+    _call(lib().lindecay_bwd, index, stream,
+          (plan.ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), _ptr(lengths), _ptr(state_in),
+           dO.data_ptr(), _ptr(dstate_out), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(dstate_in),
+           ws.data_ptr(), ws.numel() * ws.element_size()), "lindecay_bwd")
     return dq, dk, dv
 
 
 def lindecay_decode_step(q_t, k_t, v_t, log_a, states, o_t=None, stream=None):
     """One token: q_t, k_t (B, G, d_k); v_t (B, H, d_v); states (B, H, d_k, d_v) fp32, updated
     in place.  Returns o_t (B, H, d_v)."""
-    shape, st_shape, dt, dev = _lindecay_check(q_t, k_t, v_t, log_a, 1)
-    _expect("states", states, st_shape, torch.float32, dev)
+    plan, index = _lin_checked(q_t, k_t, v_t, log_a, 1)
+    if not _ok(states, plan.states, torch.float32, index):
+        _bad("states", states, plan.states, torch.float32, index)
     if o_t is None:
         o_t = torch.empty_like(v_t)
-    else:
-        _expect("o_t", o_t, v_t.shape, dt, dev)
-    with _Device(dev):
-        st = lib().lindecay_decode_step(ctypes.byref(shape), q_t.data_ptr(), k_t.data_ptr(), v_t.data_ptr(),
-                                        log_a.data_ptr(), o_t.data_ptr(), states.data_ptr(), _stream_ptr(stream))
-    _check(st, "lindecay_decode_step")
+    elif not _ok(o_t, v_t.shape, v_t.dtype, index):
+        _bad("o_t", o_t, v_t.shape, v_t.dtype, index)
+    _call(lib().lindecay_decode_step, index, stream,
+          (plan.ref, q_t.data_ptr(), k_t.data_ptr(), v_t.data_ptr(), log_a.data_ptr(), o_t.data_ptr(),
+           states.data_ptr()), "lindecay_decode_step")
     return o_t
 
 
@@ -609,20 +656,46 @@ class BlocknormGrads(NamedTuple):
     dw_pre: Optional[torch.Tensor]
 
 
-def _blocknorm_check(first, acts, weights, group, act, eps):
-    """Checks activations (name -> tensor or None) against `first` and weights (dim) fp32."""
-    shape, dt, dev = first.shape, first.dtype, first.device
-    code = _dtype_code(dt)
-    if not shape or shape[-1] == 0 or first.numel() == 0:
-        raise ValueError(f"activations must hold at least one row, got shape {tuple(shape)}")
-    D = shape[-1]
+class _BnPlan:
+    """What follows from the sizes and options of a block norm alone."""
+
+    __slots__ = ("shape", "ref", "weights", "bwd_bytes")
+
+    def __init__(self, size, dtype, group, act, eps):
+        code = _dtype_code(dtype)
+        if not size or 0 in size:
+            raise ValueError(f"activations must hold at least one row, got shape {tuple(size)}")
+        if act not in ACTS:
+            raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
+        D = size[-1]
+        self.shape = BlocknormShape(size.numel() // D, D, D if group is None else int(group), ACTS[act], eps, code)
+        self.ref = ctypes.byref(self.shape)
+        self.weights = torch.Size((D,))
+        self.bwd_bytes = int(lib().blocknorm_bwd_workspace_bytes(self.ref))
+        if self.bwd_bytes == 0:
+            raise LogLinearError(2, "blocknorm")
+
+
+_bn_plans = {}
+
+
+def _bn_checked(first, acts, weights, group, act, eps):
+    """Checks activations against `first` and weights against its last size ((name, tensor or
+    None) pairs); returns the plan and the CUDA device."""
+    size, dtype, index = first.shape, first.dtype, _cuda_index(first)
+    key = (size, dtype, group, act, eps)
+    plan = _bn_plans.get(key)
+    if plan is None:
+        if len(_bn_plans) >= 4096:
+            _bn_plans.clear()
+        plan = _bn_plans[key] = _BnPlan(size, dtype, group, act, eps)
     for name, x in acts:
-        _expect(name, x, shape, dt, dev, True)
+        if x is not None and not _ok(x, size, dtype, index):
+            _bad(name, x, size, dtype, index)
     for name, x in weights:
-        _expect(name, x, (D,), torch.float32, dev, True)
-    if act not in ACTS:
-        raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
-    return BlocknormShape(first.numel() // D, D, D if group is None else int(group), ACTS[act], eps, code), dev
+        if x is not None and not _ok(x, plan.weights, torch.float32, index):
+            _bad(name, x, plan.weights, torch.float32, index)
+    return plan, index
 
 
 def blocknorm_fwd(y=None, w_post=None, x=None, gate=None, scale=None, w_pre=None, group=None, act="silu", eps=1e-6,
@@ -634,18 +707,20 @@ def blocknorm_fwd(y=None, w_post=None, x=None, gate=None, scale=None, w_pre=None
     first = y if y is not None else x
     if first is None:
         raise ValueError("y or x is required")
-    shape, dev = _blocknorm_check(first, (("y", y), ("x", x), ("gate", gate), ("x_new", x_new), ("h", h)),
-                                  (("w_post", w_post), ("scale", scale), ("w_pre", w_pre)), group, act, eps)
-    if y is None and x_new is not None:
-        raise ValueError("x_new is x itself without y")
-    if y is not None and x_new is None:
+    plan, index = _bn_checked(first, (("y", y), ("x", x), ("gate", gate), ("x_new", x_new), ("h", h)),
+                              (("w_post", w_post), ("scale", scale), ("w_pre", w_pre)), group, act, eps)
+    if y is None:
+        if x_new is not None or gate is not None or w_post is not None or scale is not None:
+            raise ValueError("without y there is no x_new, gate, w_post or scale")
+        if w_pre is None and h is None:
+            raise ValueError("nothing to compute: neither y nor w_pre is given")
+    elif x_new is None:
         x_new = torch.empty_like(y)
     if h is None and w_pre is not None:
         h = torch.empty_like(first)
-    with _Device(dev):
-        st = lib().blocknorm_fwd(ctypes.byref(shape), _ptr(x), _ptr(y), _ptr(gate), _ptr(w_post), _ptr(scale),
-                                 _ptr(w_pre), _ptr(x_new), _ptr(h), _stream_ptr(stream))
-    _check(st, "blocknorm_fwd")
+    _call(lib().blocknorm_fwd, index, stream,
+          (plan.ref, _ptr(x), _ptr(y), _ptr(gate), _ptr(w_post), _ptr(scale), _ptr(w_pre), _ptr(x_new), _ptr(h)),
+          "blocknorm_fwd")
     return (x if y is None else x_new), h
 
 
@@ -657,20 +732,19 @@ def blocknorm_bwd(dx_new, y=None, w_post=None, dh=None, x_new=None, gate=None, s
     first = dx_new if dx_new is not None else dh
     if first is None:
         raise ValueError("dx_new or dh is required")
-    shape, dev = _blocknorm_check(first, (("dh", dh), ("x_new", x_new), ("y", y), ("gate", gate)),
-                                  (("w_post", w_post), ("scale", scale), ("w_pre", w_pre)), group, act, eps)
-    _expect("dx_new", dx_new, first.shape, first.dtype, dev, True)
+    if (dh is None) != (x_new is None):
+        raise ValueError("dh and x_new go together")
+    plan, index = _bn_checked(first, (("dx_new", dx_new), ("dh", dh), ("x_new", x_new), ("y", y), ("gate", gate)),
+                              (("w_post", w_post), ("scale", scale), ("w_pre", w_pre)), group, act, eps)
     if residual is None:
         residual = y is None or scale is not None or x_new is not None
-    like = lambda t: None if t is None else torch.empty_like(t)  # noqa: E731
-    g = BlocknormGrads(torch.empty_like(first) if residual else None, like(y), like(gate), like(w_post), like(scale),
-                       like(w_pre))
-    with _Device(dev):
-        nb = int(lib().blocknorm_bwd_workspace_bytes(ctypes.byref(shape)))
-        workspace = _workspace(workspace, nb, dev, "blocknorm_bwd_workspace_bytes")
-        st = lib().blocknorm_bwd(ctypes.byref(shape), _ptr(dx_new), _ptr(dh), _ptr(x_new), _ptr(y), _ptr(gate),
-                                 _ptr(w_post), _ptr(scale), _ptr(w_pre), _ptr(g.dx), _ptr(g.dy), _ptr(g.dgate),
-                                 _ptr(g.dw_post), _ptr(g.dscale), _ptr(g.dw_pre), workspace.data_ptr(),
-                                 workspace.numel() * workspace.element_size(), _stream_ptr(stream))
-    _check(st, "blocknorm_bwd")
+    like = torch.empty_like
+    g = BlocknormGrads(like(first) if residual else None, None if y is None else like(y),
+                       None if gate is None else like(gate), None if w_post is None else like(w_post),
+                       None if scale is None else like(scale), None if w_pre is None else like(w_pre))
+    ws = _workspace(workspace, plan.bwd_bytes, index)
+    _call(lib().blocknorm_bwd, index, stream,
+          (plan.ref, _ptr(dx_new), _ptr(dh), _ptr(x_new), _ptr(y), _ptr(gate), _ptr(w_post), _ptr(scale),
+           _ptr(w_pre), _ptr(g.dx), _ptr(g.dy), _ptr(g.dgate), _ptr(g.dw_post), _ptr(g.dscale), _ptr(g.dw_pre),
+           ws.data_ptr(), ws.numel() * ws.element_size()), "blocknorm_bwd")
     return g

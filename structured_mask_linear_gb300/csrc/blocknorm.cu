@@ -18,46 +18,72 @@
 #include <cuda_runtime.h>
 
 #include "blocknorm.cuh"
+#include "launch_util.cuh"
 #include "ptx.cuh"
 
 namespace ll {
 
 namespace {
 
+// Eight consecutive values as four fp32 pairs (packed arithmetic, ptx::mul2 and so on).
 struct F8 {
-  float v[8];
+  float2 v[4];
+};
+using ptx::add2;
+using ptx::fma2;
+using ptx::mul2;
+__device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
+__device__ __forceinline__ F8 fill8(float c) { return {{pair(c), pair(c), pair(c), pair(c)}}; }
+// The same as they lie in memory: kept so until they are used.
+struct RawF {
+  float4 a, b;
+};
+template <typename T>
+struct Raw;
+template <>
+struct Raw<float> {
+  using type = RawF;
+};
+template <>
+struct Raw<__nv_bfloat16> {
+  using type = uint4;
 };
 __device__ __forceinline__ F8 unpack8(const uint4& x) {
   F8 r;
   const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    r.v[2 * i] = __uint_as_float(w[i] << 16);
-    r.v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+  for (int i = 0; i < 4; ++i) r.v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
   return r;
 }
-__device__ __forceinline__ F8 load8(const float* p) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  return {{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w}};
+__device__ __forceinline__ F8 unpack8(const RawF& x) {
+  return {{make_float2(x.a.x, x.a.y), make_float2(x.a.z, x.a.w), make_float2(x.b.x, x.b.y), make_float2(x.b.z, x.b.w)}};
 }
-__device__ __forceinline__ F8 load8(const __nv_bfloat16* p) { return unpack8(*reinterpret_cast<const uint4*>(p)); }
+__device__ __forceinline__ uint4 raw8(const __nv_bfloat16* p) { return *reinterpret_cast<const uint4*>(p); }
+__device__ __forceinline__ RawF raw8(const float* p) {
+  return {reinterpret_cast<const float4*>(p)[0], reinterpret_cast<const float4*>(p)[1]};
+}
+template <typename T>
+__device__ __forceinline__ F8 load8(const T* p) {
+  return unpack8(raw8(p));
+}
 __device__ __forceinline__ void store8(float* p, const F8& x) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(x.v[0], x.v[1], x.v[2], x.v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(x.v[4], x.v[5], x.v[6], x.v[7]);
+  reinterpret_cast<float4*>(p)[0] = make_float4(x.v[0].x, x.v[0].y, x.v[1].x, x.v[1].y);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x.v[2].x, x.v[2].y, x.v[3].x, x.v[3].y);
 }
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+__device__ __forceinline__ uint32_t pack2(float2 a) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(a.x, a.y);
   return *reinterpret_cast<uint32_t*>(&h);
 }
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const F8& x) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack2(x.v[0], x.v[1]), pack2(x.v[2], x.v[3]), pack2(x.v[4], x.v[5]),
-                                            pack2(x.v[6], x.v[7]));
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack2(x.v[0]), pack2(x.v[1]), pack2(x.v[2]), pack2(x.v[3]));
 }
-__device__ __forceinline__ F8 fill8(float c) { return {{c, c, c, c, c, c, c, c}}; }
 __device__ __forceinline__ F8 weight8(const float* w, int c) { return w ? load8(w + c) : fill8(1.f); }
+__device__ __forceinline__ float sum8(const F8& x) {
+  const float2 s = add2(add2(x.v[0], x.v[1]), add2(x.v[2], x.v[3]));
+  return s.x + s.y;
+}
 
-__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + __expf(-x)); }
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
 __device__ __forceinline__ float act_of(int act, float g) {
   return act == BN_SILU ? g * sigmoid(g) : act == BN_SIGMOID ? sigmoid(g) : g;
 }
@@ -67,6 +93,7 @@ __device__ __forceinline__ float2 act_grad(int act, float g) {
   const float s = sigmoid(g);
   return act == BN_SILU ? make_float2(g * s, s * (1.f + g * (1.f - s))) : make_float2(s, s * (1.f - s));
 }
+__device__ __forceinline__ float2 act_of2(int act, float2 g) { return make_float2(act_of(act, g.x), act_of(act, g.y)); }
 
 // Sum over the aligned groups of `width` lanes (a power of two) that hold a value each.
 __device__ __forceinline__ float lanes_sum(float x, int width) {
@@ -100,6 +127,7 @@ __device__ __forceinline__ void row_sum(float (&x)[K], int tpr, float* red) {
 // ---------------------------------------------------------------------------------
 template <typename T, int NV>
 __global__ void __launch_bounds__(512) bn_fwd_kernel(const __grid_constant__ BnArgs p, int tpr, int gl) {
+  using R8 = typename Raw<T>::type;
   __shared__ float red1[16], red2[16];
   const int t = threadIdx.x & (tpr - 1);
   const long long row = (long long)blockIdx.x * (blockDim.x / tpr) + threadIdx.x / tpr;
@@ -108,22 +136,24 @@ __global__ void __launch_bounds__(512) bn_fwd_kernel(const __grid_constant__ BnA
   const T* X = static_cast<const T*>(p.x);
   const T* Y = static_cast<const T*>(p.y);
   const T* Gt = static_cast<const T*>(p.gate);
-  F8 x[NV], y[NV], g[NV];
+  R8 yr[NV], xr[NV], gr[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = (i * tpr + t) * 8;
     const bool on = live && c < p.D;
-    y[i] = on && Y ? load8(Y + base + c) : fill8(0.f);
-    x[i] = on && X ? load8(X + base + c) : fill8(0.f);
-    g[i] = on && Gt ? load8(Gt + base + c) : fill8(0.f);
+    yr[i] = on && Y ? raw8(Y + base + c) : R8{};
+    xr[i] = on && X ? raw8(X + base + c) : R8{};
+    gr[i] = on && Gt ? raw8(Gt + base + c) : R8{};
   }
+  F8 x[NV];
   if (Y) {
     float ss[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      ss[i] = 0.f;
+      F8 y = unpack8(yr[i]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss[i] += y[i].v[e] * y[i].v[e];
+      for (int e = 0; e < 4; ++e) y.v[e] = mul2(y.v[e], y.v[e]);
+      ss[i] = sum8(y);
     }
     if (gl) {
 #pragma unroll
@@ -140,24 +170,31 @@ __global__ void __launch_bounds__(512) bn_fwd_kernel(const __grid_constant__ BnA
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * tpr + t) * 8;
+      x[i] = unpack8(xr[i]);
       if (!live || c >= p.D) continue;
       const float r = rsqrtf(ss[i] * p.inv_group + p.eps);
-      const F8 w = weight8(p.w_post, c), sc = weight8(p.scale, c);
+      const F8 w = weight8(p.w_post, c), sc = weight8(p.scale, c), y = unpack8(yr[i]), g = unpack8(gr[i]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        float m = y[i].v[e] * r * w.v[e];
-        if (Gt) m *= act_of(p.act, g[i].v[e]);
-        x[i].v[e] += sc.v[e] * m;
+      for (int e = 0; e < 4; ++e) {
+        float2 m = mul2(mul2(y.v[e], pair(r)), w.v[e]);
+        if (Gt) m = mul2(m, act_of2(p.act, g.v[e]));
+        x[i].v[e] = fma2(sc.v[e], m, x[i].v[e]);
       }
       store8(XN + base + c, x[i]);
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) x[i] = unpack8(xr[i]);
   }
   if (!p.h) return;
   float s[1] = {0.f};
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+  for (int i = 0; i < NV; ++i) {
+    F8 q;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s[0] += x[i].v[e] * x[i].v[e];
+    for (int e = 0; e < 4; ++e) q.v[e] = mul2(x[i].v[e], x[i].v[e]);
+    s[0] += sum8(q);
+  }
   row_sum(s, tpr, red2);
   const float r = rsqrtf(s[0] * p.inv_D + p.eps);
 #pragma unroll
@@ -166,27 +203,28 @@ __global__ void __launch_bounds__(512) bn_fwd_kernel(const __grid_constant__ BnA
     if (!live || c >= p.D) continue;
     const F8 w = weight8(p.w_pre, c);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[i].v[e] *= r * w.v[e];
+    for (int e = 0; e < 4; ++e) x[i].v[e] = mul2(mul2(x[i].v[e], pair(r)), w.v[e]);
     store8(static_cast<T*>(p.h) + base + c, x[i]);
   }
 }
 
 // ---------------------------------------------------------------------------------
-// bn_bwd: persistent CTAs of 512 threads, one per SM, 512 / tpr rows at a time.  Rows are
-// contiguous, so a step's rows of each input are one bulk copy into a ring of stages in
-// shared memory; the reductions of one step overlap the copies of the next ones.  The
-// weights' gradients stay in registers over a CTA's rows and go out once, as one partial
-// row per row slot combined in shared memory; bn_reduce adds the CTAs' partials in order.
+// bn_bwd: persistent CTAs, two per SM (one for rows that need 512 threads), blockDim / tpr
+// rows at a time.  Rows are contiguous, so a step's rows of each input are one bulk copy
+// into a ring of stages in shared memory; the reductions of one step overlap the copies of
+// the next ones and the other CTA's arithmetic.  The weights' gradients stay in registers
+// over a CTA's rows and go out once, the row slots combined in shared memory; bn_reduce adds
+// the CTAs' partials in order.
 // ---------------------------------------------------------------------------------
-constexpr int kBwdT = 512;
+constexpr int kBwdMaxT = 512;
 constexpr int kBwdMaxStages = 8;
 
 template <typename T, int NV>
-__global__ void __launch_bounds__(kBwdT, 1) bn_bwd_kernel(const __grid_constant__ BnArgs p, int tpr, int gl, int stages) {
+__global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant__ BnArgs p, int tpr, int gl, int stages) {
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ __align__(8) uint64_t full[kBwdMaxStages];
-  __shared__ float red1[3 * (kBwdT / 32)], red2[kBwdT / 32];
-  const int tid = threadIdx.x, t = tid & (tpr - 1), slot = tid / tpr, R = kBwdT / tpr;
+  __shared__ float red1[3 * (kBwdMaxT / 32)], red2[kBwdMaxT / 32];
+  const int tid = threadIdx.x, t = tid & (tpr - 1), slot = tid / tpr, R = blockDim.x / tpr;
   const T* in[5] = {static_cast<const T*>(p.dh), static_cast<const T*>(p.x), static_cast<const T*>(p.dx_new),
                     static_cast<const T*>(p.y), static_cast<const T*>(p.gate)};
   const size_t arr = (size_t)R * p.D * sizeof(T);  // one array of a stage
@@ -211,11 +249,9 @@ __global__ void __launch_bounds__(kBwdT, 1) bn_bwd_kernel(const __grid_constant_
         load((long long)blockIdx.x + (long long)i * gridDim.x, i);
   }
   __syncthreads();
-  float apre[NV][8], apost[NV][8], ascale[NV][8];
+  F8 apre[NV], apost[NV], ascale[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) apre[i][e] = apost[i][e] = ascale[i][e] = 0.f;
+  for (int i = 0; i < NV; ++i) apre[i] = apost[i] = ascale[i] = fill8(0.f);
   long long it = 0;
   for (long long step = blockIdx.x; step < steps; step += gridDim.x, ++it) {
     const int st = (int)(it % stages);
@@ -240,16 +276,21 @@ __global__ void __launch_bounds__(kBwdT, 1) bn_bwd_kernel(const __grid_constant_
       if (!live || c >= p.D) continue;
       if (in[0]) {
         const F8 x = load8(aX + c), dh = load8(aH + c), w = weight8(p.w_pre, c);
+        float2 xx = mul2(x.v[0], x.v[0]), ux = mul2(mul2(dh.v[0], w.v[0]), x.v[0]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          s3[0] += x.v[e] * x.v[e];
-          s3[1] += dh.v[e] * w.v[e] * x.v[e];
+        for (int e = 1; e < 4; ++e) {
+          xx = fma2(x.v[e], x.v[e], xx);
+          ux = fma2(mul2(dh.v[e], w.v[e]), x.v[e], ux);
         }
+        s3[0] += xx.x + xx.y;
+        s3[1] += ux.x + ux.y;
       }
       if (in[3]) {
         const F8 y = load8(aY + c);
+        float2 yy = mul2(y.v[0], y.v[0]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sg[i] += y.v[e] * y.v[e];
+        for (int e = 1; e < 4; ++e) yy = fma2(y.v[e], y.v[e], yy);
+        sg[i] = yy.x + yy.y;
         s3[2] += sg[i];
       }
     }
@@ -258,43 +299,50 @@ __global__ void __launch_bounds__(kBwdT, 1) bn_bwd_kernel(const __grid_constant_
       for (int i = 0; i < NV; ++i) sg[i] = lanes_sum(sg[i], gl);
     }
     row_sum(s3, tpr, red1);
-    const float r2 = rsqrtf(s3[0] * p.inv_D + p.eps), c2 = r2 * r2 * s3[1] * p.inv_D;
+    const float r2 = rsqrtf(s3[0] * p.inv_D + p.eps), c2 = -r2 * r2 * r2 * s3[1] * p.inv_D;
     float se[NV], r1[NV];
-    F8 un[NV], yy[NV];
+    F8 un[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (i * tpr + t) * 8;
       se[i] = 0.f;
       r1[i] = rsqrtf((gl ? sg[i] : s3[2]) * p.inv_group + p.eps);
-      un[i] = yy[i] = fill8(0.f);
+      un[i] = fill8(0.f);
       if (!live || c >= p.D) continue;
       F8 dx = in[2] ? load8(aD + c) : fill8(0.f);
       if (in[0]) {
         const F8 x = load8(aX + c), dh = load8(aH + c), w = weight8(p.w_pre, c);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          apre[i][e] += dh.v[e] * x.v[e] * r2;
-          dx.v[e] += r2 * (dh.v[e] * w.v[e] - x.v[e] * c2);
+        for (int e = 0; e < 4; ++e) {
+          const float2 d = mul2(dh.v[e], pair(r2));
+          apre[i].v[e] = fma2(d, x.v[e], apre[i].v[e]);
+          dx.v[e] = fma2(d, w.v[e], fma2(x.v[e], pair(c2), dx.v[e]));
         }
       }
       if (p.dx) store8(static_cast<T*>(p.dx) + (size_t)row * p.D + c, dx);
       if (in[3]) {
-        const F8 w = weight8(p.w_post, c), sc = weight8(p.scale, c);
-        yy[i] = load8(aY + c);
+        const F8 w = weight8(p.w_post, c), sc = weight8(p.scale, c), y = load8(aY + c);
         F8 dg;
-        F8 g = in[4] ? load8(aG + c) : fill8(0.f);
+        const F8 g = in[4] ? load8(aG + c) : fill8(0.f);
+        float2 s = pair(0.f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float yn = yy[i].v[e] * r1[i], n = yn * w.v[e];
-          const float2 a = in[4] ? act_grad(p.act, g.v[e]) : make_float2(1.f, 0.f);
-          ascale[i][e] += dx.v[e] * a.x * n;
-          const float dm = dx.v[e] * sc.v[e];
-          dg.v[e] = dm * n * a.y;
-          const float dn = dm * a.x;
-          apost[i][e] += dn * yn;
-          un[i].v[e] = dn * w.v[e];
-          se[i] += un[i].v[e] * yy[i].v[e];
+        for (int e = 0; e < 4; ++e) {
+          const float2 yn = mul2(y.v[e], pair(r1[i])), n = mul2(yn, w.v[e]);
+          float2 dn = mul2(dx.v[e], sc.v[e]);
+          if (in[4]) {
+            const float2 a0 = act_grad(p.act, g.v[e].x), a1 = act_grad(p.act, g.v[e].y);
+            const float2 av = make_float2(a0.x, a1.x);
+            ascale[i].v[e] = fma2(mul2(dx.v[e], av), n, ascale[i].v[e]);
+            dg.v[e] = mul2(mul2(dn, n), make_float2(a0.y, a1.y));
+            dn = mul2(dn, av);
+          } else {
+            ascale[i].v[e] = fma2(dx.v[e], n, ascale[i].v[e]);
+          }
+          apost[i].v[e] = fma2(dn, yn, apost[i].v[e]);
+          un[i].v[e] = mul2(dn, w.v[e]);
+          s = fma2(un[i].v[e], y.v[e], s);
         }
+        se[i] = s.x + s.y;
         if (in[4]) store8(static_cast<T*>(p.dgate) + (size_t)row * p.D + c, dg);
       }
     }
@@ -309,19 +357,20 @@ __global__ void __launch_bounds__(kBwdT, 1) bn_bwd_kernel(const __grid_constant_
 #pragma unroll
       for (int i = 0; i < NV; ++i) se[i] = s[0];
     }
-    __syncthreads();  // every thread has read the stage (and red1, red2)
-    if (tid == 0 && step + (long long)stages * gridDim.x < steps) load(step + (long long)stages * gridDim.x, st);
     if (in[3]) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * tpr + t) * 8;
         if (!live || c >= p.D) continue;
-        const float k = r1[i] * r1[i] * se[i] * p.inv_group;
+        const float k = -r1[i] * r1[i] * r1[i] * se[i] * p.inv_group;
+        const F8 y = load8(aY + c);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) un[i].v[e] = r1[i] * (un[i].v[e] - yy[i].v[e] * k);
+        for (int e = 0; e < 4; ++e) un[i].v[e] = fma2(y.v[e], pair(k), mul2(un[i].v[e], pair(r1[i])));
         store8(static_cast<T*>(p.dy) + (size_t)row * p.D + c, un[i]);
       }
     }
+    __syncthreads();  // every thread has read the stage (and red1, red2)
+    if (tid == 0 && step + (long long)stages * gridDim.x < steps) load(step + (long long)stages * gridDim.x, st);
   }
   // partial sums of this CTA, the row slots combined in slot order
   float* part = p.part + (size_t)blockIdx.x * 3 * p.D;
@@ -333,17 +382,21 @@ __global__ void __launch_bounds__(kBwdT, 1) bn_bwd_kernel(const __grid_constant_
     for (int i = 0; i < NV; ++i) {
       const int c = (i * tpr + t) * 8;
       if (c >= p.D) continue;
+      const F8* from[3] = {&apre[i], &apost[i], &ascale[i]};
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float a0 = s ? acc[c + e] : 0.f, a1 = s ? acc[p.D + c + e] : 0.f, a2 = s ? acc[2 * p.D + c + e] : 0.f;
-        acc[c + e] = a0 + apre[i][e];
-        acc[p.D + c + e] = a1 + apost[i][e];
-        acc[2 * p.D + c + e] = a2 + ascale[i][e];
+      for (int k = 0; k < 3; ++k) {
+        F8 x = *from[k];
+        if (s) {
+          const F8 y = load8(acc + k * p.D + c);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x.v[e] = add2(y.v[e], x.v[e]);
+        }
+        store8(acc + k * p.D + c, x);
       }
     }
   }
   __syncthreads();
-  for (int c = tid; c < 3 * p.D; c += kBwdT) part[c] = acc[c];
+  for (int c = tid; c < 3 * p.D; c += blockDim.x) part[c] = acc[c];
 }
 
 // Sums of the CTAs' partials, in order: 32 columns x 8 slices of the parts per CTA.
@@ -523,14 +576,16 @@ cudaError_t fwd(const BnArgs& p, cudaStream_t st) {
   const int gl = group_lanes(p), nvec = p.D / 8;
   if (p.D % 8 || gl < 0) {
     const int smem = p.y ? p.D / p.group * 4 : 0;
-    cudaError_t e = cudaFuncSetAttribute(bn_fwd_any_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kBnMaxGroups * 4);
+    static SmemLimit limit;
+    const cudaError_t e = limit.raise(bn_fwd_any_kernel<T>, kBnMaxGroups * 4);
     if (e != cudaSuccess) return e;
     bn_fwd_any_kernel<T><<<(unsigned)p.rows, kAny, smem, st>>>(p);
     return cudaGetLastError();
   }
-  // one vector a thread up to 512 threads a row, then two or four
-  const int nv = nvec <= 512 ? 1 : nvec <= 1024 ? 2 : 4;
+  // With many rows, four vectors a thread (two in fp32): fewer threads a row, more rows on
+  // an SM at a time.  With few, one, for the shortest way through a row.
+  int nv = p.rows >= 4 * 152 && nvec >= 64 ? (sizeof(T) == 2 && nvec >= 128 ? 4 : 2) : 1;
+  while (nvec > 512 * nv) nv *= 2;
   int tpr = ceil_pow2((nvec + nv - 1) / nv);
   tpr = tpr < 32 ? 32 : tpr;
   const int threads = tpr < 128 ? 128 : tpr, R = threads / tpr;
@@ -541,37 +596,34 @@ cudaError_t fwd(const BnArgs& p, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-constexpr int kBwdSmem = 220 * 1024;
-
 template <typename T, int NV>
-cudaError_t bwd_fast(const BnArgs& p, int tpr, int gl, int ctas, cudaStream_t st) {
+cudaError_t bwd_fast(const BnArgs& p, const BnBwdPlan& pl, int gl, cudaStream_t st) {
   const int nin = (p.dh ? 2 : 0) + (p.dx_new ? 1 : 0) + (p.y ? 1 : 0) + (p.gate ? 1 : 0);
-  const size_t stage = (size_t)nin * (kBwdT / tpr) * p.D * sizeof(T), acc = (size_t)3 * p.D * 4;
-  int stages = (int)(kBwdSmem / stage);
+  const size_t stage = (size_t)nin * (pl.threads / pl.tpr) * p.D * sizeof(T), acc = (size_t)3 * p.D * 4;
+  int stages = (int)((size_t)pl.smem / stage);
   stages = stages > kBwdMaxStages ? kBwdMaxStages : stages;
   const size_t smem = stage * stages > acc ? stage * stages : acc;
-  cudaError_t e = cudaFuncSetAttribute(bn_bwd_kernel<T, NV>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBwdSmem);
+  static SmemLimit limit;
+  const cudaError_t e = limit.raise(bn_bwd_kernel<T, NV>, kBnBwdSmem);
   if (e != cudaSuccess) return e;
-  bn_bwd_kernel<T, NV><<<ctas, kBwdT, smem, st>>>(p, tpr, gl, stages);
+  bn_bwd_kernel<T, NV><<<pl.ctas, pl.threads, smem, st>>>(p, pl.tpr, gl, stages);
   return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t bwd(const BnArgs& p, cudaStream_t st) {
-  const int gl = group_lanes(p), nvec = p.D / 8;
+  const int gl = group_lanes(p);
   const BnBwdPlan pl = bn_bwd_plan(p, sizeof(T) == 2);
   cudaError_t e;
   if (!pl.fast) {
     const int smem = (3 * p.D + 2 * (p.D / p.group)) * 4;
-    e = cudaFuncSetAttribute(bn_bwd_any_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (3 * kBnMaxD + 2 * kBnMaxGroups) * 4);
+    static SmemLimit limit;
+    e = limit.raise(bn_bwd_any_kernel<T>, (3 * kBnMaxD + 2 * kBnMaxGroups) * 4);
     if (e != cudaSuccess) return e;
     bn_bwd_any_kernel<T><<<pl.ctas, kAny, smem, st>>>(p);
     e = cudaGetLastError();
   } else {
-    int tpr = ceil_pow2(nvec > 512 ? nvec / 2 + nvec % 2 : nvec);
-    tpr = tpr < 32 ? 32 : tpr;
-    e = nvec <= 512 ? bwd_fast<T, 1>(p, tpr, gl, pl.ctas, st) : bwd_fast<T, 2>(p, tpr, gl, pl.ctas, st);
+    e = pl.nv == 1 ? bwd_fast<T, 1>(p, pl, gl, st) : bwd_fast<T, 2>(p, pl, gl, st);
   }
   if (e != cudaSuccess) return e;
   note_launch();
@@ -588,14 +640,20 @@ cudaError_t bwd(const BnArgs& p, cudaStream_t st) {
 // Which backward kernel runs and on how many CTAs (each leaves a partial of the weights'
 // gradients in the workspace).
 BnBwdPlan bn_bwd_plan(const BnArgs& p, bool bf16) {
-  BnBwdPlan pl;
+  BnBwdPlan pl{};
   const int nvec = p.D / 8, e = bf16 ? 2 : 4;
-  int tpr = ceil_pow2(nvec > 512 ? nvec / 2 + nvec % 2 : nvec);
-  tpr = tpr < 32 ? 32 : tpr;
-  // the widest rows that leave room for one step of rows of all five inputs
-  pl.fast = p.D % 8 == 0 && nvec <= 1024 && group_lanes(p) >= 0 && (long long)5 * (kBwdT / tpr) * p.D * e <= kBwdSmem;
-  const long long steps = pl.fast ? (p.rows + kBwdT / tpr - 1) / (kBwdT / tpr) : p.rows;
-  pl.ctas = (int)(steps < 152 ? steps : 152);
+  pl.nv = nvec <= 32 ? 1 : 2;
+  pl.tpr = ceil_pow2((nvec + pl.nv - 1) / pl.nv);
+  pl.tpr = pl.tpr < 32 ? 32 : pl.tpr;
+  pl.threads = pl.tpr <= 256 ? 256 : 512;
+  // two CTAs an SM where the rows of a step leave room for two of them, else one
+  const long long stage = 5LL * (pl.threads / pl.tpr) * p.D * e;
+  const int per_sm = pl.threads == 256 && 2 * stage <= kBnBwdSmem ? 2 : 1;
+  pl.smem = kBnBwdSmem / per_sm;
+  pl.fast = p.D % 8 == 0 && nvec <= 1024 && group_lanes(p) >= 0 && stage <= pl.smem;
+  const long long steps = pl.fast ? (p.rows + pl.threads / pl.tpr - 1) / (pl.threads / pl.tpr) : p.rows;
+  const int most = pl.fast ? 152 * per_sm : kBnMaxParts;
+  pl.ctas = (int)(steps < most ? steps : most);
   return pl;
 }
 

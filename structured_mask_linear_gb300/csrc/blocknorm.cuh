@@ -34,9 +34,12 @@ struct BnArgs {
   unsigned* status;
 };
 
+constexpr int kBnMaxParts = 304;           // CTAs of the backward: at most two per SM
+constexpr int kBnBwdSmem = 220 * 1024;     // its shared memory per SM
+
 struct BnBwdPlan {
   bool fast;
-  int ctas;
+  int ctas, threads, tpr, nv, smem;
 };
 BnBwdPlan bn_bwd_plan(const BnArgs& p, bool bf16);
 cudaError_t launch_bn_fwd(const BnArgs& p, bool bf16, cudaStream_t st);

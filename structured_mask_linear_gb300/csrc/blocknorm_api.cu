@@ -60,7 +60,7 @@ ll_status blocknorm_fwd(const blocknorm_shape* s, const void* x, const void* y, 
 
 size_t blocknorm_bwd_workspace_bytes(const blocknorm_shape* s) {
   if (check_shape(s) != LL_OK) return 0;
-  return (size_t)152 * 3 * s->dim * 4;
+  return (size_t)ll::kBnMaxParts * 3 * s->dim * 4;
 }
 
 ll_status blocknorm_bwd(const blocknorm_shape* s, const void* dx_new, const void* dh, const void* x_new,

@@ -2,6 +2,7 @@
 // lindecay.cuh): the prefix over segment totals, the fp32 scan, and the single-token step.
 #include <cuda_runtime.h>
 
+#include "launch_util.cuh"
 #include "lindecay.cuh"
 
 namespace ll {
@@ -330,17 +331,15 @@ cudaError_t launch_lin_f32(LinArgs& p, cudaStream_t st) {
   cudaError_t e;
   constexpr int smem = sizeof(F32Smem);
   if (p.nseg > 1) {
-    if ((e = cudaFuncSetAttribute(lin_f32_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) !=
-        cudaSuccess)
-      return e;
+    static SmemLimit limit;
+    if ((e = limit.raise(lin_f32_kernel<true>, smem)) != cudaSuccess) return e;
     lin_f32_kernel<true><<<p.sitems, kF, smem, st>>>(p);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     note_launch();
     if ((e = launch_lin_scan(p, st)) != cudaSuccess) return e;
   }
-  if ((e = cudaFuncSetAttribute(lin_f32_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) !=
-      cudaSuccess)
-    return e;
+  static SmemLimit limit;
+  if ((e = limit.raise(lin_f32_kernel<false>, smem)) != cudaSuccess) return e;
   lin_f32_kernel<false><<<p.items, kF, smem, st>>>(p);
   if ((e = cudaGetLastError()) == cudaSuccess) note_launch();
   return e;

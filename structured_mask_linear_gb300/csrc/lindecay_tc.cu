@@ -32,6 +32,7 @@
 // The launch gives 96 registers a thread; the last two groups hand 32 each to the others.
 // Every mbarrier wait is bounded (wait_bar); one that runs out records LL_ERR_TIMEOUT and
 // ends its role, the others follow by their own limits.
+#include "launch_util.cuh"
 #include "lindecay.cuh"
 #include "tc_common.cuh"
 
@@ -711,8 +712,8 @@ bool lin_map(CUtensorMap* m, const void* base, int inner, int count, int T, int 
 template <int KA, bool kStateOnly, bool kGrouped>
 cudaError_t launch_one(const LinArgs& p, const LinMaps& maps, int items, int ctas, cudaStream_t st) {
   constexpr int smem = Lay<KA>::kBytes;
-  cudaError_t e = cudaFuncSetAttribute(lin_tc_kernel<KA, kStateOnly, kGrouped>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static SmemLimit limit;
+  cudaError_t e = limit.raise(lin_tc_kernel<KA, kStateOnly, kGrouped>, smem);
   if (e != cudaSuccess) return e;
   lin_tc_kernel<KA, kStateOnly, kGrouped><<<min(ctas, items), kThreads, smem, st>>>(maps, p);
   if ((e = cudaGetLastError()) == cudaSuccess) note_launch();
