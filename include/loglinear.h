@@ -394,7 +394,8 @@ ll_status ssd_fwd(const ll_shape* shape, const void* q, const void* k, const voi
  * 128-token chunk, earlier tokens included (0 times infinity in a masked product).
  */
 
-/* Bytes of device workspace lindecay_fwd needs (0: invalid shape). */
+/* Bytes of device workspace lindecay_fwd needs (0: invalid shape; 16: none is used, NULL
+ * will do). */
 size_t lindecay_fwd_workspace_bytes(const ll_shape* shape);
 
 /*
@@ -411,7 +412,8 @@ ll_status lindecay_fwd(const ll_shape* shape, const void* q, const void* k, cons
                        const int* lengths, const float* state_in, void* o, float* state_out, void* workspace,
                        size_t workspace_bytes, void* stream);
 
-/* Bytes of device workspace lindecay_bwd needs (0: invalid shape). */
+/* Bytes of device workspace lindecay_bwd needs (0: invalid shape; 16: none is used, NULL
+ * will do). */
 size_t lindecay_bwd_workspace_bytes(const ll_shape* shape);
 
 /*

@@ -515,6 +515,7 @@ def _call(fn, index, stream, args, where):
 
 
 def _workspace(workspace, nbytes, index):
+    """The caller's workspace or a new one; (pointer, bytes)."""
     if workspace is None:
         return torch.empty(nbytes, dtype=torch.uint8, device=index)
     if workspace.get_device() != index or not workspace.is_contiguous():

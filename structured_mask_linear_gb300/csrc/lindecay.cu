@@ -24,7 +24,6 @@ __global__ void __launch_bounds__(256) lin_scan_kernel(const __grid_constant__ L
   LinItem x;
   x.prob = blockIdx.y;
   x.unit = r.split0 + uh / r.nh;
-  x.seg = 0;
   lin_locate(p, x);
   const int tile = x.tile, b = x.b, h = x.oh * r.nh + uh % r.nh, bh = b * p.H + h;
   const int row = q / (kLinTile / 4), c = q % (kLinTile / 4) * 4;
@@ -43,7 +42,7 @@ __global__ void __launch_bounds__(256) lin_scan_kernel(const __grid_constant__ L
   auto fetch = [&](int i0, float4(&to)[kBatch]) {
 #pragma unroll
     for (int k = 0; k < kBatch; ++k)
-      if (i0 + k < last) to[k] = s4[(size_t)(r.rev ? last - i0 - k : i0 + k) * n4];
+      if (i0 + k < last) to[k] = s4[(size_t)(i0 + k) * n4];
   };
   fetch(0, now);
   for (int i0 = 0; i0 <= last; i0 += kBatch) {
@@ -52,9 +51,11 @@ __global__ void __launch_bounds__(256) lin_scan_kernel(const __grid_constant__ L
     for (int k = 0; k < kBatch; ++k) {
       const int i = i0 + k;
       if (i <= last) {
-        const int s = r.rev ? last - i : i;
-        s4[(size_t)s * n4] = acc;
-        const float d = exp2f(l2 * (float)max(0, min(len - s * span, span)));
+        s4[(size_t)i * n4] = acc;
+        // tokens of segment i: in sequence order it starts at chunk i L, or ends there from the end
+        const int t0 = r.rev ? max(0, p.NC - (i + 1) * p.L) * p.chunk : i * span;
+        const int t1 = r.rev ? (p.NC - i * p.L) * p.chunk : t0 + span;
+        const float d = exp2f(l2 * (float)max(0, min(len, t1) - t0));
         acc.x = d * acc.x + now[k].x;
         acc.y = d * acc.y + now[k].y;
         acc.z = d * acc.z + now[k].z;
@@ -92,13 +93,13 @@ __global__ void __launch_bounds__(kF, 1) lin_f32_kernel(const __grid_constant__ 
   const LinItem x =
       kStateOnly ? lin_state_item(p, (int)blockIdx.x, &head0) : lin_item(p, (int)blockIdx.x);
   const LinProb& r = p.pr[x.prob];
-  const bool rev = r.rev != 0, split = lin_is_split(p, x);
+  const bool rev = r.rev != 0;
   const int sh = rev ? 0 : 1;
   const int a = r.a, b = r.b, c0 = kLinTile * x.tile, nc = min(kLinTile, b - c0);
   const int ldx = a + 4;
-  const int len = lin_len(p, x.b);
-  const int lo = x.lo, hi = min(x.hi, (len + kC32 - 1) / kC32);
-  const int n = max(0, hi - lo);
+  const int len = lin_len(p, x.b), cv = (len + kC32 - 1) / kC32;
+  int first, step;
+  const int n = lin_visit(p, x, cv, &first, &step);
   const float* Xg = static_cast<const float*>(r.X);
   const float* Yg = static_cast<const float*>(r.Y);
   const float* Zg = static_cast<const float*>(r.Z);
@@ -108,20 +109,20 @@ __global__ void __launch_bounds__(kF, 1) lin_f32_kernel(const __grid_constant__ 
     const int hx = r.xh == p.H ? h : g, hy = r.yh == p.H ? h : g, hz = r.zh == p.H ? h : g;
     const size_t bh = (size_t)x.b * p.H + h;
     const float l2 = lin_log2_decay(p.log_a, h);
-    float* seg = split ? lin_seg(p, x, hi_h) : nullptr;
+    float* seg = kStateOnly || x.from == kLinSeg ? lin_seg(p, x, hi_h) : nullptr;
     __syncthreads();
     for (int e = tid; e < a * kLinTile; e += kF) {
       const int i = e / kLinTile, j = e % kLinTile;
       float v = 0.f;
       if (!kStateOnly) {
-        if (split) v = seg[e];
+        if (seg) v = seg[e];
         else if (r.init && j < nc) v = r.init[bh * a * b + (size_t)i * r.init_rs + (size_t)(c0 + j) * r.init_cs];
       }
       sm.R[i * kLd + j] = v;
     }
     if (tid <= kC32) sm.pw[tid] = exp2f(l2 * (float)tid);
     for (int k = 0; k < n; ++k) {
-      const int ch = rev ? hi - 1 - k : lo + k;
+      const int ch = first + step * k;
       const int nv = min(kC32, len - ch * kC32);
       const size_t t0 = (size_t)x.b * p.T + (size_t)ch * kC32;
       __syncthreads();
@@ -212,16 +213,16 @@ __global__ void __launch_bounds__(kF, 1) lin_f32_kernel(const __grid_constant__ 
     __syncthreads();
     if (kStateOnly) {
       for (int e = tid; e < a * kLinTile; e += kF) seg[e] = sm.R[e / kLinTile * kLd + e % kLinTile];
-    } else if (r.fin && lin_is_last(p, x)) {
+    } else if (r.fin && x.to == kLinInit) {
       for (int e = tid; e < a * nc; e += kF)
         r.fin[(bh * a + e / nc) * b + c0 + e % nc] = sm.R[e / nc * kLd + e % nc];
     }
   }
   if (!kStateOnly) {  // chunks past the row's length: zeros
-    const int t1 = min(p.T, x.hi * kC32);
-    const int n4 = nc / 4;
+    int t0;
+    const int t1 = lin_past(p, x, cv, &t0), n4 = nc / 4;
     for (int e = tid;; e += kF) {
-      const int t = (lo + n) * kC32 + e / n4;
+      const int t = t0 + e / n4;
       if (t >= t1) break;
       *reinterpret_cast<float4*>(out + (((size_t)x.b * p.T + t) * r.oh + x.oh) * b + c0 + e % n4 * 4) =
           make_float4(0.f, 0.f, 0.f, 0.f);

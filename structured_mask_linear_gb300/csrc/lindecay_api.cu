@@ -12,6 +12,14 @@ using ll::LinProb;
 constexpr int kSms = 152;  // CTAs of a persistent launch: one per SM
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// Whether the current device has an SM for each CTA of a cooperative launch (without a
+// device, as if it had).
+bool all_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return true;
+  return n >= kSms;
+}
 size_t a256(size_t x) { return (x + 255) & ~size_t(255); }
 
 ll_status check_shape(const ll_shape* s) {
@@ -30,50 +38,82 @@ ll_status check_seq_shape(const ll_shape* s) {
 
 struct Plan {
   LinArgs args;
-  size_t off_seg[ll::kLinProbs], off_scratch, bytes;
+  size_t off_seg[ll::kLinProbs], off_scratch, off_hand, off_flag, bytes;
 };
 
-// How the units become work items.  Persistent CTAs take whole units in turn, one per SM;
-// the units of the last, incomplete turn (all of them when there are fewer units than SMs)
-// may be cut into segments, which costs them a pass over Y and Z first (kState of an
-// output chunk's time per chunk), two more launches (kLaunch chunks), a start per item
-// (kItem) and the prefix over the segments (kSeg each).  The cut with the least estimated
-// time wins, no cut included; in units of one output chunk on one SM, about 2 us.
-void cut_units(LinArgs& p) {
+// How the units become work items, by estimated time in eighths of what a chunk of a wide
+// scan (a > 64) takes on one SM (about 1.9 us):
+//  - wrapped: every SM gets an equal share of the line of units, or the longest unit's time
+//    where that is more.  Tensor cores only.
+//  - segmented: whole units in turn, the last incomplete turn's (all of them when there are
+//    fewer units than SMs) cut into segments.  The cut costs a pass over Y and Z first
+//    (kState of an output chunk's time per chunk), two more launches (kLaunch chunks), a
+//    start per item (kItem) and the prefix over the segments (kSeg each).
+// With many units the first needs no extra pass; with fewer than SMs only the second gives
+// every SM work.
+void cut_units(LinArgs& p, bool bf16) {
   constexpr double kState = 0.6, kLaunch = 4.0, kItem = 1.0, kSeg = 0.1;
   int units = 0, nh_tail = 1;
+  long long line = 0, longest = 0;
+  int abreast = 8;  // divides the 152 SMs
   for (int i = 0; i < p.nprob; ++i) {
-    p.pr[i].unit0 = units;
-    units += p.B * p.pr[i].oh * p.pr[i].tiles;
+    LinProb& r = p.pr[i];
+    r.nunits = p.B * r.oh * r.tiles;
+    r.unit0 = units;
+    r.pos0 = line;
+    r.cost = (bf16 && r.a <= 64 ? 7 : 8) * r.nh;
+    units += r.nunits;
+    // units that read the same X and Y: a head's tiles, and the heads of a group where X and
+    // Y have one head for the group
+    int same = r.tiles * (r.xh != p.H && r.yh != p.H && r.oh == p.H ? p.hpg : 1);
+    while (same % abreast) abreast /= 2;
+    line += r.cost * p.NC * r.nunits;
+    longest = r.cost * p.NC > longest ? r.cost * p.NC : longest;
   }
   const int whole = units / kSms * kSms, rest = units - whole;
   for (int i = 0; i < p.nprob; ++i)
-    if (p.pr[i].unit0 + p.B * p.pr[i].oh * p.pr[i].tiles > whole && p.pr[i].nh > nh_tail) nh_tail = p.pr[i].nh;
+    if (p.pr[i].unit0 + p.pr[i].nunits > whole && p.pr[i].nh > nh_tail) nh_tail = p.pr[i].nh;
   p.nwhole = units;
   p.nseg = 1;
   p.L = p.NC;
-  if (rest > 0) {
-    double best = (double)p.NC * nh_tail;
-    for (int n = 2; n <= 256 && n <= p.NC; ++n) {
-      const int l = (p.NC + n - 1) / n, nseg = (p.NC + l - 1) / l;
-      const long long items = (long long)rest * nseg, sitems = (long long)rest * nh_tail * (nseg - 1);
-      const double c = (double)((items + kSms - 1) / kSms) * (l * nh_tail + kItem) +
-                       (double)((sitems + kSms - 1) / kSms) * (l * kState + kItem) + kLaunch + kSeg * nseg;
-      if (c < best) {
-        best = c;
-        p.nwhole = whole;
-        p.nseg = nseg;
-        p.L = l;
-      }
+  double tail = rest > 0 ? (double)p.NC * nh_tail : 0.0;
+  for (int n = 2; rest > 0 && n <= 256 && n <= p.NC; ++n) {
+    const int l = (p.NC + n - 1) / n, nseg = (p.NC + l - 1) / l;
+    const long long items = (long long)rest * nseg, sitems = (long long)rest * nh_tail * (nseg - 1);
+    const double c = (double)((items + kSms - 1) / kSms) * (l * nh_tail + kItem) +
+                     (double)((sitems + kSms - 1) / kSms) * (l * kState + kItem) + kLaunch + kSeg * nseg;
+    if (c < tail) {
+      tail = c;
+      p.nwhole = whole;
+      p.nseg = nseg;
+      p.L = l;
     }
+  }
+  double head = 0.0;  // the whole turns, each as long as its longest unit
+  for (int u = 0; u < whole; u += kSms) {
+    long long most = 0;
+    for (int i = 0; i < p.nprob; ++i)
+      if (p.pr[i].unit0 < u + kSms && p.pr[i].unit0 + p.pr[i].nunits > u && p.pr[i].cost > most) most = p.pr[i].cost;
+    head += (double)most / 8.0 * p.NC;
+  }
+  // the wait for a part's state is bounded by seconds: not for sequences whose parts may take that
+  const long long even = (line + kSms - 1) / kSms, turn = even > longest ? even : longest;
+  if (bf16 && units > kSms && units % kSms != 0 && p.NC <= (1 << 17) && turn / 8.0 + 1.0 < head + tail && all_sms()) {
+    p.turn = turn;
+    p.total = line / abreast;
+    p.abreast = abreast;
+    for (int i = 0; i < p.nprob; ++i) p.pr[i].pos0 /= abreast;
+    p.nwhole = units;
+    p.nseg = 1;
+    p.L = p.NC;
   }
   p.items = p.nwhole + (units - p.nwhole) * p.nseg;
   p.sitems = 0;
   for (int i = 0; i < p.nprob; ++i) {
     LinProb& r = p.pr[i];
-    const int n = p.B * r.oh * r.tiles, w = p.nwhole - r.unit0;
-    r.split0 = w < 0 ? 0 : w > n ? n : w;
-    r.nsplit = n - r.split0;
+    const int w = p.nwhole - r.unit0;
+    r.split0 = w < 0 ? 0 : w > r.nunits ? r.nunits : w;
+    r.nsplit = r.nunits - r.split0;
     r.sunit0 = p.sitems;
     p.sitems += r.nsplit * r.nh * (p.nseg - 1);
   }
@@ -99,7 +139,7 @@ void finish_plan(const ll_shape* s, Plan* pl) {
     p.pr[i].nh = p.pr[i].oh == p.H ? 1 : p.hpg;
     grouped = grouped || p.pr[i].nh > 1;
   }
-  cut_units(p);
+  cut_units(p, bf16);
   size_t off = 0;
   for (int i = 0; i < p.nprob; ++i) {
     const LinProb& r = p.pr[i];
@@ -108,6 +148,10 @@ void finish_plan(const ll_shape* s, Plan* pl) {
   }
   pl->off_scratch = off;
   if (bf16 && grouped) off += a256((size_t)kSms * (p.sub + p.hpg) * ll::kLinChunk * ll::kLinTile * 4);
+  pl->off_hand = off;
+  if (p.turn > 0) off += a256((size_t)(kSms + 1) * p.hpg * ll::kLinChunk * ll::kLinTile * 4);
+  pl->off_flag = off;
+  if (p.turn > 0) off += a256(kSms * sizeof(unsigned));
   pl->bytes = off;
 }
 
@@ -136,28 +180,23 @@ void plan_fwd(const ll_shape* s, const void* q, const void* k, const void* v, vo
   finish_plan(s, pl);
 }
 
-// The gradients' three scans, in one launch, or in two on the tensor cores where d_k and
-// d_v are padded to different widths (the kernel's).
+// The gradients' three scans: in one launch, or in two where the tensor-core kernels pad d_k
+// and d_v to different widths (dq and dk run over d_v, dv over d_k).  Returns the number of
+// launches; they run one after the other and share the workspace.
 int plan_bwd(const ll_shape* s, const void* q, const void* k, const void* v, const void* dO, void* dq, void* dk,
              void* dv, Plan* pl) {
   const int H = s->heads, G = H / s->heads_per_group;
-  const bool split = s->dtype == LL_BF16 && ll::lin_is_wide(s->d_k) != ll::lin_is_wide(s->d_v);
-  const LinProb pq = scan(dO, H, v, H, k, G, dq, G, s->d_v, s->d_k, 0);
-  const LinProb pk = scan(v, H, dO, H, q, G, dk, G, s->d_v, s->d_k, 1);
-  const LinProb pv = scan(k, G, q, G, dO, H, dv, H, s->d_k, s->d_v, 1);
-  pl[0].args = LinArgs{};
-  pl[0].args.pr[0] = pq;
-  pl[0].args.pr[1] = pk;
-  pl[0].args.nprob = split ? 2 : 3;
-  if (!split) pl[0].args.pr[2] = pv;
-  finish_plan(s, &pl[0]);
-  if (!split) return 1;
-  pl[1].args = LinArgs{};
-  pl[1].args.pr[0] = pv;
+  const int n = s->dtype == LL_BF16 && (s->d_k > 64) != (s->d_v > 64) ? 2 : 1;
+  pl[0].args = pl[1].args = LinArgs{};
+  pl[0].args.pr[0] = scan(dO, H, v, H, k, G, dq, G, s->d_v, s->d_k, 0);
+  pl[0].args.pr[1] = scan(v, H, dO, H, q, G, dk, G, s->d_v, s->d_k, 1);
+  (n == 2 ? pl[1].args.pr[0] : pl[0].args.pr[2]) = scan(k, G, q, G, dO, H, dv, H, s->d_k, s->d_v, 1);
+  pl[0].args.nprob = n == 2 ? 2 : 3;
   pl[1].args.nprob = 1;
-  finish_plan(s, &pl[1]);  // the launches run one after the other and share the workspace
-  return 2;
+  for (int i = 0; i < n; ++i) finish_plan(s, &pl[i]);
+  return n;
 }
+size_t bwd_bytes(const Plan* pl, int n) { return n == 2 && pl[1].bytes > pl[0].bytes ? pl[1].bytes : pl[0].bytes; }
 
 ll_status run(const ll_shape* s, Plan* pl, const float* log_a, const int* lengths, void* workspace, void* stream) {
   LinArgs& p = pl->args;
@@ -168,6 +207,8 @@ ll_status run(const ll_shape* s, Plan* pl, const float* log_a, const int* length
   char* ws = static_cast<char*>(workspace);
   for (int i = 0; i < p.nprob; ++i) p.pr[i].seg = reinterpret_cast<float*>(ws + pl->off_seg[i]);
   p.scratch = reinterpret_cast<float*>(ws + pl->off_scratch);
+  p.hand = reinterpret_cast<float*>(ws + pl->off_hand);
+  p.flag = reinterpret_cast<unsigned*>(ws + pl->off_flag);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = s->dtype == LL_BF16 ? ll::launch_lin_tc(p, kSms, st) : ll::launch_lin_f32(p, st);
   return e == cudaSuccess ? LL_OK : LL_ERR_CUDA;
@@ -181,7 +222,7 @@ size_t lindecay_fwd_workspace_bytes(const ll_shape* s) {
   if (check_seq_shape(s) != LL_OK) return 0;
   Plan pl;
   plan_fwd(s, nullptr, nullptr, nullptr, nullptr, &pl);
-  return pl.bytes + 256;
+  return pl.bytes > 0 ? pl.bytes : 16;
 }
 
 ll_status lindecay_fwd(const ll_shape* s, const void* q, const void* k, const void* v, const float* log_a,
@@ -194,7 +235,7 @@ ll_status lindecay_fwd(const ll_shape* s, const void* q, const void* k, const vo
     if (!aligned16(x)) return LL_ERR_ALIGN;
   Plan pl;
   plan_fwd(s, q, k, v, o, &pl);
-  if (!workspace || workspace_bytes < pl.bytes) return LL_ERR_WORKSPACE;
+  if (pl.bytes > 0 && (!workspace || workspace_bytes < pl.bytes)) return LL_ERR_WORKSPACE;
   if (!aligned16(workspace)) return LL_ERR_ALIGN;
   LinProb& r = pl.args.pr[0];
   r.init = state_in;
@@ -208,9 +249,7 @@ size_t lindecay_bwd_workspace_bytes(const ll_shape* s) {
   if (check_seq_shape(s) != LL_OK) return 0;
   Plan pl[2];
   const int n = plan_bwd(s, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, pl);
-  size_t b = pl[0].bytes;
-  if (n == 2 && pl[1].bytes > b) b = pl[1].bytes;
-  return b + 256;
+  return bwd_bytes(pl, n) > 0 ? bwd_bytes(pl, n) : 16;
 }
 
 ll_status lindecay_bwd(const ll_shape* s, const void* q, const void* k, const void* v, const float* log_a,
@@ -226,13 +265,9 @@ ll_status lindecay_bwd(const ll_shape* s, const void* q, const void* k, const vo
   if (dstate_in && (dstate_in == state_in || dstate_in == dstate_out)) return LL_ERR_SHAPE;
   Plan pl[2];
   const int n = plan_bwd(s, q, k, v, dO, dq, dk, dv, pl);
-  size_t need = pl[0].bytes;
-  if (n == 2 && pl[1].bytes > need) need = pl[1].bytes;
-  if (!workspace || workspace_bytes < need) return LL_ERR_WORKSPACE;
+  if (bwd_bytes(pl, n) > 0 && (!workspace || workspace_bytes < bwd_bytes(pl, n))) return LL_ERR_WORKSPACE;
   if (!aligned16(workspace)) return LL_ERR_ALIGN;
-  LinProb& pq = pl[0].args.pr[0];
-  LinProb& pk = pl[0].args.pr[1];
-  LinProb& pv = n == 2 ? pl[1].args.pr[0] : pl[0].args.pr[2];
+  LinProb &pq = pl[0].args.pr[0], &pk = pl[0].args.pr[1], &pv = n == 2 ? pl[1].args.pr[0] : pl[0].args.pr[2];
   pq.init = state_in;
   pk.init = pv.init = dstate_out;
   pq.init_rs = pk.init_rs = 1;  // dq and dk run over the transposed states

@@ -29,9 +29,10 @@
 //   warp 16     TMA loads, kStages chunks ahead
 //   warp 17     the MMAs of S, one chunk ahead of
 //   warp 18     the MMAs of D, Ob and Oa
-// The launch gives 96 registers a thread; the last two groups hand 32 each to the others.
-// Every mbarrier wait is bounded (wait_bar); one that runs out records LL_ERR_TIMEOUT and
-// ends its role, the others follow by their own limits.
+// The launch gives 96 registers a thread; the groups pass on what they do not need.
+// Every wait is bounded; one that runs out records LL_ERR_TIMEOUT, after which the roles run
+// through their walks without waiting or working (those that meet at named barriers keep
+// meeting there), let what they started end, and the CTA returns.
 #include "launch_util.cuh"
 #include "lindecay.cuh"
 #include "tc_common.cuh"
@@ -48,15 +49,40 @@ constexpr int kMisc = 1024;
 template <int KA>
 struct Lay {
   static constexpr int kX = kC * KA * 2;
-  static constexpr int kStage = 2 * kX + kZBytes;  // X, Y, Z (in this order)
   static constexpr int kStages = KA == 64 ? 3 : 2;
-  static constexpr int kZt = kStages * kStage;     // w Z: high part, low part
+  static constexpr int kRing = kStages * (2 * kX + kZBytes);
+  static constexpr int kZt = kRing;                // w Z: high part, low part
   static constexpr int kImg = kZt + 2 * kZBytes;   // R as bf16: KA rows x 128 bytes
   static constexpr int kOut = kImg + KA * 128;     // out tile on its way out
   static constexpr int kMiscOff = kOut + kZBytes;
   static constexpr int kBytes = kMiscOff + kMisc + 1024;  // + alignment
 };
 static_assert(Lay<128>::kBytes <= 232448, "shared memory");
+static_assert(3 * (2 * Lay<64>::kX + kZBytes) <= Lay<128>::kRing, "a narrow scan's three stages in a wide ring");
+
+// The ring of stages, X then Y then Z in each: three stages of a scan with a <= 64, two of a
+// wider one (KS = 64-wide blocks of a).  Where a CTA's items differ in width, the ring starts
+// over with the other layout; every role follows it through the same sequence.
+template <int KA>
+struct Ring {
+  uint32_t st = 0, bits = 0;  // stage, and the phase of each stage's barriers
+  int ks = KA == 64 ? 1 : 0;
+  __device__ __forceinline__ bool narrow() const { return KA == 64 || ks == 1; }
+  __device__ __forceinline__ bool width(int k) {  // whether the layout changes
+    if (KA == 64 || k == ks) return false;
+    ks = k;
+    st = 0;
+    return true;
+  }
+  __device__ __forceinline__ uint32_t x() const { return st * (narrow() ? 49152u : 81920u); }
+  __device__ __forceinline__ uint32_t y() const { return x() + (narrow() ? 16384u : 32768u); }
+  __device__ __forceinline__ uint32_t z() const { return x() + (narrow() ? 32768u : 65536u); }
+  __device__ __forceinline__ uint32_t phase() const { return (bits >> st) & 1u; }
+  __device__ __forceinline__ void next() {
+    bits ^= 1u << st;
+    st = st + 1 == (narrow() ? 3u : 2u) ? 0u : st + 1;
+  }
+};
 
 struct LinMaps {
   CUtensorMap m[kLinProbs][4];  // X, Y, Z (loads), out (stores)
@@ -71,31 +97,38 @@ constexpr uint32_t kColS = 0, kColOb = 256, kColD = 384;
 // block by block; otherwise the item is one run.
 struct Walk {
   const LinArgs& p;
-  bool state_only;
-  int u;             // item
+  bool state_only, live_;
+  int u;             // item: its number, or (wrapped) how manyth of this CTA
   LinItem x;
-  int nh, hi;        // heads of the item (first and current one)
+  int nh, hi;        // heads of the item, current one (first: h0)
   int h0;
-  int lo, n;         // first valid chunk, number of valid chunks
+  int n;             // number of chunks with tokens
   int len;           // valid tokens of the batch row
   int k0, k, k1;     // the run's chunks in scan order: k0 .. k1 - 1, k the current one
-  int c0, dc;        // chunk k is c0 + dc k
+  int c0, dc;        // chunk k is c0 + dc k in sequence order
   bool rev;
-  __device__ __forceinline__ Walk(const LinArgs& a, bool s) : p(a), state_only(s), u((int)blockIdx.x) { enter(); }
-  __device__ __forceinline__ bool live() const { return u < (state_only ? p.sitems : p.items); }
+  __device__ __forceinline__ Walk(const LinArgs& a, bool s) : p(a), state_only(s) {
+    u = !s && p.turn > 0 ? 0 : (int)blockIdx.x;
+    enter();
+  }
+  __device__ __forceinline__ bool live() const { return live_; }
   __device__ __forceinline__ const LinProb& prob() const { return p.pr[x.prob]; }
+  __device__ __forceinline__ int chunks_valid() const { return (len + kC - 1) / kC; }
   __device__ __forceinline__ void enter() {
-    if (!live()) return;
     h0 = 0;
-    x = state_only ? lin_state_item(p, u, &h0) : lin_item(p, u);
+    if (!state_only && p.turn > 0) {
+      // CTA numbers run against the line, so that a CTA waits for one of a lower number
+      live_ = lin_wrapped_item(p, (int)(gridDim.x - 1 - blockIdx.x), u, x);
+    } else {
+      live_ = u < (state_only ? p.sitems : p.items);
+      if (live_) x = state_only ? lin_state_item(p, u, &h0) : lin_item(p, u);
+    }
+    if (!live_) return;
     nh = state_only ? 1 : prob().nh;
     hi = h0;
     len = lin_len(p, x.b);
-    lo = x.lo;
-    n = max(0, min(x.hi, (len + kC - 1) / kC) - lo);
-    rev = prob().rev != 0;
-    c0 = rev ? lo + n - 1 : lo;
-    dc = rev ? -1 : 1;
+    n = lin_visit(p, x, chunks_valid(), &c0, &dc);
+    rev = dc < 0;
     block(0);
   }
   __device__ __forceinline__ void block(int first) {
@@ -117,7 +150,7 @@ struct Walk {
       hi = h0;
       block(k1);
     } else {
-      u += (int)gridDim.x;
+      u += !state_only && p.turn > 0 ? 1 : (int)gridDim.x;
       enter();
     }
   }
@@ -130,12 +163,13 @@ struct Bars {
   uint32_t tmem;
 };
 
-// A bounded wait; %globaltimer is slow to read, so only waits that last come to it.
+// A bounded wait; %globaltimer is slow to read, so only waits that last come to it.  Once a
+// wait has run out somewhere the others do not wait for theirs.
 __device__ __forceinline__ bool lin_wait(uint64_t* bar, uint32_t parity, const LinArgs& p) {
 #pragma unroll 1
   for (int i = 0; i < 1024; ++i)
     if (__builtin_expect(ptx::mbar_try_wait(bar, parity), 1)) return true;
-  if (wait_bar(bar, parity)) return true;
+  if (*reinterpret_cast<volatile unsigned*>(p.status) != kStatusTimeout && wait_bar(bar, parity)) return true;
   atomicExch(p.status, kStatusTimeout);
   return false;
 }
@@ -144,8 +178,25 @@ __device__ __forceinline__ bool lin_wait_warp(uint64_t* bar, uint32_t parity, co
   return __all_sync(0xffffffffu, lin_wait(bar, parity, p));
 }
 
+// Waits (bounded: 4 s) until another CTA has raised a flag; reads behind it see what that
+// CTA wrote before.
+__device__ __forceinline__ bool lin_wait_flag(const unsigned* flag, const LinArgs& p) {
+  const uint64_t t0 = ptx::globaltimer_ns();
+  bool ok = true;
+  while (ok && !__all_sync(0xffffffffu, ptx::ld_acquire_gpu(flag) != 0u))
+    ok = !__any_sync(0xffffffffu, ptx::globaltimer_ns() - t0 > 2 * kWaitNs);
+  if (!ok) atomicExch(p.status, kStatusTimeout);
+  return ok;
+}
 __device__ __forceinline__ bool lin_failed(const LinArgs& p) {
   return __any_sync(0xffffffffu, *reinterpret_cast<volatile unsigned*>(p.status) == kStatusTimeout);
+}
+
+// KA is the width that the stages are laid out for; with KA = 128 a scan of a <= 64 uses the
+// first half of its X and Y places (KS = 64-wide blocks of a).
+template <int KA>
+__device__ __forceinline__ int lin_blocks(const LinProb& r) {
+  return KA == 64 || r.a <= 64 ? 1 : 2;
 }
 
 template <int KA, bool kStateOnly, bool kGrouped>
@@ -195,71 +246,92 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
 
   const int group = warp >> 2;
   if (group == 4) {
-    ptx::regs_dec<64>();
+    ptx::regs_dec<kGrouped ? 64 : 80>();
   if (warp == 16) {
     // ---- loads --------------------------------------------------------------------------
-    uint32_t it = 0;
+    Ring<KA> rg;
+    uint32_t used = 0;  // stages that have been filled
     bool ok = true;
     for (Walk w(p, kStateOnly); ok && w.live(); w.next_run()) {
       const LinProb& r = w.prob();
       const CUtensorMap* m = maps.m[w.x.prob];
       const int h = w.head(), g = h / p.hpg;
       const int hx = r.xh == p.H ? h : g, hy = r.yh == p.H ? h : g, hz = r.zh == p.H ? h : g;
-      for (; w.k < w.k1; ++w.k, ++it) {
-        const uint32_t s = it % S::kStages, par = ((it / S::kStages) & 1) ^ 1;
-        const bool again = it >= (uint32_t)S::kStages;
-        uint8_t* st = smem + s * S::kStage;
+      const int ks = lin_blocks<KA>(r);
+      if (rg.width(ks))  // the whole ring has to be free of the other layout
+        for (int i = 0; i < 3; ++i)
+          if ((used >> i) & 1u) {
+            const uint32_t par = ((rg.bits >> i) & 1u) ^ 1u;
+            ok = ok && lin_wait_warp(&bars.xy_empty[i], par, p) && lin_wait_warp(&bars.z_empty[i], par, p);
+          }
+      for (; ok && w.k < w.k1; ++w.k) {
+        const uint32_t s = rg.st, par = rg.phase() ^ 1u;
+        const bool again = (used >> s) & 1u;
         const int t0 = w.chunk() * kC;
         ok = !again || lin_wait_warp(&bars.xy_empty[s], par, p);
         if (!ok) break;
         if (ptx::elect_one()) {
-          ptx::mbar_arrive_expect_tx(&bars.xy_full[s], kStateOnly ? S::kX : 2 * S::kX);
+          ptx::mbar_arrive_expect_tx(&bars.xy_full[s], (kStateOnly ? 1 : 2) * ks * 16384);
 #pragma unroll
           for (int c = 0; c < KA / 64; ++c) {
-            ptx::tma_load_4d(st + S::kX + c * 16384, &m[1], &bars.xy_full[s], 64 * c, hy, t0, w.x.b);
-            if (!kStateOnly) ptx::tma_load_4d(st + c * 16384, &m[0], &bars.xy_full[s], 64 * c, hx, t0, w.x.b);
+            if (c >= ks) break;
+            ptx::tma_load_4d(smem + rg.y() + c * 16384, &m[1], &bars.xy_full[s], 64 * c, hy, t0, w.x.b);
+            if (!kStateOnly) ptx::tma_load_4d(smem + rg.x() + c * 16384, &m[0], &bars.xy_full[s], 64 * c, hx, t0, w.x.b);
           }
         }
+        __syncwarp();
         ok = !again || lin_wait_warp(&bars.z_empty[s], par, p);
         if (!ok) {  // X and Y of this chunk are on their way
-          wait_bar(&bars.xy_full[s], par ^ 1);
+          wait_bar(&bars.xy_full[s], rg.phase());
           break;
         }
         if (ptx::elect_one()) {
           ptx::mbar_arrive_expect_tx(&bars.z_full[s], kZBytes);
-          ptx::tma_load_4d(st + 2 * S::kX, &m[2], &bars.z_full[s], kLinTile * w.x.tile, hz, t0, w.x.b);
+          ptx::tma_load_4d(smem + rg.z(), &m[2], &bars.z_full[s], kLinTile * w.x.tile, hz, t0, w.x.b);
         }
+        __syncwarp();
+        used |= 1u << s;
+        rg.next();
       }
     }
     if (!ok)  // let the copies in flight land before the CTA ends (bounded)
-      for (uint32_t j = it >= (uint32_t)S::kStages ? it - S::kStages : 0; j < it; ++j) {
-        wait_bar(&bars.xy_full[j % S::kStages], (j / S::kStages) & 1);
-        wait_bar(&bars.z_full[j % S::kStages], (j / S::kStages) & 1);
-      }
+      for (int i = 0; i < 3; ++i)
+        if ((used >> i) & 1u) {
+          const uint32_t par = ((rg.bits >> i) & 1u) ^ 1u;
+          wait_bar(&bars.xy_full[i], par);
+          wait_bar(&bars.z_full[i], par);
+        }
   } else if (!kStateOnly && warp == 17) {
     // ---- MMAs of S: the whole warp walks, one lane issues --------------------------------------
-    uint32_t n = 0;  // chunks of this CTA
-    for (Walk w(p, false); w.live(); w.next_run()) n += w.k1 - w.k0;
     // descriptors at the start of shared memory; their low 14 bits count 16-byte units, so
     // an offset is added there (addresses stay below 2^18)
     const uint64_t kmaj = ptx::smem_desc_sw128(ptx::smem_u32(smem), 16, 1024);
-    for (uint32_t it = 0; it < n; ++it) {
-      const uint32_t st = it % S::kStages, bf = it & 1;
-      if (it >= 2 && !lin_wait_warp(&bars.o_empty[bf], ((it >> 1) & 1) ^ 1, p)) break;
-      if (!lin_wait_warp(&bars.xy_full[st], (it / S::kStages) & 1, p)) break;
-      ptx::tc_fence_after();
-      if (ptx::elect_one()) {
-        const uint32_t idesc = ptx::idesc_bf16_f32(128, 128, 0, 0);
-        const uint64_t dx = kmaj + ((st * S::kStage) >> 4), dy = dx + (S::kX >> 4);
+    uint32_t it = 0;
+    Ring<KA> rg;
+    bool ok = true;
+    for (Walk w(p, false); ok && w.live(); w.next_run()) {
+      const int ks = lin_blocks<KA>(w.prob());
+      rg.width(ks);
+      for (; w.k < w.k1; ++w.k, ++it, rg.next()) {
+        const uint32_t bf = it & 1;
+        ok = it < 2 || lin_wait_warp(&bars.o_empty[bf], ((it >> 1) & 1) ^ 1, p);
+        ok = ok && lin_wait_warp(&bars.xy_full[rg.st], rg.phase(), p);
+        if (!ok) break;
+        ptx::tc_fence_after();
+        if (ptx::elect_one()) {
+          const uint32_t idesc = ptx::idesc_bf16_f32(128, 128, 0, 0);
+          const uint64_t dx = kmaj + (rg.x() >> 4), dy = kmaj + (rg.y() >> 4);
 #pragma unroll
-        for (int kk = 0; kk < KA / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-          ptx::umma_f16(tb + kColS + 128 * bf, dx + off, dy + off, idesc, kk > 0);
+          for (int kk = 0; kk < KA / 16; ++kk) {
+            if (kk >= 4 * ks) break;
+            const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+            ptx::umma_f16(tb + kColS + 128 * bf, dx + off, dy + off, idesc, kk > 0);
+          }
+          ptx::umma_commit(&bars.s_full[bf]);
+          ptx::umma_commit(&bars.xy_empty[rg.st]);
         }
-        ptx::umma_commit(&bars.s_full[bf]);
-        ptx::umma_commit(&bars.xy_empty[st]);
+        __syncwarp();
       }
-      __syncwarp();
     }
     if (lin_failed(p)) {  // the MMAs issued may still run: give them a bounded wait
       if (ptx::elect_one()) ptx::umma_commit(&bars.fin[0]);
@@ -267,76 +339,81 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     }
   } else if (warp == 18) {
     // ---- MMAs of D, Ob, Oa ------------------------------------------------------------------
-    uint32_t n = 0;
-    for (Walk w(p, kStateOnly); w.live(); w.next_run()) n += w.k1 - w.k0;
     const uint32_t s0 = ptx::smem_u32(smem);
     const uint64_t kmaj = ptx::smem_desc_sw128(s0, 16, 1024);       // X of Ob
     const uint64_t zmaj = ptx::smem_desc_sw128(s0, 1024, 1024);     // Z and R's image, N = 64
     const uint64_t amaj = ptx::smem_desc_sw128(s0, 16384, 1024);    // Yᵀ and [Zhi | Zlo] of D
     static_assert(kZBytes == 16384, "one LBO for both operands of D");
     const uint32_t idesc = ptx::idesc_bf16_f32(128, 64, 0, 1);
-    auto issue_oa = [&](uint32_t it) -> bool {
-      const uint32_t st = it % S::kStages, bf = it & 1;
-      if (!lin_wait_warp(&bars.p_ready[bf], (it >> 1) & 1, p)) return false;
-      ptx::tc_fence_after();
-      if (ptx::elect_one()) {
-        const uint32_t zo = (st * S::kStage + 2 * S::kX) >> 4, tp = tb + kColS + 128 * bf;
-#pragma unroll
-        for (int kk = 0; kk < kC / 16; ++kk)
-          ptx::umma_f16_tmem_a(tp + 64, tp + kk * 8, zmaj + zo + kk * 128, idesc, kk > 0);
-        ptx::umma_commit(&bars.o_full[bf]);
-        ptx::umma_commit(&bars.z_empty[st]);
-      }
-      __syncwarp();
-      return true;
-    };
+    uint32_t it = 0;
+    Ring<KA> rg;
     bool ok = true;
-    for (uint32_t it = 0; ok && it < n; ++it) {
-      const uint32_t st = it % S::kStages, bf = it & 1, par = it & 1;
-      const uint32_t xo = (st * S::kStage) >> 4, yo = xo + (S::kX >> 4);
-      // D = Yᵀ [Zhi | Zlo], by halves of 64 tokens: A is MN-major with M = 128 (with a padded
-      // to 64 its second 64 rows read Z's tile that follows Y, LBO 16 KB: lanes 64..127 of D
-      // are never read), B two 64-wide atoms 16 KB apart.
-      if (!lin_wait_warp(&bars.xy_full[st], (it / S::kStages) & 1, p)) break;
-      if (it > 0 && !lin_wait_warp(&bars.d_free, par ^ 1, p)) break;
+    for (Walk w(p, kStateOnly); ok && w.live(); w.next_run()) {
+      const int ks = lin_blocks<KA>(w.prob());
+      rg.width(ks);
+      for (; w.k < w.k1; ++w.k, ++it, rg.next()) {
+        const uint32_t st = rg.st, bf = it & 1, par = it & 1;
+        // D = Yᵀ [Zhi | Zlo], by halves of 64 tokens: A is MN-major with M = 128 (with a padded
+        // to 64 its second 64 rows read what lies 16 KB behind Y: lanes 64..127 of D are never
+        // read), B two 64-wide atoms 16 KB apart.
+        ok = lin_wait_warp(&bars.xy_full[st], rg.phase(), p);
+        if (it > 0) ok = ok && lin_wait_warp(&bars.d_free, par ^ 1, p);
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        ok = ok && lin_wait_warp(&bars.z_ready[half], par, p);
-        if (!ok) break;
-        ptx::tc_fence_after();
-        if (ptx::elect_one()) {
-          const uint32_t idesc_d = ptx::idesc_bf16_f32(128, 128, 1, 1);
+        for (int half = 0; half < 2; ++half) {
+          ok = ok && lin_wait_warp(&bars.z_ready[half], par, p);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          if (ptx::elect_one()) {
+            const uint32_t idesc_d = ptx::idesc_bf16_f32(128, 128, 1, 1);
+            const uint64_t dy = amaj + (rg.y() >> 4);
 #pragma unroll
-          for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-            ptx::umma_f16(tb + kColD, amaj + yo + kk * 128, amaj + (S::kZt >> 4) + kk * 128, idesc_d, kk > 0);
-          ptx::umma_commit(&bars.z_free[half]);
-          if (half == 1) {
-            ptx::umma_commit(&bars.d_full);
-            if (kStateOnly) {
-              ptx::umma_commit(&bars.xy_empty[st]);
-              ptx::umma_commit(&bars.z_empty[st]);
+            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+              ptx::umma_f16(tb + kColD, dy + kk * 128, amaj + (S::kZt >> 4) + kk * 128, idesc_d, kk > 0);
+            ptx::umma_commit(&bars.z_free[half]);
+            if (half == 1) {
+              ptx::umma_commit(&bars.d_full);
+              if (kStateOnly) {
+                ptx::umma_commit(&bars.xy_empty[st]);
+                ptx::umma_commit(&bars.z_empty[st]);
+              }
             }
           }
+          __syncwarp();
         }
-        __syncwarp();
-      }
-      if (!ok) break;
-      if (!kStateOnly) {
-        // Ob's columns have been read two chunks ago
-        if (it >= 2 && !lin_wait_warp(&bars.o_empty[bf], ((it >> 1) & 1) ^ 1, p)) break;
-        if (!lin_wait_warp(&bars.r_ready, par, p)) break;
-        ptx::tc_fence_after();
-        if (ptx::elect_one()) {
+        if (!ok) break;
+        if (!kStateOnly) {
+          const uint32_t idesc = ptx::idesc_bf16_f32(128, 64, 0, 1);
+          // Ob's columns have been read two chunks ago
+          if (it >= 2) ok = lin_wait_warp(&bars.o_empty[bf], ((it >> 1) & 1) ^ 1, p);
+          ok = ok && lin_wait_warp(&bars.r_ready, par, p);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          if (ptx::elect_one()) {
+            const uint64_t dx = kmaj + (rg.x() >> 4);
 #pragma unroll
-          for (int kk = 0; kk < KA / 16; ++kk) {
-            const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-            ptx::umma_f16(tb + kColOb + 64 * bf, kmaj + xo + off, zmaj + (S::kImg >> 4) + kk * 128, idesc, kk > 0);
+            for (int kk = 0; kk < KA / 16; ++kk) {
+              if (kk >= 4 * ks) break;
+              const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+              ptx::umma_f16(tb + kColOb + 64 * bf, dx + off, zmaj + (S::kImg >> 4) + kk * 128, idesc, kk > 0);
+            }
+            ptx::umma_commit(&bars.q_full);
+            ptx::umma_commit(&bars.xy_empty[st]);
           }
-          ptx::umma_commit(&bars.q_full);
-          ptx::umma_commit(&bars.xy_empty[st]);
+          __syncwarp();
+          ok = lin_wait_warp(&bars.p_ready[bf], (it >> 1) & 1, p);
+          if (!ok) break;
+          ptx::tc_fence_after();
+          if (ptx::elect_one()) {
+            const uint32_t tp = tb + kColS + 128 * bf;
+            const uint64_t dz = zmaj + (rg.z() >> 4);
+#pragma unroll
+            for (int kk = 0; kk < kC / 16; ++kk)
+              ptx::umma_f16_tmem_a(tp + 64, tp + kk * 8, dz + kk * 128, idesc, kk > 0);
+            ptx::umma_commit(&bars.o_full[bf]);
+            ptx::umma_commit(&bars.z_empty[st]);
+          }
+          __syncwarp();
         }
-        __syncwarp();
-        ok = issue_oa(it);
       }
     }
     if (lin_failed(p)) {
@@ -350,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     // ---- P ------------------------------------------------------------------------------
     uint32_t it = 0;
     bool ok = true;
-    for (Walk w(p, false); ok && w.live(); w.next_run()) {
+    for (Walk w(p, false); w.live(); w.next_run()) {
       if (w.k0 == w.k1) continue;
       const bool rev = w.rev;
       const float l2 = lin_log2_decay(p.log_a, w.head());
@@ -371,10 +448,8 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
       for (; w.k < w.k1; ++w.k, ++it) {
         const uint32_t bf = it & 1;
         const int nv = w.valid();
-        if (!lin_wait_warp(&bars.s_full[bf], (it >> 1) & 1, p)) {
-          ok = false;
-          break;
-        }
+        ok = ok && lin_wait_warp(&bars.s_full[bf], (it >> 1) & 1, p);
+        if (!ok) continue;
         ptx::tc_fence_after();
         const uint32_t ts = tb + kColS + 128 * bf + loff;
         // Group cg's packed columns 16 cg .. 16 cg + 15 lie over S of groups cg / 2 and, for
@@ -429,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     const uint32_t td = tb + kColD + loff;
     const int rot = row & 7;
     uint8_t* img = smem + S::kImg + row * 128;
-    const bool holds = row < KA;  // warp-uniform
+    bool holds = true;  // a row of R (warp-uniform)
     uint32_t it = 0;
     bool ok = true;
     float R[kLinTile];
@@ -444,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
       }
       ptx::mbar_arrive(&bars.r_ready);
     };
-    for (Walk w(p, kStateOnly); ok && w.live(); w.next_run()) {
+    for (Walk w(p, kStateOnly); w.live(); w.next_run()) {
       const LinProb& r = w.prob();
       const int h = w.head();
       const size_t bh = (size_t)w.x.b * p.H + h;
@@ -456,14 +531,21 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                      ((size_t)blockIdx.x * (p.sub + p.hpg) + p.sub + w.hi) * (kC * kLinTile / 4) + row;
 #pragma unroll
       for (int j = 0; j < kLinTile; ++j) R[j] = 0.f;
+      holds = row < 64 * lin_blocks<KA>(r);
+      if (!kStateOnly && w.first_block() && w.first_head() && w.x.from == kLinHand) {
+        ok = ok && lin_wait_flag(p.flag + w.x.slot, p);
+      }
+      float4* hand = reinterpret_cast<float4*>(p.hand) + ((size_t)w.x.slot * p.hpg + w.hi) * (kC * kLinTile / 4) + row;
       if (!kStateOnly && row < r.a) {
         const float4* from = nullptr;
-        int step = 1;
+        int step = kC;
         if (!w.first_block()) {
           from = keep;
-          step = kC;
-        } else if (lin_is_split(p, w.x)) {
+        } else if (w.x.from == kLinHand) {
+          from = hand;
+        } else if (w.x.from == kLinSeg) {
           from = reinterpret_cast<const float4*>(lin_seg(p, w.x, w.hi) + (size_t)row * kLinTile);
+          step = 1;
         }
         if (from) {
 #pragma unroll
@@ -483,17 +565,13 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
       }
       for (; w.k < w.k1; ++w.k, ++it) {
         if (!kStateOnly) {
-          if (it > 0 && !lin_wait_warp(&bars.q_full, (it & 1) ^ 1, p)) {  // the image is free
-            ok = false;
-            break;
-          }
+          if (it > 0) ok = ok && lin_wait_warp(&bars.q_full, (it & 1) ^ 1, p);  // the image is free
+          if (!ok) continue;
           write_image();
         }
         const float dec = exp2f(l2 * (float)w.valid());
-        if (!lin_wait_warp(&bars.d_full, it & 1, p)) {
-          ok = false;
-          break;
-        }
+        ok = ok && lin_wait_warp(&bars.d_full, it & 1, p);
+        if (!ok) continue;
         if (holds) {
           ptx::tc_fence_after();
 #pragma unroll
@@ -512,27 +590,33 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         }
         ptx::mbar_arrive(&bars.d_free);
       }
-      if (!ok) break;
-      if (row < r.a) {
+      if (ok && row < r.a) {
         if (kStateOnly) {
           float* seg = lin_seg(p, w.x, w.hi) + (size_t)row * kLinTile;
 #pragma unroll
           for (int j = 0; j < kLinTile; j += 4)
             *reinterpret_cast<float4*>(seg + j) = make_float4(R[j], R[j + 1], R[j + 2], R[j + 3]);
-        } else if (!w.last_block()) {
+        } else if (!w.last_block() || w.x.to == kLinHand) {
+          float4* to = w.last_block() ? hand : keep;
 #pragma unroll
           for (int j = 0; j < kLinTile / 4; ++j)
-            keep[j * kC] = make_float4(R[4 * j], R[4 * j + 1], R[4 * j + 2], R[4 * j + 3]);
-        } else if (r.fin && lin_is_last(p, w.x)) {
+            to[j * kC] = make_float4(R[4 * j], R[4 * j + 1], R[4 * j + 2], R[4 * j + 3]);
+        } else if (r.fin && w.x.to == kLinInit) {
           float* out = r.fin + (bh * r.a + row) * r.b + c0;
 #pragma unroll
           for (int j = 0; j < kLinTile; j += 4)
             if (j < nc) *reinterpret_cast<float4*>(out + j) = make_float4(R[j], R[j + 1], R[j + 2], R[j + 3]);
         }
       }
+      if (!kStateOnly && w.x.to == kLinHand && w.last_block() && w.last_head()) {  // every head's state is out
+        __threadfence();
+        ptx::named_bar_sync(3, 128);
+        if (ok && row == 0) ptx::st_release_gpu(p.flag + w.x.slot, 1u);
+      }
     }
   } else if (group == 2) {
-    ptx::regs_inc<120>();
+    if (kGrouped) ptx::regs_inc<120>();
+    else ptx::regs_dec<88>();
     if (!kStateOnly) {
     // ---- output -------------------------------------------------------------------------
     const int rot = row & 7;
@@ -541,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                   (size_t)blockIdx.x * (p.sub + p.hpg) * (kC * kLinTile / 4) + row;
     uint32_t it = 0;
     bool ok = true;
-    for (Walk w(p, false); ok && w.live(); w.next_run()) {
+    for (Walk w(p, false); w.live(); w.next_run()) {
       const LinProb& r = w.prob();
       const bool rev = w.rev;
       const float l2 = lin_log2_decay(p.log_a, w.head());
@@ -558,10 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
 #pragma unroll
           for (int j = 0; j < kLinTile / 4; ++j) sum[kGrouped ? j : 0] = sc[j * kC];
         }
-        if (!lin_wait_warp(&bars.o_full[bf], (it >> 1) & 1, p)) {
-          ok = false;
-          break;
-        }
+        ok = ok && lin_wait_warp(&bars.o_full[bf], (it >> 1) & 1, p);
         ptx::tc_fence_after();
         if (!kGrouped || last) {
           if (row == 0) ptx::bulk_wait_read_all();  // the previous tile has left the staging area
@@ -602,28 +683,31 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
                              pack_bf16(oa[8 * c + 4], oa[8 * c + 5]), pack_bf16(oa[8 * c + 6], oa[8 * c + 7]));
           }
         };
-        if (kGrouped) {
+        if (ok) {
+          if (kGrouped) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) quarter(q, sum + 4 * q);
-        } else {
+            for (int q = 0; q < 4; ++q) quarter(q, sum + 4 * q);
+          } else {
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) quarter(q, nullptr);
+            for (int q = 0; q < 4; ++q) quarter(q, nullptr);
+          }
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(&bars.o_empty[bf]);
         }
-        ptx::tc_fence_before();
-        ptx::mbar_arrive(&bars.o_empty[bf]);
         if (!kGrouped || last) {
           ptx::fence_proxy_async_smem();
           ptx::named_bar_sync(2, 128);
-          if (row == 0) {
+          if (ok && row == 0) {
             ptx::tma_store_4d(&maps.m[w.x.prob][3], stage, c0, w.x.oh, ch * kC, w.x.b);
             ptx::bulk_commit_group();
           }
         }
       }
       if (ok && last && w.last_block()) {  // chunks past the row's length: zeros
-        const int t1 = min(p.T, w.x.hi * kC);
+        int t0;
+        const int t1 = lin_past(p, w.x, w.chunks_valid(), &t0);
         const int n8 = min(kLinTile, r.b - c0) / 8;
-        for (int t = (w.lo + w.n) * kC + row; t < t1; t += kC) {
+        for (int t = t0 + row; t < t1; t += kC) {
           uint4* o = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(r.out) +
                                               (((size_t)w.x.b * p.T + t) * r.oh + w.x.oh) * r.b + c0);
           for (int c = 0; c < n8; ++c) o[c] = make_uint4(0u, 0u, 0u, 0u);
@@ -633,24 +717,25 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     if (row == 0) ptx::bulk_wait_read_all();
     }
   } else if (group == 3) {
-    ptx::regs_dec<64>();
+    ptx::regs_dec<kGrouped ? 64 : 80>();
     // ---- w Z: two threads a token, 32 columns each, 64 tokens at a time --------------------
     const int part = (row & 1) * 4;
     uint32_t it = 0;
+    Ring<KA> rg;
     bool ok = true;
     for (Walk w(p, kStateOnly); ok && w.live(); w.next_run()) {
       const bool rev = w.rev;
       const float l2 = lin_log2_decay(p.log_a, w.head());
-      for (; ok && w.k < w.k1; ++w.k, ++it) {
-        const uint32_t s = it % S::kStages;
+      rg.width(lin_blocks<KA>(w.prob()));
+      for (; ok && w.k < w.k1; ++w.k, ++it, rg.next()) {
         const int nv = w.valid();
-        ok = lin_wait_warp(&bars.z_full[s], (it / S::kStages) & 1, p);
+        ok = lin_wait_warp(&bars.z_full[rg.st], rg.phase(), p);
         // rows of Y past the row's length are overwritten below: after their copy has landed
-        if (ok && nv < kC) ok = lin_wait_warp(&bars.xy_full[s], (it / S::kStages) & 1, p);
+        if (ok && nv < kC) ok = lin_wait_warp(&bars.xy_full[rg.st], rg.phase(), p);
 #pragma unroll 1
         for (int half = 0; half < 2; ++half) {
           const int t = 64 * half + (row >> 1), rot = t & 7;
-          uint8_t* z0 = smem + s * S::kStage + 2 * S::kX + t * 128;
+          uint8_t* z0 = smem + rg.z() + t * 128;
           uint8_t* zhi = smem + S::kZt + t * 128;
           uint4 x[4];
 #pragma unroll
@@ -682,15 +767,14 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
           } else {
             // past the row's length: whatever the padding holds must not reach a product
             const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-            uint8_t* y0 = smem + s * S::kStage + S::kX + t * 128;
+            uint8_t* y0 = smem + rg.y() + t * 128;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
               const int off = (part + c) << 4;
               *reinterpret_cast<uint4*>(zhi + off) = zero;
               *reinterpret_cast<uint4*>(zhi + kZBytes + off) = zero;
               *reinterpret_cast<uint4*>(z0 + off) = zero;
-#pragma unroll
-              for (int d = 0; d < KA / 64; ++d) *reinterpret_cast<uint4*>(y0 + d * 16384 + off) = zero;
+              for (int d = 0; d < rg.ks; ++d) *reinterpret_cast<uint4*>(y0 + d * 16384 + off) = zero;
             }
           }
           ptx::fence_proxy_async_smem();
@@ -705,18 +789,26 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
   if (warp == 18) ptx::tmem_dealloc(tb, 512);
 }
 
-bool lin_map(CUtensorMap* m, const void* base, int inner, int count, int T, int B) {
-  return make_map(m, base, inner, count, T, B);
-}
-
 template <int KA, bool kStateOnly, bool kGrouped>
-cudaError_t launch_one(const LinArgs& p, const LinMaps& maps, int items, int ctas, cudaStream_t st) {
+cudaError_t launch_one(const LinArgs& p, const LinMaps& maps, int ctas, cudaStream_t st) {
   constexpr int smem = Lay<KA>::kBytes;
   static SmemLimit limit;
   cudaError_t e = limit.raise(lin_tc_kernel<KA, kStateOnly, kGrouped>, smem);
   if (e != cudaSuccess) return e;
-  lin_tc_kernel<KA, kStateOnly, kGrouped><<<min(ctas, items), kThreads, smem, st>>>(maps, p);
-  if ((e = cudaGetLastError()) == cudaSuccess) note_launch();
+  const bool wrapped = !kStateOnly && p.turn > 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(wrapped ? ctas : min(ctas, kStateOnly ? p.sitems : p.items));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  if (wrapped) {  // CTAs wait for one another: they have to run at the same time
+    at[0].id = cudaLaunchAttributeCooperative;
+    at[0].val.cooperative = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+  }
+  if ((e = cudaLaunchKernelEx(&cfg, lin_tc_kernel<KA, kStateOnly, kGrouped>, maps, p)) == cudaSuccess) note_launch();
   return e;
 }
 
@@ -725,30 +817,30 @@ cudaError_t launch_ka(const LinArgs& p, const LinMaps& maps, int ctas, cudaStrea
   cudaError_t e;
   bool grouped = false;
   for (int i = 0; i < p.nprob; ++i) grouped = grouped || p.pr[i].nh > 1;
-  if (p.nseg > 1) {
-    if ((e = launch_one<KA, true, false>(p, maps, p.sitems, ctas, st)) != cudaSuccess) return e;
+  if (p.turn > 0) {
+    if ((e = cudaMemsetAsync(p.flag, 0, ctas * sizeof(unsigned), st)) != cudaSuccess) return e;
+  } else if (p.nseg > 1) {
+    if ((e = launch_one<KA, true, false>(p, maps, ctas, st)) != cudaSuccess) return e;
     if ((e = launch_lin_scan(p, st)) != cudaSuccess) return e;
   }
-  return grouped ? launch_one<KA, false, true>(p, maps, p.items, ctas, st)
-                 : launch_one<KA, false, false>(p, maps, p.items, ctas, st);
+  return grouped ? launch_one<KA, false, true>(p, maps, ctas, st) : launch_one<KA, false, false>(p, maps, ctas, st);
 }
 
 }  // namespace
 
-bool lin_is_wide(int a) { return a > 64; }
-
-// Every scan of p pads a to the same width (64 or 128).
 cudaError_t launch_lin_tc(LinArgs& p, int ctas, cudaStream_t st) {
+  bool wide = false;
   LinMaps maps;
   for (int i = 0; i < p.nprob; ++i) {
     const LinProb& r = p.pr[i];
-    if (!lin_map(&maps.m[i][0], r.X, r.a, r.xh, p.T, p.B) || !lin_map(&maps.m[i][1], r.Y, r.a, r.yh, p.T, p.B) ||
-        !lin_map(&maps.m[i][2], r.Z, r.b, r.zh, p.T, p.B) || !lin_map(&maps.m[i][3], r.out, r.b, r.oh, p.T, p.B))
+    wide = wide || r.a > 64;
+    if (!make_map(&maps.m[i][0], r.X, r.a, r.xh, p.T, p.B) || !make_map(&maps.m[i][1], r.Y, r.a, r.yh, p.T, p.B) ||
+        !make_map(&maps.m[i][2], r.Z, r.b, r.zh, p.T, p.B) || !make_map(&maps.m[i][3], r.out, r.b, r.oh, p.T, p.B))
       return cudaErrorInvalidValue;
   }
   for (int i = p.nprob; i < kLinProbs; ++i)
     for (int j = 0; j < 4; ++j) maps.m[i][j] = maps.m[0][j];
-  return lin_is_wide(p.pr[0].a) ? launch_ka<128>(p, maps, ctas, st) : launch_ka<64>(p, maps, ctas, st);
+  return wide ? launch_ka<128>(p, maps, ctas, st) : launch_ka<64>(p, maps, ctas, st);
 }
 
 }  // namespace ll
