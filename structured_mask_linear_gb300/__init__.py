@@ -25,6 +25,7 @@ Functions mirror the C names:
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import threading
 from typing import NamedTuple, Optional
@@ -32,6 +33,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from ._build import LIB as _LIB_PATH
+from ._build import NATIVE as _NATIVE_PATH
 
 LL_OK = 0
 STATUS_NAMES = {0: "LL_OK", 1: "LL_ERR_NULL", 2: "LL_ERR_SHAPE", 3: "LL_ERR_DTYPE",
@@ -468,115 +470,31 @@ def loglinear_selftest_wait_timeout(spins: int, stream=None) -> None:
 
 
 # ---- linear attention with a decay per head ------------------------------------------------
-# These calls take a few microseconds on the GPU at their smallest, so the checks are kept
-# short: what follows from the sizes alone (the C shape, the sizes of the other tensors, the
-# workspace) is worked out once per combination of sizes.
-try:  # the current stream's handle without building a Stream object
-    _raw_stream = torch._C._cuda_getCurrentRawStream
-except AttributeError:
-    def _raw_stream(index):
-        return torch.cuda.current_stream(index).cuda_stream
+# These calls and the block norm's take a few microseconds on the GPU at their smallest, so
+# their arguments are checked and marshalled by a small CPython module (csrc/binding.cpp)
+# that calls the same C functions.
+_native_module = None
 
 
-def _bad(name, x, shape, dtype, index):
-    """Raises for a tensor that _ok refused."""
-    if x is None:
-        raise ValueError(f"{name} is required")
-    if x.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
-    if x.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(x.shape)}")
-    if x.get_device() != index:
-        raise ValueError(f"{name} is on {x.device}, the first tensor on CUDA device {index}")
-    raise ValueError(f"{name} must be contiguous")
-
-
-def _ok(x, shape, dtype, index):
-    return (x is not None and x.shape == shape and x.dtype is dtype and x.get_device() == index and
-            x.is_contiguous())
-
-
-def _cuda_index(x):
-    index = x.get_device()
-    if index < 0:
-        raise ValueError(f"tensors must be on a CUDA device, got {x.device}")
-    return index
-
-
-def _call(fn, index, stream, args, where):
-    """fn(*args, stream) with the CUDA device `index` current; raises on an error status."""
-    if torch.cuda.current_device() == index:
-        st = fn(*args, _raw_stream(index) if stream is None else _stream_ptr(stream))
-    else:
-        with torch.cuda.device(index):
-            st = fn(*args, _stream_ptr(stream))
-    if st != LL_OK:
-        raise LogLinearError(st, where)
-
-
-def _workspace(workspace, nbytes, index):
-    """The caller's workspace or a new one; (pointer, bytes)."""
-    if workspace is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=index)
-    if workspace.get_device() != index or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on CUDA device {index}")
-    return workspace
-
-
-class _LinPlan:
-    """What follows from the sizes of q and v alone."""
-
-    __slots__ = ("shape", "ref", "states", "heads", "rows", "fwd_bytes", "bwd_bytes")
-
-    def __init__(self, q, v, dtype, lead):
-        if len(q) != lead + 2 or len(v) != lead + 2:
-            raise ValueError(f"q and v must have {lead + 2} dimensions, got {len(q)} and {len(v)}")
-        (G, dk), (H, dv) = q[lead:], v[lead:]
-        if q[:lead] != v[:lead]:
-            raise ValueError(f"q and v must agree in their first {lead} sizes, got {tuple(q)} and {tuple(v)}")
-        if G == 0 or H % G:
-            raise ValueError(f"{H} heads do not divide into {G} groups")
-        self.shape = LLShape(q[0], q[1] if lead == 2 else 1, H, H // G, dk, dv, 0, 0, _dtype_code(dtype))
-        self.ref = ctypes.byref(self.shape)
-        self.states = torch.Size((q[0], H, dk, dv))
-        self.heads = torch.Size((H,))
-        self.rows = torch.Size((q[0],))
-        self.fwd_bytes = lindecay_fwd_workspace_bytes(self.shape)
-        self.bwd_bytes = lindecay_bwd_workspace_bytes(self.shape)
-        if self.fwd_bytes == 0:
-            raise LogLinearError(2, "lindecay")
-
-
-_lin_plans = {}
-
-
-def _lin_plan(q, v, dtype, lead):
-    key = (q, v, dtype, lead)
-    plan = _lin_plans.get(key)
-    if plan is None:
-        if len(_lin_plans) >= 4096:
-            _lin_plans.clear()
-        plan = _lin_plans[key] = _LinPlan(q, v, dtype, lead)
-    return plan
-
-
-def _lin_checked(q, k, v, log_a, lead):
-    """Checks q, k, v, log_a against each other; returns the plan and the CUDA device."""
-    shape, dtype, index = q.shape, q.dtype, _cuda_index(q)
-    plan = _lin_plan(shape, v.shape, dtype, lead)
-    if not (_ok(k, shape, dtype, index) and _ok(v, v.shape, dtype, index) and q.is_contiguous() and
-            _ok(log_a, plan.heads, torch.float32, index)):
-        for name, x, want, dt in (("q", q, shape, dtype), ("k", k, shape, dtype), ("v", v, v.shape, dtype),
-                                  ("log_a", log_a, plan.heads, torch.float32)):
-            if not _ok(x, want, dt, index):
-                _bad(name, x, want, dt, index)
-    return plan, index
-
-
-def _lin_states(plan, index, **states):
-    for name, x in states.items():
-        if x is not None and not _ok(x, plan.states, torch.float32, index):
-            _bad(name, x, plan.states, torch.float32, index)
+def _native():
+    """The loaded module, bound to the library (raises if it has not been built)."""
+    global _native_module
+    if _native_module is not None:
+        return _native_module
+    L = lib()
+    with _lock:
+        if _native_module is None:
+            if not os.path.exists(_NATIVE_PATH):
+                raise RuntimeError(f"{_NATIVE_PATH} is missing: run __graft_entry__.build() "
+                                   "(or python -m structured_mask_linear_gb300._build)")
+            spec = importlib.util.spec_from_file_location("_native", _NATIVE_PATH)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            names = ("lindecay_fwd", "lindecay_fwd_workspace_bytes", "lindecay_bwd", "lindecay_bwd_workspace_bytes",
+                     "lindecay_decode_step", "blocknorm_fwd", "blocknorm_bwd", "blocknorm_bwd_workspace_bytes")
+            module.bind(tuple(ctypes.cast(getattr(L, n), _vp).value for n in names), LogLinearError)
+            _native_module = module
+    return _native_module
 
 
 def lindecay_fwd_workspace_bytes(shape: LLShape) -> int:
@@ -592,54 +510,23 @@ def lindecay_fwd(q, k, v, log_a, lengths=None, state_in=None, state_out=None, o=
     v: (B, T, H, d_v), bf16 or fp32; log_a: (H,) fp32.  lengths: (B,) int32 tokens per row;
     state_in, state_out: (B, H, d_k, d_v) fp32 states before the first and after the last
     token (state_out is written; it may be state_in)."""
-    plan, index = _lin_checked(q, k, v, log_a, 2)
-    if lengths is not None and not _ok(lengths, plan.rows, torch.int32, index):
-        _bad("lengths", lengths, plan.rows, torch.int32, index)
-    _lin_states(plan, index, state_in=state_in, state_out=state_out)
-    if o is None:
-        o = torch.empty_like(v)
-    elif not _ok(o, v.shape, v.dtype, index):
-        _bad("o", o, v.shape, v.dtype, index)
-    ws = _workspace(workspace, plan.fwd_bytes, index)
-    _call(lib().lindecay_fwd, index, stream,
-          (plan.ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), _ptr(lengths), _ptr(state_in),
-           o.data_ptr(), _ptr(state_out), ws.data_ptr(), ws.numel() * ws.element_size()), "lindecay_fwd")
-    return o
+    return (_native_module or _native()).lindecay_fwd(q, k, v, log_a, lengths, state_in, state_out, o, workspace,
+                                                      None if stream is None else _stream_ptr(stream))
 
 
 def lindecay_bwd(q, k, v, log_a, dO, lengths=None, state_in=None, dstate_out=None, dstate_in=None, workspace=None,
                  stream=None):
     """Gradients of sum(dO * o) + sum(dstate_out * state_out) of lindecay_fwd: returns dq, dk
     (B, T, G, d_k) and dv (B, T, H, d_v); dstate_in, where given, receives state_in's."""
-    plan, index = _lin_checked(q, k, v, log_a, 2)
-    if not _ok(dO, v.shape, v.dtype, index):
-        _bad("dO", dO, v.shape, v.dtype, index)
-    if lengths is not None and not _ok(lengths, plan.rows, torch.int32, index):
-        _bad("lengths", lengths, plan.rows, torch.int32, index)
-    _lin_states(plan, index, state_in=state_in, dstate_out=dstate_out, dstate_in=dstate_in)
-    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    ws = _workspace(workspace, plan.bwd_bytes, index)
-    _call(lib().lindecay_bwd, index, stream,
-          (plan.ref, q.data_ptr(), k.data_ptr(), v.data_ptr(), log_a.data_ptr(), _ptr(lengths), _ptr(state_in),
-           dO.data_ptr(), _ptr(dstate_out), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), _ptr(dstate_in),
-           ws.data_ptr(), ws.numel() * ws.element_size()), "lindecay_bwd")
-    return dq, dk, dv
+    return (_native_module or _native()).lindecay_bwd(q, k, v, log_a, dO, lengths, state_in, dstate_out, dstate_in,
+                                                      workspace, None if stream is None else _stream_ptr(stream))
 
 
 def lindecay_decode_step(q_t, k_t, v_t, log_a, states, o_t=None, stream=None):
     """One token: q_t, k_t (B, G, d_k); v_t (B, H, d_v); states (B, H, d_k, d_v) fp32, updated
     in place.  Returns o_t (B, H, d_v)."""
-    plan, index = _lin_checked(q_t, k_t, v_t, log_a, 1)
-    if not _ok(states, plan.states, torch.float32, index):
-        _bad("states", states, plan.states, torch.float32, index)
-    if o_t is None:
-        o_t = torch.empty_like(v_t)
-    elif not _ok(o_t, v_t.shape, v_t.dtype, index):
-        _bad("o_t", o_t, v_t.shape, v_t.dtype, index)
-    _call(lib().lindecay_decode_step, index, stream,
-          (plan.ref, q_t.data_ptr(), k_t.data_ptr(), v_t.data_ptr(), log_a.data_ptr(), o_t.data_ptr(),
-           states.data_ptr()), "lindecay_decode_step")
-    return o_t
+    return (_native_module or _native()).lindecay_decode_step(q_t, k_t, v_t, log_a, states, o_t,
+                                                              None if stream is None else _stream_ptr(stream))
 
 
 # ---- norms around a block ------------------------------------------------------------------
@@ -657,46 +544,11 @@ class BlocknormGrads(NamedTuple):
     dw_pre: Optional[torch.Tensor]
 
 
-class _BnPlan:
-    """What follows from the sizes and options of a block norm alone."""
-
-    __slots__ = ("shape", "ref", "weights", "bwd_bytes")
-
-    def __init__(self, size, dtype, group, act, eps):
-        code = _dtype_code(dtype)
-        if not size or 0 in size:
-            raise ValueError(f"activations must hold at least one row, got shape {tuple(size)}")
-        if act not in ACTS:
-            raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
-        D = size[-1]
-        self.shape = BlocknormShape(size.numel() // D, D, D if group is None else int(group), ACTS[act], eps, code)
-        self.ref = ctypes.byref(self.shape)
-        self.weights = torch.Size((D,))
-        self.bwd_bytes = int(lib().blocknorm_bwd_workspace_bytes(self.ref))
-        if self.bwd_bytes == 0:
-            raise LogLinearError(2, "blocknorm")
-
-
-_bn_plans = {}
-
-
-def _bn_checked(first, acts, weights, group, act, eps):
-    """Checks activations against `first` and weights against its last size ((name, tensor or
-    None) pairs); returns the plan and the CUDA device."""
-    size, dtype, index = first.shape, first.dtype, _cuda_index(first)
-    key = (size, dtype, group, act, eps)
-    plan = _bn_plans.get(key)
-    if plan is None:
-        if len(_bn_plans) >= 4096:
-            _bn_plans.clear()
-        plan = _bn_plans[key] = _BnPlan(size, dtype, group, act, eps)
-    for name, x in acts:
-        if x is not None and not _ok(x, size, dtype, index):
-            _bad(name, x, size, dtype, index)
-    for name, x in weights:
-        if x is not None and not _ok(x, plan.weights, torch.float32, index):
-            _bad(name, x, plan.weights, torch.float32, index)
-    return plan, index
+def _act_code(act):
+    code = ACTS.get(act)
+    if code is None:
+        raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
+    return code
 
 
 def blocknorm_fwd(y=None, w_post=None, x=None, gate=None, scale=None, w_pre=None, group=None, act="silu", eps=1e-6,
@@ -705,24 +557,8 @@ def blocknorm_fwd(y=None, w_post=None, x=None, gate=None, scale=None, w_pre=None
     pass; returns (x', h).  Activations (..., D) in bf16 or fp32, weights (D,) fp32.  Without x,
     x' is the gated norm alone; h is computed where w_pre is given (else None); without y,
     x' is x."""
-    first = y if y is not None else x
-    if first is None:
-        raise ValueError("y or x is required")
-    plan, index = _bn_checked(first, (("y", y), ("x", x), ("gate", gate), ("x_new", x_new), ("h", h)),
-                              (("w_post", w_post), ("scale", scale), ("w_pre", w_pre)), group, act, eps)
-    if y is None:
-        if x_new is not None or gate is not None or w_post is not None or scale is not None:
-            raise ValueError("without y there is no x_new, gate, w_post or scale")
-        if w_pre is None and h is None:
-            raise ValueError("nothing to compute: neither y nor w_pre is given")
-    elif x_new is None:
-        x_new = torch.empty_like(y)
-    if h is None and w_pre is not None:
-        h = torch.empty_like(first)
-    _call(lib().blocknorm_fwd, index, stream,
-          (plan.ref, _ptr(x), _ptr(y), _ptr(gate), _ptr(w_post), _ptr(scale), _ptr(w_pre), _ptr(x_new), _ptr(h)),
-          "blocknorm_fwd")
-    return (x if y is None else x_new), h
+    return (_native_module or _native()).blocknorm_fwd(y, w_post, x, gate, scale, w_pre, group, _act_code(act), eps,
+                                                       x_new, h, None if stream is None else _stream_ptr(stream))
 
 
 def blocknorm_bwd(dx_new, y=None, w_post=None, dh=None, x_new=None, gate=None, scale=None, w_pre=None, group=None,
@@ -730,22 +566,6 @@ def blocknorm_bwd(dx_new, y=None, w_post=None, dh=None, x_new=None, gate=None, s
     """Gradients of sum(dx_new * x') + sum(dh * h) of blocknorm_fwd, from its x' (x_new, with
     dh) and its inputs; dx_new or dh may be None (zero).  dx is returned where the forward
     had a residual input x (`residual`; by default taken from scale or x_new being given)."""
-    first = dx_new if dx_new is not None else dh
-    if first is None:
-        raise ValueError("dx_new or dh is required")
-    if (dh is None) != (x_new is None):
-        raise ValueError("dh and x_new go together")
-    plan, index = _bn_checked(first, (("dx_new", dx_new), ("dh", dh), ("x_new", x_new), ("y", y), ("gate", gate)),
-                              (("w_post", w_post), ("scale", scale), ("w_pre", w_pre)), group, act, eps)
-    if residual is None:
-        residual = y is None or scale is not None or x_new is not None
-    like = torch.empty_like
-    g = BlocknormGrads(like(first) if residual else None, None if y is None else like(y),
-                       None if gate is None else like(gate), None if w_post is None else like(w_post),
-                       None if scale is None else like(scale), None if w_pre is None else like(w_pre))
-    ws = _workspace(workspace, plan.bwd_bytes, index)
-    _call(lib().blocknorm_bwd, index, stream,
-          (plan.ref, _ptr(dx_new), _ptr(dh), _ptr(x_new), _ptr(y), _ptr(gate), _ptr(w_post), _ptr(scale),
-           _ptr(w_pre), _ptr(g.dx), _ptr(g.dy), _ptr(g.dgate), _ptr(g.dw_post), _ptr(g.dscale), _ptr(g.dw_pre),
-           ws.data_ptr(), ws.numel() * ws.element_size()), "blocknorm_bwd")
-    return g
+    return BlocknormGrads(*(_native_module or _native()).blocknorm_bwd(
+        dx_new, y, w_post, dh, x_new, gate, scale, w_pre, group, _act_code(act), eps,
+        None if residual is None else bool(residual), workspace, None if stream is None else _stream_ptr(stream)))

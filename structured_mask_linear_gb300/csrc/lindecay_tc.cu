@@ -44,7 +44,7 @@ namespace {
 constexpr int kThreads = 640;
 constexpr int kC = kLinChunk;
 constexpr int kZBytes = kC * kLinTile * 2;  // 16 KB: 128 tokens x 64 columns, bf16
-constexpr int kMisc = 1024;
+constexpr int kMisc = 1280;     // barriers, P's table
 
 template <int KA>
 struct Lay {
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Bars& bars = *reinterpret_cast<Bars*>(smem + S::kMiscOff);
-  float* s_cf = reinterpret_cast<float*>(smem + S::kMiscOff + 512);  // 32
+  float* s_pow = reinterpret_cast<float*>(smem + S::kMiscOff + 512) + 32;  // g^d, d = -32 .. 127 (0 below 0)
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // uniform to the compiler too
   const int row = tid & 127, quad = warp & 3;
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     }
   }
   } else if (group == 0) {
-    ptx::regs_inc<104>();
+    ptx::regs_inc<96>();
     if (!kStateOnly) {
     // ---- P ------------------------------------------------------------------------------
     uint32_t it = 0;
@@ -431,20 +431,13 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
       if (w.k0 == w.k1) continue;
       const bool rev = w.rev;
       const float l2 = lin_log2_decay(p.log_a, w.head());
-      // Weights g^|i-j| of row i = 32 quad + lane.  Against its own 32-group of keys: in
-      // registers, 0 where the lag is negative.  Against a group behind it in scan order:
-      // the product of a factor of the row and group (up to the group's nearest key) and one
-      // of the key (from there, s_cf), both <= 1.
-      float2 wd[16];
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const int d0 = rev ? 2 * j - lane : lane - 2 * j, d1 = rev ? d0 + 1 : d0 - 1;
-        wd[j] = make_float2(d0 < 0 ? 0.f : exp2f(l2 * (float)d0), d1 < 0 ? 0.f : exp2f(l2 * (float)d1));
-      }
+      // Weights g^|i-j| from a table over lags: row i = 32 quad + lane against key j of group cg
+      // reads entry 32 back + (lane - j), 0 where the lag is negative; a warp's lanes read 32
+      // entries in a row.
       ptx::named_bar_sync(1, 128);
-      if (quad == 0) s_cf[lane] = exp2f(l2 * (float)(rev ? lane : 31 - lane));
+      s_pow[row] = exp2f(l2 * (float)row);
+      if (row < 32) s_pow[row - 32] = 0.f;
       ptx::named_bar_sync(1, 128);
-      const float g32 = exp2f(l2 * 32.f), near = exp2f(l2 * (float)(rev ? 32 - lane : lane + 1));
       for (; w.k < w.k1; ++w.k, ++it) {
         const uint32_t bf = it & 1;
         const int nv = w.valid();
@@ -457,29 +450,26 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
         // read before it is written.
 #pragma unroll 1
         for (int cg = 0; cg < 4; ++cg) {
-          float2 sv[16];
           uint32_t pk[16];
           const int back = rev ? cg - quad : quad - cg;  // 32-groups behind the row's own
           if (back >= 0) {
+            float2 sv[16];
             ptx::tmem_ld32(ts + 32 * cg, reinterpret_cast<float*>(sv));
-            if (back == 0) {
-              ptx::tmem_ld_wait();
+            const float* t = s_pow + 32 * back + (rev ? -lane : lane);
+            float2 wt[16];
+            if (rev) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) sv[j] = ptx::mul2(sv[j], wd[j]);
+              for (int j = 0; j < 16; ++j) wt[j] = make_float2(t[2 * j], t[2 * j + 1]);
             } else {
-              float f = near;
-              for (int i = 1; i < back; ++i) f *= g32;
-              const float4* c4 = reinterpret_cast<const float4*>(s_cf);
-              ptx::tmem_ld_wait();
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const float4 c = c4[j];
-                sv[2 * j] = ptx::mul2(sv[2 * j], ptx::mul2(make_float2(f, f), make_float2(c.x, c.y)));
-                sv[2 * j + 1] = ptx::mul2(sv[2 * j + 1], ptx::mul2(make_float2(f, f), make_float2(c.z, c.w)));
-              }
+              for (int j = 0; j < 16; ++j) wt[j] = make_float2(t[-2 * j], t[-2 * j - 1]);
             }
+            ptx::tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) pk[j] = pack_bf16(sv[j].x, sv[j].y);
+            for (int j = 0; j < 16; ++j) {
+              sv[j] = ptx::mul2(sv[j], wt[j]);
+              pk[j] = pack_bf16(sv[j].x, sv[j].y);
+            }
             if (nv < 32 * cg + 32) {  // keys past the row's length (warp-uniform): P = 0
               const int keep = nv - 32 * cg;
 #pragma unroll
@@ -615,8 +605,8 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
       }
     }
   } else if (group == 2) {
-    if (kGrouped) ptx::regs_inc<120>();
-    else ptx::regs_dec<88>();
+    if (kGrouped) ptx::regs_inc<128>();
+    else ptx::regs_inc<96>();
     if (!kStateOnly) {
     // ---- output -------------------------------------------------------------------------
     const int rot = row & 7;
