@@ -1,9 +1,10 @@
-// CUDA-core kernels of the linear attention with a decay per head (the scan of
-// lindecay.cuh): the prefix over segment totals, the fp32 scan, and the single-token step.
+// Kernels of the linear attention with a decay per head (the scan of lindecay.cuh) beside the
+// tensor-core one: the prefix over segment totals, the fp32 scan, the single-token step.
 #include <cuda_runtime.h>
 
 #include "launch_util.cuh"
 #include "lindecay.cuh"
+#include "ptx.cuh"
 
 namespace ll {
 
@@ -67,28 +68,85 @@ __global__ void __launch_bounds__(256) lin_scan_kernel(const __grid_constant__ L
 }
 
 // ---------------------------------------------------------------------------------
-// lin_f32: the scan in fp32, one CTA per unit (a head's 64 output columns, or those of a
-// whole group, over one segment), 64-token chunks.  X and Z sit in shared memory by token,
-// Y transposed, R by row; the four products of a chunk run on the CUDA cores from there.
+// lin_f32: the scan in fp32, one CTA per item (a head's 64 output columns, or those of a
+// whole group, over a unit or a segment), 64-token chunks in two buffers filled by cp.async.
+//
+// The products need fp32's accuracy, which the tensor cores give in three steps: a value is
+// split into its first 11 significant bits (hi) and the rest (lo, exact, of which 11 bits
+// enter), and a b = hi_a hi_b + hi_a lo_b + lo_a hi_b is accumulated in fp32; what is left
+// out is of the order of 2^-22 |a b|.  The operands lie in shared memory as fp32 (tcgen05
+// would need them there in 16 or 11 bits, both parts: twice the space) and are split in
+// registers, so the warp-level instruction (m16n8k8) is used.
+//
+// Tile strides make the fragment loads free of bank conflicts: 4 mod 32 for operands that
+// run along a row with k, 8 mod 32 for those that run along a row with n.
 // ---------------------------------------------------------------------------------
 constexpr int kF = 256;
 constexpr int kC32 = kLinChunk32;
-constexpr int kLd = 68;  // row stride of 64-wide tiles
+constexpr int kLdX = 132, kLdZ = 72, kLdP = 68;
 struct F32Smem {
-  float Yt[128 * kLd];
-  float R[128 * kLd];
-  float X[kC32 * 132];
-  float Z[kC32 * kLd];
-  float Zw[kC32 * kLd];
-  float P[kC32 * kLd];
+  float X[2][kC32 * kLdX];
+  float Y[2][kC32 * kLdX];
+  float Z[2][kC32 * kLdZ];
+  float R[128 * kLdZ];
+  float P[kC32 * kLdP];
   float pw[kC32 + 1];  // g^d
+};
+
+// x = hi + lo: hi is x rounded to tf32's 11 significant bits.
+__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
+  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+               "{%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
+}
+// acc (16 x 32, four n-tiles of 8) += A B over k = k0 .. k1 - 1 (multiples of 8), by one warp:
+// A(m, k) = a[m sam + k sak], B(k, n) = b[k sbk + n sbn] wk(k).
+template <typename W>
+__device__ __forceinline__ void warp_mma(float (&acc)[4][4], const float* a, int sam, int sak, const float* b, int sbk,
+                                         int sbn, int k0, int k1, W wk) {
+  const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+  // The instruction's own accumulation truncates: at most four steps add up in it before
+  // they are added to acc in fp32 arithmetic.
+  for (int kb = k0; kb < k1; kb += 32) {
+    float part[4][4] = {};
+    const int ke = min(kb + 32, k1);
+#pragma unroll 2
+    for (int k = kb; k < ke; k += 8) {
+      uint32_t ah[4], al[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) split_tf32(a[(g + 8 * (i & 1)) * sam + (k + t + 4 * (i >> 1)) * sak], ah[i], al[i]);
+      const float w0 = wk(k + t), w1 = wk(k + t + 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t bh[2], bl[2];
+        split_tf32(w0 * b[(k + t) * sbk + (8 * j + g) * sbn], bh[0], bl[0]);
+        split_tf32(w1 * b[(k + t + 4) * sbk + (8 * j + g) * sbn], bh[1], bl[1]);
+        mma_tf32(part[j], al, bh);
+        mma_tf32(part[j], ah, bl);
+        mma_tf32(part[j], ah, bh);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[j][e] += part[j][e];
+  }
+}
+struct NoWeight {
+  __device__ __forceinline__ float operator()(int) const { return 1.f; }
 };
 
 template <bool kStateOnly>
 __global__ void __launch_bounds__(kF, 1) lin_f32_kernel(const __grid_constant__ LinArgs p) {
   extern __shared__ float4 smem4[];
   F32Smem& sm = *reinterpret_cast<F32Smem*>(smem4);
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, warp = tid >> 5, g = (tid & 31) >> 2, t4 = tid & 3;
+  const int wm = (warp & 3) * 16, wn = (warp >> 2) * 32;  // this warp's part of a 64 x 64 tile
   int head0 = 0;
   const LinItem x =
       kStateOnly ? lin_state_item(p, (int)blockIdx.x, &head0) : lin_item(p, (int)blockIdx.x);
@@ -96,7 +154,6 @@ __global__ void __launch_bounds__(kF, 1) lin_f32_kernel(const __grid_constant__ 
   const bool rev = r.rev != 0;
   const int sh = rev ? 0 : 1;
   const int a = r.a, b = r.b, c0 = kLinTile * x.tile, nc = min(kLinTile, b - c0);
-  const int ldx = a + 4;
   const int len = lin_len(p, x.b), cv = (len + kC32 - 1) / kC32;
   int first, step;
   const int n = lin_visit(p, x, cv, &first, &step);
@@ -105,117 +162,136 @@ __global__ void __launch_bounds__(kF, 1) lin_f32_kernel(const __grid_constant__ 
   const float* Zg = static_cast<const float*>(r.Z);
   float* out = static_cast<float*>(r.out);
   for (int hi_h = head0; hi_h < (kStateOnly ? head0 + 1 : r.nh); ++hi_h) {
-    const int h = x.oh * r.nh + hi_h, g = h / p.hpg;
-    const int hx = r.xh == p.H ? h : g, hy = r.yh == p.H ? h : g, hz = r.zh == p.H ? h : g;
+    const int h = x.oh * r.nh + hi_h, grp = h / p.hpg;
+    const int hx = r.xh == p.H ? h : grp, hy = r.yh == p.H ? h : grp, hz = r.zh == p.H ? h : grp;
     const size_t bh = (size_t)x.b * p.H + h;
     const float l2 = lin_log2_decay(p.log_a, h);
     float* seg = kStateOnly || x.from == kLinSeg ? lin_seg(p, x, hi_h) : nullptr;
-    __syncthreads();
-    for (int e = tid; e < a * kLinTile; e += kF) {
-      const int i = e / kLinTile, j = e % kLinTile;
-      float v = 0.f;
-      if (!kStateOnly) {
-        if (seg) v = seg[e];
-        else if (r.init && j < nc) v = r.init[bh * a * b + (size_t)i * r.init_rs + (size_t)(c0 + j) * r.init_cs];
-      }
-      sm.R[i * kLd + j] = v;
-    }
-    if (tid <= kC32) sm.pw[tid] = exp2f(l2 * (float)tid);
-    for (int k = 0; k < n; ++k) {
+    // rows of X, Y, Z of one chunk, by cp.async; zeros past the row's length (whatever lies
+    // there must not reach a product) and past Z's columns
+    auto load = [&](int k, int s) {
       const int ch = first + step * k;
       const int nv = min(kC32, len - ch * kC32);
       const size_t t0 = (size_t)x.b * p.T + (size_t)ch * kC32;
-      __syncthreads();
-      const float4 zero4 = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (!kStateOnly)
-        for (int e = tid; e < kC32 * (a / 4); e += kF) {
-          const int t = e / (a / 4), c = e % (a / 4) * 4;
-          *reinterpret_cast<float4*>(sm.X + t * ldx + c) =
-              t < nv ? *reinterpret_cast<const float4*>(Xg + ((t0 + t) * r.xh + hx) * a + c) : zero4;
+      const int a4 = a / 4;
+      for (int e = tid; e < kC32 * a4; e += kF) {
+        const int t = e / a4, c = e % a4 * 4;
+        float* y = sm.Y[s] + t * kLdX + c;
+        float* xx = sm.X[s] + t * kLdX + c;
+        if (t < nv) {
+          ptx::cp_async16(y, Yg + ((t0 + t) * r.yh + hy) * a + c);
+          if (!kStateOnly) ptx::cp_async16(xx, Xg + ((t0 + t) * r.xh + hx) * a + c);
+        } else {
+          *reinterpret_cast<float4*>(y) = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (!kStateOnly) *reinterpret_cast<float4*>(xx) = make_float4(0.f, 0.f, 0.f, 0.f);
         }
-      for (int e = tid; e < kC32 * (a / 4); e += kF) {
-        const int t = e % kC32, c = e / kC32 * 4;
-        const float4 y = t < nv ? *reinterpret_cast<const float4*>(Yg + ((t0 + t) * r.yh + hy) * a + c) : zero4;
-        sm.Yt[c * kLd + t] = y.x;
-        sm.Yt[(c + 1) * kLd + t] = y.y;
-        sm.Yt[(c + 2) * kLd + t] = y.z;
-        sm.Yt[(c + 3) * kLd + t] = y.w;
       }
       for (int e = tid; e < kC32 * (kLinTile / 4); e += kF) {
         const int t = e / (kLinTile / 4), c = e % (kLinTile / 4) * 4;
-        const float4 z =
-            (t < nv && c < nc) ? *reinterpret_cast<const float4*>(Zg + ((t0 + t) * r.zh + hz) * b + c0 + c) : zero4;
-        const float w = t < nv ? sm.pw[rev ? t + 1 : nv - 1 - t] : 0.f;
-        *reinterpret_cast<float4*>(sm.Z + t * kLd + c) = z;
-        *reinterpret_cast<float4*>(sm.Zw + t * kLd + c) = make_float4(w * z.x, w * z.y, w * z.z, w * z.w);
+        float* z = sm.Z[s] + t * kLdZ + c;
+        if (t < nv && c < nc) ptx::cp_async16(z, Zg + ((t0 + t) * r.zh + hz) * b + c0 + c);
+        else *reinterpret_cast<float4*>(z) = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      ptx::cp_async_commit();
+    };
+    __syncthreads();
+    if (n > 0) load(0, 0);
+    // R, rows a .. up to a multiple of 16 zero; and the columns of X and Y up to one of 8 are
+    // all there (a is one)
+    for (int e = tid; e < 128 * kLinTile; e += kF) {
+      const int i = e / kLinTile, j = e % kLinTile;
+      float v = 0.f;
+      if (!kStateOnly && i < a) {
+        if (seg) v = seg[e];
+        else if (r.init && j < nc) v = r.init[bh * a * b + (size_t)i * r.init_rs + (size_t)(c0 + j) * r.init_cs];
+      }
+      sm.R[i * kLdZ + j] = v;
+    }
+    if (tid <= kC32) sm.pw[tid] = exp2f(l2 * (float)tid);
+    for (int k = 0; k < n; ++k) {
+      const int s = k & 1, ch = first + step * k;
+      const int nv = min(kC32, len - ch * kC32);
+      const size_t t0 = (size_t)x.b * p.T + (size_t)ch * kC32;
+      if (k + 1 < n) {
+        load(k + 1, s ^ 1);
+        ptx::cp_async_wait_group<1>();
+      } else {
+        ptx::cp_async_wait_group<0>();
       }
       __syncthreads();
+      const float *X = sm.X[s], *Y = sm.Y[s], *Z = sm.Z[s];
+      float acc[4][4];
+      auto clear = [&]() {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+      };
       if (!kStateOnly) {
-        smem_mm(kC32, kC32, a, sm.X, ldx, 1, sm.Yt, kLd, tid, kF, [&](int m0, int n0, float(&acc)[4][4]) {
+        clear();
+        // S, only where some key of the warp's 16 x 32 part counts
+        const bool some = rev ? wn + 31 >= wm : wn <= wm + 15;
+        if (some) warp_mma(acc, X + wm * kLdX, kLdX, 1, Y + wn * kLdX, 1, kLdX, 0, a, NoWeight());
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float4 v;
-            float* o = &v.x;
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int d = rev ? n0 + j - m0 - i : m0 + i - n0 - j;
-              o[j] = d >= 0 ? acc[i][j] * sm.pw[d] : 0.f;
+          for (int e = 0; e < 4; ++e) {
+            const int row = wm + g + 8 * (e >> 1), col = wn + 8 * j + 2 * t4 + (e & 1);
+            const int d = rev ? col - row : row - col;
+            sm.P[row * kLdP + col] = d >= 0 ? acc[j][e] * sm.pw[d] : 0.f;
+          }
+        // X R, its rows scaled, then P Z on top
+        clear();
+        warp_mma(acc, X + wm * kLdX, kLdX, 1, sm.R + wn, kLdZ, 1, 0, a, NoWeight());
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int row = wm + g + 8 * (e >> 1);
+          const float w = row < nv ? sm.pw[rev ? nv - 1 - row : row + sh] : 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[j][e] *= w;
+        }
+        __syncthreads();  // P complete; R has been read
+        warp_mma(acc, sm.P + wm * kLdP, kLdP, 1, Z + wn, kLdZ, 1, rev ? wm : 0, rev ? kC32 : wm + 16, NoWeight());
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int t = wm + g + 8 * e, col = wn + 8 * j + 2 * t4;
+            if (ch * kC32 + t >= p.T || col >= nc) continue;
+            float2* o = reinterpret_cast<float2*>(out + ((t0 + t) * r.oh + x.oh) * b + c0 + col);
+            float2 v = t < nv ? make_float2(acc[j][2 * e], acc[j][2 * e + 1]) : make_float2(0.f, 0.f);
+            if (hi_h > 0) {  // heads of the group add up, in order
+              const float2 y = *o;
+              v = make_float2(v.x + y.x, v.y + y.y);
             }
-            *reinterpret_cast<float4*>(sm.P + (m0 + i) * kLd + n0) = v;
+            *o = v;
           }
-        });
-        // X R: the 16 x 16 output tiles are one per thread, the same one in both products
-        float it[4][4];
-        smem_mm(kC32, kLinTile, a, sm.X, ldx, 1, sm.R, kLd, tid, kF, [&](int m0, int, float(&acc)[4][4]) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int t = m0 + i;
-            const float w = t < nv ? sm.pw[rev ? nv - 1 - t : t + sh] : 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) it[i][j] = w * acc[i][j];
-          }
-        });
-        __syncthreads();
-        smem_mm_r(
-            kC32, kLinTile, kC32, sm.P, kLd, 1, sm.Z, kLd, tid, kF,
-            [&](int m0, int, int& kb, int& ke) {
-              if (rev) kb = m0;
-              else ke = m0 + 4;
-            },
-            [&](int m0, int n0, float(&acc)[4][4]) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int t = m0 + i;
-                if (ch * kC32 + t >= p.T || n0 >= nc) continue;
-                float4* o = reinterpret_cast<float4*>(out + ((t0 + t) * r.oh + x.oh) * b + c0 + n0);
-                float4 v = t < nv ? make_float4(acc[i][0] + it[i][0], acc[i][1] + it[i][1], acc[i][2] + it[i][2],
-                                                acc[i][3] + it[i][3])
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
-                if (hi_h > 0) {  // heads of the group add up, in order
-                  const float4 y = *o;
-                  v = make_float4(v.x + y.x, v.y + y.y, v.z + y.z, v.w + y.w);
-                }
-                *o = v;
-              }
-            });
       }
+      // R <- g^nv R + Yᵀ (w Z), 16 x 32 parts handed out to the warps
       const float dec = sm.pw[nv];
-      smem_mm(a, kLinTile, kC32, sm.Yt, kLd, 1, sm.Zw, kLd, tid, kF, [&](int m0, int n0, float(&acc)[4][4]) {
+      const float* pw = sm.pw;
+      auto wz = [&](int t) { return t < nv ? pw[rev ? t + 1 : nv - 1 - t] : 0.f; };
+      for (int tile = warp; tile < (a + 15) / 16 * 2; tile += kF / 32) {
+        const int m0 = (tile >> 1) * 16, n0 = (tile & 1) * 32;
+        float* R = sm.R + (m0 + g) * kLdZ + n0 + 2 * t4;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float& R = sm.R[(m0 + i) * kLd + n0 + j];
-            R = dec * R + acc[i][j];
-          }
-      });
+          for (int e = 0; e < 4; ++e) acc[j][e] = dec * R[8 * (e >> 1) * kLdZ + 8 * j + (e & 1)];
+        warp_mma(acc, Y + m0, 1, kLdX, Z + n0, kLdZ, 1, 0, kC32, wz);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) R[8 * (e >> 1) * kLdZ + 8 * j + (e & 1)] = acc[j][e];
+      }
+      __syncthreads();  // the buffers are free, R is complete
     }
     __syncthreads();
     if (kStateOnly) {
-      for (int e = tid; e < a * kLinTile; e += kF) seg[e] = sm.R[e / kLinTile * kLd + e % kLinTile];
+      for (int e = tid; e < a * kLinTile; e += kF) seg[e] = sm.R[e / kLinTile * kLdZ + e % kLinTile];
     } else if (r.fin && x.to == kLinInit) {
       for (int e = tid; e < a * nc; e += kF)
-        r.fin[(bh * a + e / nc) * b + c0 + e % nc] = sm.R[e / nc * kLd + e % nc];
+        r.fin[(bh * a + e / nc) * b + c0 + e % nc] = sm.R[e / nc * kLdZ + e % nc];
     }
   }
   if (!kStateOnly) {  // chunks past the row's length: zeros
