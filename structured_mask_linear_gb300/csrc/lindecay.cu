@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(256) lin_scan_kernel(const __grid_constant__ L
 // Tile strides make the fragment loads free of bank conflicts: 4 mod 32 for operands that
 // run along a row with k, 8 mod 32 for those that run along a row with n.
 // ---------------------------------------------------------------------------------
-constexpr int kF = 256;
+constexpr int kF = 512;
 constexpr int kC32 = kLinChunk32;
 constexpr int kLdX = 132, kLdZ = 72, kLdP = 68;
 struct F32Smem {
@@ -99,40 +99,44 @@ __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) 
   lo = __float_as_uint(x - __uint_as_float(hi));
 }
 __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
                "{%0, %1, %2, %3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
-// acc (16 x 32, four n-tiles of 8) += A B over k = k0 .. k1 - 1 (multiples of 8), by one warp:
+// acc (16 x 16, two n-tiles of 8) += A B over k = k0 .. k1 - 1 (multiples of 8), by one warp:
 // A(m, k) = a[m sam + k sak], B(k, n) = b[k sbk + n sbn] wk(k).
+constexpr int kNt = 2;
 template <typename W>
-__device__ __forceinline__ void warp_mma(float (&acc)[4][4], const float* a, int sam, int sak, const float* b, int sbk,
+__device__ __forceinline__ void warp_mma(float (&acc)[kNt][4], const float* a, int sam, int sak, const float* b, int sbk,
                                          int sbn, int k0, int k1, W wk) {
   const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
   // The instruction's own accumulation truncates: at most four steps add up in it before
   // they are added to acc in fp32 arithmetic.
   for (int kb = k0; kb < k1; kb += 32) {
-    float part[4][4] = {};
+    float part[kNt][4] = {};
     const int ke = min(kb + 32, k1);
-#pragma unroll 2
+#pragma unroll 4
     for (int k = kb; k < ke; k += 8) {
-      uint32_t ah[4], al[4];
+      uint32_t ah[4], al[4], bh[kNt][2], bl[kNt][2];
 #pragma unroll
       for (int i = 0; i < 4; ++i) split_tf32(a[(g + 8 * (i & 1)) * sam + (k + t + 4 * (i >> 1)) * sak], ah[i], al[i]);
-      const float w0 = wk(k + t), w1 = wk(k + t + 4);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t bh[2], bl[2];
-        split_tf32(w0 * b[(k + t) * sbk + (8 * j + g) * sbn], bh[0], bl[0]);
-        split_tf32(w1 * b[(k + t + 4) * sbk + (8 * j + g) * sbn], bh[1], bl[1]);
-        mma_tf32(part[j], al, bh);
-        mma_tf32(part[j], ah, bl);
-        mma_tf32(part[j], ah, bh);
+      for (int i = 0; i < 2; ++i) {
+        const float w = wk(k + t + 4 * i);
+#pragma unroll
+        for (int j = 0; j < kNt; ++j)
+          split_tf32(w * b[(k + t + 4 * i) * sbk + (8 * j + g) * sbn], bh[j][i], bl[j][i]);
       }
+#pragma unroll
+      for (int j = 0; j < kNt; ++j) mma_tf32(part[j], al, bh[j]);
+#pragma unroll
+      for (int j = 0; j < kNt; ++j) mma_tf32(part[j], ah, bl[j]);
+#pragma unroll
+      for (int j = 0; j < kNt; ++j) mma_tf32(part[j], ah, bh[j]);
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < kNt; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[j][e] += part[j][e];
   }
@@ -146,7 +150,7 @@ __global__ void __launch_bounds__(kF, 1) lin_f32_kernel(const __grid_constant__ 
   extern __shared__ float4 smem4[];
   F32Smem& sm = *reinterpret_cast<F32Smem*>(smem4);
   const int tid = threadIdx.x, warp = tid >> 5, g = (tid & 31) >> 2, t4 = tid & 3;
-  const int wm = (warp & 3) * 16, wn = (warp >> 2) * 32;  // this warp's part of a 64 x 64 tile
+  const int wm = (warp & 3) * 16, wn = (warp >> 2) * 8 * kNt;  // this warp's part of a 64 x 64 tile
   int head0 = 0;
   const LinItem x =
       kStateOnly ? lin_state_item(p, (int)blockIdx.x, &head0) : lin_item(p, (int)blockIdx.x);
@@ -220,20 +224,20 @@ __global__ void __launch_bounds__(kF, 1) lin_f32_kernel(const __grid_constant__ 
       }
       __syncthreads();
       const float *X = sm.X[s], *Y = sm.Y[s], *Z = sm.Z[s];
-      float acc[4][4];
+      float acc[kNt][4];
       auto clear = [&]() {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < kNt; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
       };
       if (!kStateOnly) {
         clear();
-        // S, only where some key of the warp's 16 x 32 part counts
-        const bool some = rev ? wn + 31 >= wm : wn <= wm + 15;
+        // S, only where some key of the warp's 16 x 16 part counts
+        const bool some = rev ? wn + 8 * kNt > wm : wn <= wm + 15;
         if (some) warp_mma(acc, X + wm * kLdX, kLdX, 1, Y + wn * kLdX, 1, kLdX, 0, a, NoWeight());
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < kNt; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int row = wm + g + 8 * (e >> 1), col = wn + 8 * j + 2 * t4 + (e & 1);
@@ -248,12 +252,12 @@ __global__ void __launch_bounds__(kF, 1) lin_f32_kernel(const __grid_constant__ 
           const int row = wm + g + 8 * (e >> 1);
           const float w = row < nv ? sm.pw[rev ? nv - 1 - row : row + sh] : 0.f;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) acc[j][e] *= w;
+          for (int j = 0; j < kNt; ++j) acc[j][e] *= w;
         }
         __syncthreads();  // P complete; R has been read
         warp_mma(acc, sm.P + wm * kLdP, kLdP, 1, Z + wn, kLdZ, 1, rev ? wm : 0, rev ? kC32 : wm + 16, NoWeight());
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < kNt; ++j)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int t = wm + g + 8 * e, col = wn + 8 * j + 2 * t4;
@@ -267,20 +271,20 @@ __global__ void __launch_bounds__(kF, 1) lin_f32_kernel(const __grid_constant__ 
             *o = v;
           }
       }
-      // R <- g^nv R + Yᵀ (w Z), 16 x 32 parts handed out to the warps
+      // R <- g^nv R + Yᵀ (w Z), 16 x 16 parts handed out to the warps
       const float dec = sm.pw[nv];
       const float* pw = sm.pw;
       auto wz = [&](int t) { return t < nv ? pw[rev ? t + 1 : nv - 1 - t] : 0.f; };
-      for (int tile = warp; tile < (a + 15) / 16 * 2; tile += kF / 32) {
-        const int m0 = (tile >> 1) * 16, n0 = (tile & 1) * 32;
+      for (int tile = warp; tile < (a + 15) / 16 * (kLinTile / (8 * kNt)); tile += kF / 32) {
+        const int m0 = tile / (kLinTile / (8 * kNt)) * 16, n0 = tile % (kLinTile / (8 * kNt)) * 8 * kNt;
         float* R = sm.R + (m0 + g) * kLdZ + n0 + 2 * t4;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < kNt; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[j][e] = dec * R[8 * (e >> 1) * kLdZ + 8 * j + (e & 1)];
         warp_mma(acc, Y + m0, 1, kLdX, Z + n0, kLdZ, 1, 0, kC32, wz);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < kNt; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) R[8 * (e >> 1) * kLdZ + 8 * j + (e & 1)] = acc[j][e];
       }
