@@ -83,17 +83,54 @@ __device__ __forceinline__ float sum8(const F8& x) {
   return s.x + s.y;
 }
 
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
-__device__ __forceinline__ float act_of(int act, float g) {
-  return act == BN_SILU ? g * sigmoid(g) : act == BN_SIGMOID ? sigmoid(g) : g;
+// 1 / (1 + e^-x) for a pair: one exp2 and one reciprocal each (2 ulp or so).  e^-x may reach
+// infinity, whose reciprocal is 0.
+__device__ __forceinline__ float2 sigmoid2(float2 x) {
+  const float2 t = mul2(x, pair(-1.4426950408889634f));
+  float2 e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(t.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(t.y));
+  e = add2(e, pair(1.f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
+  return r;
+}
+// The gate's activation, fixed at compile time: kNoGate for a norm without one.
+constexpr int kNoGate = -1;
+template <int kAct>
+__device__ __forceinline__ float2 act_of2(float2 g) {
+  if (kAct == BN_IDENTITY) return g;
+  const float2 s = sigmoid2(g);
+  return kAct == BN_SILU ? mul2(g, s) : s;
 }
 // act(g) and its derivative
-__device__ __forceinline__ float2 act_grad(int act, float g) {
-  if (act == BN_IDENTITY) return make_float2(g, 1.f);
-  const float s = sigmoid(g);
-  return act == BN_SILU ? make_float2(g * s, s * (1.f + g * (1.f - s))) : make_float2(s, s * (1.f - s));
+template <int kAct>
+__device__ __forceinline__ void act_grad2(float2 g, float2& a, float2& d) {
+  if (kAct == BN_IDENTITY) {
+    a = g;
+    d = pair(1.f);
+    return;
+  }
+  const float2 s = sigmoid2(g), q = fma2(s, pair(-1.f), pair(1.f));
+  if (kAct == BN_SILU) {
+    a = mul2(g, s);
+    d = fma2(a, q, s);  // s + g s (1 - s)
+  } else {
+    a = s;
+    d = mul2(s, q);
+  }
 }
-__device__ __forceinline__ float2 act_of2(int act, float2 g) { return make_float2(act_of(act, g.x), act_of(act, g.y)); }
+__device__ __forceinline__ float act_of(int act, float g) {
+  const float2 x = make_float2(g, 0.f);
+  return act == BN_SILU ? act_of2<BN_SILU>(x).x : act == BN_SIGMOID ? act_of2<BN_SIGMOID>(x).x : g;
+}
+__device__ __forceinline__ float2 act_grad(int act, float g) {
+  float2 a, d;
+  if (act == BN_SILU) act_grad2<BN_SILU>(make_float2(g, 0.f), a, d);
+  else if (act == BN_SIGMOID) act_grad2<BN_SIGMOID>(make_float2(g, 0.f), a, d);
+  else act_grad2<BN_IDENTITY>(make_float2(g, 0.f), a, d);
+  return make_float2(a.x, d.x);
+}
 
 // Sum over the aligned groups of `width` lanes (a power of two) that hold a value each.
 __device__ __forceinline__ float lanes_sum(float x, int width) {
@@ -125,7 +162,7 @@ __device__ __forceinline__ void row_sum(float (&x)[K], int tpr, float* red) {
 // (column (i tpr + t) 8) that stay in registers between the two norms, so nothing is read
 // twice.  Small rows share a CTA.  gl: lanes per group of y's norm, 0: the whole row.
 // ---------------------------------------------------------------------------------
-template <typename T, int NV>
+template <typename T, int NV, int kAct>
 __global__ void __launch_bounds__(512) bn_fwd_kernel(const __grid_constant__ BnArgs p, int tpr, int gl) {
   using R8 = typename Raw<T>::type;
   __shared__ float red1[16], red2[16];
@@ -143,7 +180,7 @@ __global__ void __launch_bounds__(512) bn_fwd_kernel(const __grid_constant__ BnA
     const bool on = live && c < p.D;
     yr[i] = on && Y ? raw8(Y + base + c) : R8{};
     xr[i] = on && X ? raw8(X + base + c) : R8{};
-    gr[i] = on && Gt ? raw8(Gt + base + c) : R8{};
+    gr[i] = on && kAct != kNoGate ? raw8(Gt + base + c) : R8{};
   }
   F8 x[NV];
   if (Y) {
@@ -177,7 +214,7 @@ __global__ void __launch_bounds__(512) bn_fwd_kernel(const __grid_constant__ BnA
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         float2 m = mul2(mul2(y.v[e], pair(r)), w.v[e]);
-        if (Gt) m = mul2(m, act_of2(p.act, g.v[e]));
+        if (kAct != kNoGate) m = mul2(m, act_of2<kAct>(g.v[e]));
         x[i].v[e] = fma2(sc.v[e], m, x[i].v[e]);
       }
       store8(XN + base + c, x[i]);
@@ -219,7 +256,7 @@ __global__ void __launch_bounds__(512) bn_fwd_kernel(const __grid_constant__ BnA
 constexpr int kBwdMaxT = 512;
 constexpr int kBwdMaxStages = 8;
 
-template <typename T, int NV>
+template <typename T, int NV, int kAct>
 __global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant__ BnArgs p, int tpr, int gl, int stages) {
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ __align__(8) uint64_t full[kBwdMaxStages];
@@ -323,17 +360,17 @@ __global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant_
       if (in[3]) {
         const F8 w = weight8(p.w_post, c), sc = weight8(p.scale, c), y = load8(aY + c);
         F8 dg;
-        const F8 g = in[4] ? load8(aG + c) : fill8(0.f);
+        const F8 g = kAct != kNoGate ? load8(aG + c) : fill8(0.f);
         float2 s = pair(0.f);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 yn = mul2(y.v[e], pair(r1[i])), n = mul2(yn, w.v[e]);
           float2 dn = mul2(dx.v[e], sc.v[e]);
-          if (in[4]) {
-            const float2 a0 = act_grad(p.act, g.v[e].x), a1 = act_grad(p.act, g.v[e].y);
-            const float2 av = make_float2(a0.x, a1.x);
+          if (kAct != kNoGate) {
+            float2 av, ad;
+            act_grad2<kAct>(g.v[e], av, ad);
             ascale[i].v[e] = fma2(mul2(dx.v[e], av), n, ascale[i].v[e]);
-            dg.v[e] = mul2(mul2(dn, n), make_float2(a0.y, a1.y));
+            dg.v[e] = mul2(mul2(dn, n), ad);
             dn = mul2(dn, av);
           } else {
             ascale[i].v[e] = fma2(dx.v[e], n, ascale[i].v[e]);
@@ -343,7 +380,7 @@ __global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant_
           s = fma2(un[i].v[e], y.v[e], s);
         }
         se[i] = s.x + s.y;
-        if (in[4]) store8(static_cast<T*>(p.dgate) + (size_t)row * p.D + c, dg);
+        if (kAct != kNoGate) store8(static_cast<T*>(p.dgate) + (size_t)row * p.D + c, dg);
       }
     }
     if (gl) {
@@ -399,24 +436,30 @@ __global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant_
   for (int c = tid; c < 3 * p.D; c += blockDim.x) part[c] = acc[c];
 }
 
-// Sums of the CTAs' partials, in order: 32 columns x 8 slices of the parts per CTA.
-__global__ void __launch_bounds__(256) bn_reduce_kernel(const __grid_constant__ BnArgs p, int nparts) {
-  __shared__ float red[8][32];
-  const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane, which = blockIdx.y;
-  float* out = which == 0 ? p.dw_pre : which == 1 ? p.dw_post : p.dscale;
-  if (!out) return;
-  const int per = (nparts + 7) / 8, p0 = sl * per, p1 = min(nparts, p0 + per);
-  float s = 0.f;
-  if (c < p.D)
-#pragma unroll 8
-    for (int i = p0; i < p1; ++i) s += p.part[((size_t)i * 3 + which) * p.D + c];
+// Sums of the CTAs' partials, in order: 32 columns x 32 slices of the parts per CTA, so that
+// a thread's few loads are in flight at once.  blockIdx.y counts the gradients asked for.
+constexpr int kSlices = 32;
+constexpr int kPerSlice = (kBnMaxParts + kSlices - 1) / kSlices;
+__global__ void __launch_bounds__(32 * kSlices) bn_reduce_kernel(const __grid_constant__ BnArgs p, int nparts) {
+  __shared__ float red[kSlices][33];
+  float* const outs[3] = {p.dw_pre, p.dw_post, p.dscale};
+  int which = -1;
+  for (int i = 0, n = (int)blockIdx.y; i < 3; ++i)
+    if (outs[i] && n-- == 0) which = i;
+  const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+  const int per = (nparts + kSlices - 1) / kSlices, p0 = sl * per;
+  float x[kPerSlice], s = 0.f;
+#pragma unroll
+  for (int i = 0; i < kPerSlice; ++i)
+    x[i] = c < p.D && i < per && p0 + i < nparts ? p.part[((size_t)(p0 + i) * 3 + which) * p.D + c] : 0.f;
+#pragma unroll
+  for (int i = 0; i < kPerSlice; ++i) s += x[i];
   red[sl][lane] = s;
   __syncthreads();
   if (sl == 0 && c < p.D) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += red[i][lane];
-    out[c] = s;
+    for (int i = 1; i < kSlices; ++i) s += red[i][lane];
+    outs[which][c] = s;
   }
 }
 
@@ -571,6 +614,19 @@ int group_lanes(const BnArgs& p) {
   return p.group % 8 == 0 && n <= 32 && (n & (n - 1)) == 0 ? n : -1;
 }
 
+template <int N>
+struct Int {
+  static constexpr int value = N;
+};
+// f(Int<the gate's activation>)
+template <typename F>
+void with_act(const BnArgs& p, F f) {
+  if (!p.gate) f(Int<kNoGate>());
+  else if (p.act == BN_SILU) f(Int<BN_SILU>());
+  else if (p.act == BN_SIGMOID) f(Int<BN_SIGMOID>());
+  else f(Int<BN_IDENTITY>());
+}
+
 template <typename T>
 cudaError_t fwd(const BnArgs& p, cudaStream_t st) {
   const int gl = group_lanes(p), nvec = p.D / 8;
@@ -590,9 +646,12 @@ cudaError_t fwd(const BnArgs& p, cudaStream_t st) {
   tpr = tpr < 32 ? 32 : tpr;
   const int threads = tpr < 128 ? 128 : tpr, R = threads / tpr;
   const unsigned grid = (unsigned)((p.rows + R - 1) / R);
-  if (nv == 1) bn_fwd_kernel<T, 1><<<grid, threads, 0, st>>>(p, tpr, gl);
-  else if (nv == 2) bn_fwd_kernel<T, 2><<<grid, threads, 0, st>>>(p, tpr, gl);
-  else bn_fwd_kernel<T, 4><<<grid, threads, 0, st>>>(p, tpr, gl);
+  with_act(p, [&](auto act) {
+    constexpr int kAct = decltype(act)::value;
+    if (nv == 1) bn_fwd_kernel<T, 1, kAct><<<grid, threads, 0, st>>>(p, tpr, gl);
+    else if (nv == 2) bn_fwd_kernel<T, 2, kAct><<<grid, threads, 0, st>>>(p, tpr, gl);
+    else bn_fwd_kernel<T, 4, kAct><<<grid, threads, 0, st>>>(p, tpr, gl);
+  });
   return cudaGetLastError();
 }
 
@@ -603,11 +662,15 @@ cudaError_t bwd_fast(const BnArgs& p, const BnBwdPlan& pl, int gl, cudaStream_t 
   int stages = (int)((size_t)pl.smem / stage);
   stages = stages > kBwdMaxStages ? kBwdMaxStages : stages;
   const size_t smem = stage * stages > acc ? stage * stages : acc;
-  static SmemLimit limit;
-  const cudaError_t e = limit.raise(bn_bwd_kernel<T, NV>, kBnBwdSmem);
-  if (e != cudaSuccess) return e;
-  bn_bwd_kernel<T, NV><<<pl.ctas, pl.threads, smem, st>>>(p, pl.tpr, gl, stages);
-  return cudaGetLastError();
+  cudaError_t e = cudaSuccess;
+  with_act(p, [&](auto act) {
+    constexpr int kAct = decltype(act)::value;
+    static SmemLimit limit;
+    if ((e = limit.raise(bn_bwd_kernel<T, NV, kAct>, kBnBwdSmem)) != cudaSuccess) return;
+    bn_bwd_kernel<T, NV, kAct><<<pl.ctas, pl.threads, smem, st>>>(p, pl.tpr, gl, stages);
+    e = cudaGetLastError();
+  });
+  return e;
 }
 
 template <typename T>
@@ -628,7 +691,8 @@ cudaError_t bwd(const BnArgs& p, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   note_launch();
   if (p.dw_pre || p.dw_post || p.dscale) {
-    bn_reduce_kernel<<<dim3((p.D + 31) / 32, 3), 256, 0, st>>>(p, pl.ctas);
+    const int outs = (p.dw_pre ? 1 : 0) + (p.dw_post ? 1 : 0) + (p.dscale ? 1 : 0);
+    bn_reduce_kernel<<<dim3((p.D + 31) / 32, outs), 32 * kSlices, 0, st>>>(p, pl.ctas);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     note_launch();
   }
