@@ -256,7 +256,12 @@ __global__ void __launch_bounds__(512) bn_fwd_kernel(const __grid_constant__ BnA
 constexpr int kBwdMaxT = 512;
 constexpr int kBwdMaxStages = 8;
 
-template <typename T, int NV, int kAct>
+// Which arguments there are, where that is known at compile time: all of them (the joint
+// between two blocks), or dx_new, y and w_post alone (a norm per head, with or without a
+// gate).  kAny looks at the pointers, for every other combination.
+enum { kJoint, kHeads, kAny };
+
+template <typename T, int NV, int kAct, int kArgs>
 __global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant__ BnArgs p, int tpr, int gl, int stages) {
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ __align__(8) uint64_t full[kBwdMaxStages];
@@ -264,6 +269,14 @@ __global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant_
   const int tid = threadIdx.x, t = tid & (tpr - 1), slot = tid / tpr, R = blockDim.x / tpr;
   const T* in[5] = {static_cast<const T*>(p.dh), static_cast<const T*>(p.x), static_cast<const T*>(p.dx_new),
                     static_cast<const T*>(p.y), static_cast<const T*>(p.gate)};
+  const bool has_pre = kArgs == kAny ? p.dh != nullptr : kArgs == kJoint;
+  const bool has_dxn = kArgs != kAny || p.dx_new, has_y = kArgs != kAny || p.y;
+  const bool has_dx = kArgs == kAny ? p.dx != nullptr : kArgs == kJoint;
+  auto w_pre = [&](int c) { return kArgs == kJoint ? load8(p.w_pre + c) : weight8(p.w_pre, c); };
+  auto w_post = [&](int c) { return kArgs != kAny ? load8(p.w_post + c) : weight8(p.w_post, c); };
+  auto scale = [&](int c) {
+    return kArgs == kJoint ? load8(p.scale + c) : kArgs == kHeads ? fill8(1.f) : weight8(p.scale, c);
+  };
   const size_t arr = (size_t)R * p.D * sizeof(T);  // one array of a stage
   int nin = 0, at[5];
 #pragma unroll
@@ -311,8 +324,8 @@ __global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant_
       const int c = (i * tpr + t) * 8;
       sg[i] = 0.f;
       if (!live || c >= p.D) continue;
-      if (in[0]) {
-        const F8 x = load8(aX + c), dh = load8(aH + c), w = weight8(p.w_pre, c);
+      if (has_pre) {
+        const F8 x = load8(aX + c), dh = load8(aH + c), w = w_pre(c);
         float2 xx = mul2(x.v[0], x.v[0]), ux = mul2(mul2(dh.v[0], w.v[0]), x.v[0]);
 #pragma unroll
         for (int e = 1; e < 4; ++e) {
@@ -322,7 +335,7 @@ __global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant_
         s3[0] += xx.x + xx.y;
         s3[1] += ux.x + ux.y;
       }
-      if (in[3]) {
+      if (has_y) {
         const F8 y = load8(aY + c);
         float2 yy = mul2(y.v[0], y.v[0]);
 #pragma unroll
@@ -346,9 +359,9 @@ __global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant_
       r1[i] = rsqrtf((gl ? sg[i] : s3[2]) * p.inv_group + p.eps);
       un[i] = fill8(0.f);
       if (!live || c >= p.D) continue;
-      F8 dx = in[2] ? load8(aD + c) : fill8(0.f);
-      if (in[0]) {
-        const F8 x = load8(aX + c), dh = load8(aH + c), w = weight8(p.w_pre, c);
+      F8 dx = has_dxn ? load8(aD + c) : fill8(0.f);
+      if (has_pre) {
+        const F8 x = load8(aX + c), dh = load8(aH + c), w = w_pre(c);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 d = mul2(dh.v[e], pair(r2));
@@ -356,9 +369,9 @@ __global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant_
           dx.v[e] = fma2(d, w.v[e], fma2(x.v[e], pair(c2), dx.v[e]));
         }
       }
-      if (p.dx) store8(static_cast<T*>(p.dx) + (size_t)row * p.D + c, dx);
-      if (in[3]) {
-        const F8 w = weight8(p.w_post, c), sc = weight8(p.scale, c), y = load8(aY + c);
+      if (has_dx) store8(static_cast<T*>(p.dx) + (size_t)row * p.D + c, dx);
+      if (has_y) {
+        const F8 w = w_post(c), sc = scale(c), y = load8(aY + c);
         F8 dg;
         const F8 g = kAct != kNoGate ? load8(aG + c) : fill8(0.f);
         float2 s = pair(0.f);
@@ -369,11 +382,11 @@ __global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant_
           if (kAct != kNoGate) {
             float2 av, ad;
             act_grad2<kAct>(g.v[e], av, ad);
-            ascale[i].v[e] = fma2(mul2(dx.v[e], av), n, ascale[i].v[e]);
+            if (kArgs != kHeads) ascale[i].v[e] = fma2(mul2(dx.v[e], av), n, ascale[i].v[e]);
             dg.v[e] = mul2(mul2(dn, n), ad);
             dn = mul2(dn, av);
           } else {
-            ascale[i].v[e] = fma2(dx.v[e], n, ascale[i].v[e]);
+            if (kArgs != kHeads) ascale[i].v[e] = fma2(dx.v[e], n, ascale[i].v[e]);
           }
           apost[i].v[e] = fma2(dn, yn, apost[i].v[e]);
           un[i].v[e] = mul2(dn, w.v[e]);
@@ -394,7 +407,7 @@ __global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant_
 #pragma unroll
       for (int i = 0; i < NV; ++i) se[i] = s[0];
     }
-    if (in[3]) {
+    if (has_y) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = (i * tpr + t) * 8;
@@ -468,7 +481,7 @@ __global__ void __launch_bounds__(32 * kSlices) bn_reduce_kernel(const __grid_co
 // The rsqrt of each group stays in shared memory; inputs are read again for each step
 // (from L1 or L2).
 // ---------------------------------------------------------------------------------
-constexpr int kAny = 256;
+constexpr int kAnyT = 256;
 
 __device__ __forceinline__ float block_sum(float x, float* red) {
   x = lanes_sum(x, 32);
@@ -477,7 +490,7 @@ __device__ __forceinline__ float block_sum(float x, float* red) {
   __syncthreads();
   float s = 0.f;
 #pragma unroll
-  for (int w = 0; w < kAny / 32; ++w) s += red[w];
+  for (int w = 0; w < kAnyT / 32; ++w) s += red[w];
   return s;
 }
 // out[k] = sum over group k of f(column), for every group of the row: by the whole CTA for
@@ -487,11 +500,11 @@ __device__ __forceinline__ void group_sums(int D, int group, float* out, float* 
   const int n = D / group;
   if (n == 1) {
     float s = 0.f;
-    for (int c = threadIdx.x; c < D; c += kAny) s += f(c);
+    for (int c = threadIdx.x; c < D; c += kAnyT) s += f(c);
     s = block_sum(s, red);
     if (threadIdx.x == 0) out[0] = s;
   } else {
-    for (int k = threadIdx.x >> 5; k < n; k += kAny / 32) {
+    for (int k = threadIdx.x >> 5; k < n; k += kAnyT / 32) {
       float s = 0.f;
       for (int c = threadIdx.x & 31; c < group; c += 32) s += f(k * group + c);
       s = lanes_sum(s, 32);
@@ -502,9 +515,9 @@ __device__ __forceinline__ void group_sums(int D, int group, float* out, float* 
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kAny) bn_fwd_any_kernel(const __grid_constant__ BnArgs p) {
+__global__ void __launch_bounds__(kAnyT) bn_fwd_any_kernel(const __grid_constant__ BnArgs p) {
   extern __shared__ float s_grp[];
-  __shared__ float red[kAny / 32];
+  __shared__ float red[kAnyT / 32];
   const size_t base = (size_t)blockIdx.x * p.D;
   const T *X = static_cast<const T*>(p.x), *Y = static_cast<const T*>(p.y), *Gt = static_cast<const T*>(p.gate);
   if (Y)
@@ -524,13 +537,13 @@ __global__ void __launch_bounds__(kAny) bn_fwd_any_kernel(const __grid_constant_
   };
   float s = 0.f;
   // x' may be written over x or y only after h has been formed: the values are read again
-  for (int c = threadIdx.x; c < p.D; c += kAny) {
+  for (int c = threadIdx.x; c < p.D; c += kAnyT) {
     const float x = value(c);
     s += x * x;
   }
   s = block_sum(s, red);
   const float r = rsqrtf(s * p.inv_D + p.eps);
-  for (int c = threadIdx.x; c < p.D; c += kAny) {
+  for (int c = threadIdx.x; c < p.D; c += kAnyT) {
     const float x = value(c);
     if (Y) ll_store(static_cast<T*>(p.x_new), base + c, x);
     if (p.h) ll_store(static_cast<T*>(p.h), base + c, p.w_pre ? x * r * p.w_pre[c] : x * r);
@@ -538,21 +551,21 @@ __global__ void __launch_bounds__(kAny) bn_fwd_any_kernel(const __grid_constant_
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kAny) bn_bwd_any_kernel(const __grid_constant__ BnArgs p) {
+__global__ void __launch_bounds__(kAnyT) bn_bwd_any_kernel(const __grid_constant__ BnArgs p) {
   extern __shared__ float s_dyn[];
-  __shared__ float red[kAny / 32];
+  __shared__ float red[kAnyT / 32];
   const int ng = p.D / p.group;
   float *acc = s_dyn;                       // 3 x D weight gradients of this CTA's rows
   float *s_y = acc + 3 * p.D, *s_e = s_y + ng;  // per group: sum y², sum un y
   const T *H = static_cast<const T*>(p.dh), *X = static_cast<const T*>(p.x), *Dn = static_cast<const T*>(p.dx_new),
           *Y = static_cast<const T*>(p.y), *Gt = static_cast<const T*>(p.gate);
-  for (int c = threadIdx.x; c < 3 * p.D; c += kAny) acc[c] = 0.f;
+  for (int c = threadIdx.x; c < 3 * p.D; c += kAnyT) acc[c] = 0.f;
   for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
     const size_t base = (size_t)row * p.D;
     __syncthreads();
     float a = 0.f, b = 0.f;
     if (H)
-      for (int c = threadIdx.x; c < p.D; c += kAny) {
+      for (int c = threadIdx.x; c < p.D; c += kAnyT) {
         const float x = ll_load(X, base + c), u = ll_load(H, base + c) * (p.w_pre ? p.w_pre[c] : 1.f);
         a += x * x;
         b += u * x;
@@ -576,7 +589,7 @@ __global__ void __launch_bounds__(kAny) bn_bwd_any_kernel(const __grid_constant_
       return p.w_post ? d * p.w_post[c] : d;
     };
     if (Y) group_sums(p.D, p.group, s_e, red, [&](int c) { return un_of(c) * ll_load(Y, base + c); });
-    for (int c = threadIdx.x; c < p.D; c += kAny) {
+    for (int c = threadIdx.x; c < p.D; c += kAnyT) {
       const float dx = dx_of(c);
       if (H) acc[c] += ll_load(H, base + c) * ll_load(X, base + c) * r2;
       float dy = 0.f, dg = 0.f;
@@ -598,7 +611,7 @@ __global__ void __launch_bounds__(kAny) bn_bwd_any_kernel(const __grid_constant_
   }
   __syncthreads();
   float* part = p.part + (size_t)blockIdx.x * 3 * p.D;
-  for (int c = threadIdx.x; c < 3 * p.D; c += kAny) part[c] = acc[c];
+  for (int c = threadIdx.x; c < 3 * p.D; c += kAnyT) part[c] = acc[c];
 }
 
 int ceil_pow2(int x) {
@@ -635,7 +648,7 @@ cudaError_t fwd(const BnArgs& p, cudaStream_t st) {
     static SmemLimit limit;
     const cudaError_t e = limit.raise(bn_fwd_any_kernel<T>, kBnMaxGroups * 4);
     if (e != cudaSuccess) return e;
-    bn_fwd_any_kernel<T><<<(unsigned)p.rows, kAny, smem, st>>>(p);
+    bn_fwd_any_kernel<T><<<(unsigned)p.rows, kAnyT, smem, st>>>(p);
     return cudaGetLastError();
   }
   // With many rows, four vectors a thread (two in fp32): fewer threads a row, more rows on
@@ -662,13 +675,22 @@ cudaError_t bwd_fast(const BnArgs& p, const BnBwdPlan& pl, int gl, cudaStream_t 
   int stages = (int)((size_t)pl.smem / stage);
   stages = stages > kBwdMaxStages ? kBwdMaxStages : stages;
   const size_t smem = stage * stages > acc ? stage * stages : acc;
+  const bool base = p.dx_new && p.y && p.w_post;
+  const int args = base && p.dh && p.w_pre && p.scale && p.dx ? kJoint : base && !p.dh && !p.scale && !p.dx ? kHeads : kAny;
   cudaError_t e = cudaSuccess;
   with_act(p, [&](auto act) {
     constexpr int kAct = decltype(act)::value;
-    static SmemLimit limit;
-    if ((e = limit.raise(bn_bwd_kernel<T, NV, kAct>, kBnBwdSmem)) != cudaSuccess) return;
-    bn_bwd_kernel<T, NV, kAct><<<pl.ctas, pl.threads, smem, st>>>(p, pl.tpr, gl, stages);
-    e = cudaGetLastError();
+    auto launch = [&](auto kernel, SmemLimit& limit) {
+      if ((e = limit.raise(kernel, kBnBwdSmem)) != cudaSuccess) return;
+      kernel<<<pl.ctas, pl.threads, smem, st>>>(p, pl.tpr, gl, stages);
+      e = cudaGetLastError();
+    };
+    static SmemLimit limits[3];
+    if constexpr (kAct == kNoGate || kAct == BN_SILU) {  // the activations in use have their own kernels
+      if (args == kJoint) return launch(bn_bwd_kernel<T, NV, kAct, kJoint>, limits[0]);
+      if (args == kHeads) return launch(bn_bwd_kernel<T, NV, kAct, kHeads>, limits[1]);
+    }
+    launch(bn_bwd_kernel<T, NV, kAct, kAny>, limits[2]);
   });
   return e;
 }
@@ -683,7 +705,7 @@ cudaError_t bwd(const BnArgs& p, cudaStream_t st) {
     static SmemLimit limit;
     e = limit.raise(bn_bwd_any_kernel<T>, (3 * kBnMaxD + 2 * kBnMaxGroups) * 4);
     if (e != cudaSuccess) return e;
-    bn_bwd_any_kernel<T><<<pl.ctas, kAny, smem, st>>>(p);
+    bn_bwd_any_kernel<T><<<pl.ctas, kAnyT, smem, st>>>(p);
     e = cudaGetLastError();
   } else {
     e = pl.nv == 1 ? bwd_fast<T, 1>(p, pl, gl, st) : bwd_fast<T, 2>(p, pl, gl, st);
