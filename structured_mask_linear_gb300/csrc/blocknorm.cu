@@ -602,7 +602,8 @@ __global__ void __launch_bounds__(kAnyT) bn_bwd_any_kernel(const __grid_constant
         acc[p.D + c] += dm * ac.x * yn;
         acc[2 * p.D + c] += dx * ac.x * n;
         dg = dm * n * ac.y;
-        dy = r1 * (un_of(c) - y * r1 * r1 * s_e[k] * p.inv_group);
+        // a group of one: the two terms are equal but for eps, which is all that is left
+        dy = p.group == 1 ? r1 * r1 * r1 * p.eps * un_of(c) : r1 * (un_of(c) - y * r1 * r1 * s_e[k] * p.inv_group);
       }
       if (p.dx) ll_store(static_cast<T*>(p.dx), base + c, dx);
       if (Gt) ll_store(static_cast<T*>(p.dgate), base + c, dg);
