@@ -77,7 +77,45 @@ __device__ __forceinline__ uint32_t pack2(float2 a) {
 __device__ __forceinline__ void store8(__nv_bfloat16* p, const F8& x) {
   *reinterpret_cast<uint4*>(p) = make_uint4(pack2(x.v[0]), pack2(x.v[1]), pack2(x.v[2]), pack2(x.v[3]));
 }
-__device__ __forceinline__ F8 weight8(const float* w, int c) { return w ? load8(w + c) : fill8(1.f); }
+// The eight columns of a thread's vector: side by side, or where rows are not whole vectors
+// (D no multiple of 8, so that they start anywhere) `step` apart, so that the threads of a row
+// read neighbours; those from D on are 0.
+template <bool kOdd>
+struct Eight {
+  int c, step, D;
+  __device__ __forceinline__ Eight(int i, int t, int tpr, int D) : c(kOdd ? i * 8 * tpr + t : (i * tpr + t) * 8), step(tpr), D(D) {}
+  __device__ __forceinline__ bool any() const { return c < D; }
+  __device__ __forceinline__ uint4 raw(const __nv_bfloat16* p) const {
+    if (!kOdd) return raw8(p + c);
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const unsigned short* q = reinterpret_cast<const unsigned short*>(p) + c + 2 * e * step;
+      const uint32_t lo = c + 2 * e * step < D ? q[0] : 0u, hi = c + (2 * e + 1) * step < D ? q[step] : 0u;
+      w[e] = lo | hi << 16;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ RawF raw(const float* p) const {
+    if (!kOdd) return raw8(p + c);
+    float w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = c + e * step < D ? p[c + e * step] : 0.f;
+    return {make_float4(w[0], w[1], w[2], w[3]), make_float4(w[4], w[5], w[6], w[7])};
+  }
+  template <typename T>
+  __device__ __forceinline__ F8 load(const T* p) const {
+    return unpack8(raw(p));
+  }
+  __device__ __forceinline__ F8 weight(const float* w) const { return w ? load(w) : fill8(1.f); }
+  template <typename T>
+  __device__ __forceinline__ void store(T* p, const F8& x) const {
+    if (!kOdd) return store8(p + c, x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (c + e * step < D) ll_store(p, c + e * step, e & 1 ? x.v[e >> 1].y : x.v[e >> 1].x);
+  }
+};
 __device__ __forceinline__ float sum8(const F8& x) {
   const float2 s = add2(add2(x.v[0], x.v[1]), add2(x.v[2], x.v[3]));
   return s.x + s.y;
@@ -158,11 +196,11 @@ __device__ __forceinline__ void row_sum(float (&x)[K], int tpr, float* red) {
 }
 
 // ---------------------------------------------------------------------------------
-// bn_fwd: D a multiple of 8, up to 512 threads a row, each with NV vectors of 8 values
-// (column (i tpr + t) 8) that stay in registers between the two norms, so nothing is read
-// twice.  Small rows share a CTA.  gl: lanes per group of y's norm, 0: the whole row.
+// bn_fwd: up to 512 threads a row, each with NV vectors of 8 values that stay in registers
+// between the two norms, so nothing is read twice.  Small rows share a CTA.  gl: lanes per
+// group of y's norm, 0: the whole row (kOdd: D is no multiple of 8).
 // ---------------------------------------------------------------------------------
-template <typename T, int NV, int kAct>
+template <typename T, int NV, int kAct, bool kOdd>
 __global__ void __launch_bounds__(512) bn_fwd_kernel(const __grid_constant__ BnArgs p, int tpr, int gl) {
   using R8 = typename Raw<T>::type;
   __shared__ float red1[16], red2[16];
@@ -176,11 +214,11 @@ __global__ void __launch_bounds__(512) bn_fwd_kernel(const __grid_constant__ BnA
   R8 yr[NV], xr[NV], gr[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = (i * tpr + t) * 8;
-    const bool on = live && c < p.D;
-    yr[i] = on && Y ? raw8(Y + base + c) : R8{};
-    xr[i] = on && X ? raw8(X + base + c) : R8{};
-    gr[i] = on && kAct != kNoGate ? raw8(Gt + base + c) : R8{};
+    const Eight<kOdd> c(i, t, tpr, p.D);
+    const bool on = live && c.any();
+    yr[i] = on && Y ? c.raw(Y + base) : R8{};
+    xr[i] = on && X ? c.raw(X + base) : R8{};
+    gr[i] = on && kAct != kNoGate ? c.raw(Gt + base) : R8{};
   }
   F8 x[NV];
   if (Y) {
@@ -206,18 +244,18 @@ __global__ void __launch_bounds__(512) bn_fwd_kernel(const __grid_constant__ BnA
     T* XN = static_cast<T*>(p.x_new);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * tpr + t) * 8;
+      const Eight<kOdd> c(i, t, tpr, p.D);
       x[i] = unpack8(xr[i]);
-      if (!live || c >= p.D) continue;
+      if (!live || !c.any()) continue;
       const float r = rsqrtf(ss[i] * p.inv_group + p.eps);
-      const F8 w = weight8(p.w_post, c), sc = weight8(p.scale, c), y = unpack8(yr[i]), g = unpack8(gr[i]);
+      const F8 w = c.weight(p.w_post), sc = c.weight(p.scale), y = unpack8(yr[i]), g = unpack8(gr[i]);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         float2 m = mul2(mul2(y.v[e], pair(r)), w.v[e]);
         if (kAct != kNoGate) m = mul2(m, act_of2<kAct>(g.v[e]));
         x[i].v[e] = fma2(sc.v[e], m, x[i].v[e]);
       }
-      store8(XN + base + c, x[i]);
+      c.store(XN + base, x[i]);
     }
   } else {
 #pragma unroll
@@ -236,12 +274,12 @@ __global__ void __launch_bounds__(512) bn_fwd_kernel(const __grid_constant__ BnA
   const float r = rsqrtf(s[0] * p.inv_D + p.eps);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = (i * tpr + t) * 8;
-    if (!live || c >= p.D) continue;
-    const F8 w = weight8(p.w_pre, c);
+    const Eight<kOdd> c(i, t, tpr, p.D);
+    if (!live || !c.any()) continue;
+    const F8 w = c.weight(p.w_pre);
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[i].v[e] = mul2(mul2(x[i].v[e], pair(r)), w.v[e]);
-    store8(static_cast<T*>(p.h) + base + c, x[i]);
+    c.store(static_cast<T*>(p.h) + base, x[i]);
   }
 }
 
@@ -251,7 +289,9 @@ __global__ void __launch_bounds__(512) bn_fwd_kernel(const __grid_constant__ BnA
 // into a ring of stages in shared memory; the reductions of one step overlap the copies of
 // the next ones and the other CTA's arithmetic.  The weights' gradients stay in registers
 // over a CTA's rows and go out once, the row slots combined in shared memory; bn_reduce adds
-// the CTAs' partials in order.
+// the CTAs' partials in order.  Rows that are not whole vectors (kOdd) cannot be copied that
+// way: they are read where they lie, the second and third time from L1 (37317 rows of 222 in
+// bf16: 94 us, of which memory needs 20; value by value with a CTA per row 489).
 // ---------------------------------------------------------------------------------
 constexpr int kBwdMaxT = 512;
 constexpr int kBwdMaxStages = 8;
@@ -261,7 +301,7 @@ constexpr int kBwdMaxStages = 8;
 // gate).  kAny looks at the pointers, for every other combination.
 enum { kJoint, kHeads, kAny };
 
-template <typename T, int NV, int kAct, int kArgs>
+template <typename T, int NV, int kAct, int kArgs, bool kOdd>
 __global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant__ BnArgs p, int tpr, int gl, int stages) {
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ __align__(8) uint64_t full[kBwdMaxStages];
@@ -272,10 +312,11 @@ __global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant_
   const bool has_pre = kArgs == kAny ? p.dh != nullptr : kArgs == kJoint;
   const bool has_dxn = kArgs != kAny || p.dx_new, has_y = kArgs != kAny || p.y;
   const bool has_dx = kArgs == kAny ? p.dx != nullptr : kArgs == kJoint;
-  auto w_pre = [&](int c) { return kArgs == kJoint ? load8(p.w_pre + c) : weight8(p.w_pre, c); };
-  auto w_post = [&](int c) { return kArgs != kAny ? load8(p.w_post + c) : weight8(p.w_post, c); };
-  auto scale = [&](int c) {
-    return kArgs == kJoint ? load8(p.scale + c) : kArgs == kHeads ? fill8(1.f) : weight8(p.scale, c);
+  using C8 = Eight<kOdd>;
+  auto w_pre = [&](const C8& c) { return kArgs == kJoint ? c.load(p.w_pre) : c.weight(p.w_pre); };
+  auto w_post = [&](const C8& c) { return kArgs != kAny ? c.load(p.w_post) : c.weight(p.w_post); };
+  auto scale = [&](const C8& c) {
+    return kArgs == kJoint ? c.load(p.scale) : kArgs == kHeads ? fill8(1.f) : c.weight(p.scale);
   };
   const size_t arr = (size_t)R * p.D * sizeof(T);  // one array of a stage
   int nin = 0, at[5];
@@ -291,7 +332,7 @@ __global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant_
     for (int k = 0; k < 5; ++k)
       if (in[k]) ptx::bulk_load(sm + ((size_t)st * nin + at[k]) * arr, in[k] + (size_t)r0 * p.D, bytes, &full[st]);
   };
-  if (tid == 0) {
+  if (!kOdd && tid == 0) {
     for (int i = 0; i < stages; ++i) ptx::mbar_init(&full[i], 1);
     ptx::fence_mbar_init();
     for (int i = 0; i < stages; ++i)
@@ -304,28 +345,32 @@ __global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant_
   for (int i = 0; i < NV; ++i) apre[i] = apost[i] = ascale[i] = fill8(0.f);
   long long it = 0;
   for (long long step = blockIdx.x; step < steps; step += gridDim.x, ++it) {
-    const int st = (int)(it % stages);
+    const int st = kOdd ? 0 : (int)(it % stages);
     const long long row = step * R + slot;
     const bool live = row < p.rows;
-    bool ok = bn_wait(&full[st], (uint32_t)(it / stages) & 1);
-    if (!ok) atomicExch(p.status, (unsigned)LL_ERR_TIMEOUT);
-    if (!__syncthreads_and(ok)) {
-      if (tid == 0)  // let the other copies in flight land (bounded)
-        for (int i = 0; i < stages; ++i) bn_wait(&full[i], (uint32_t)((it + (i - st + stages) % stages) / stages) & 1);
-      return;
+    if (!kOdd) {
+      bool ok = bn_wait(&full[st], (uint32_t)(it / stages) & 1);
+      if (!ok) atomicExch(p.status, (unsigned)LL_ERR_TIMEOUT);
+      if (!__syncthreads_and(ok)) {
+        if (tid == 0)  // let the other copies in flight land (bounded)
+          for (int i = 0; i < stages; ++i) bn_wait(&full[i], (uint32_t)((it + (i - st + stages) % stages) / stages) & 1);
+        return;
+      }
     }
     const T* a = reinterpret_cast<const T*>(sm + (size_t)st * nin * arr) + (size_t)slot * p.D;
     const size_t arre = arr / sizeof(T);
-    const T *aH = a + at[0] * arre, *aX = a + at[1] * arre, *aD = a + at[2] * arre, *aY = a + at[3] * arre,
-            *aG = a + at[4] * arre;
+    const size_t here = (size_t)row * p.D;
+    const T *aH = kOdd ? in[0] + here : a + at[0] * arre, *aX = kOdd ? in[1] + here : a + at[1] * arre,
+            *aD = kOdd ? in[2] + here : a + at[2] * arre, *aY = kOdd ? in[3] + here : a + at[3] * arre,
+            *aG = kOdd ? in[4] + here : a + at[4] * arre;
     float s3[3] = {0.f, 0.f, 0.f}, sg[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * tpr + t) * 8;
+      const C8 c(i, t, tpr, p.D);
       sg[i] = 0.f;
-      if (!live || c >= p.D) continue;
+      if (!live || !c.any()) continue;
       if (has_pre) {
-        const F8 x = load8(aX + c), dh = load8(aH + c), w = w_pre(c);
+        const F8 x = c.load(aX), dh = c.load(aH), w = w_pre(c);
         float2 xx = mul2(x.v[0], x.v[0]), ux = mul2(mul2(dh.v[0], w.v[0]), x.v[0]);
 #pragma unroll
         for (int e = 1; e < 4; ++e) {
@@ -336,7 +381,7 @@ __global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant_
         s3[1] += ux.x + ux.y;
       }
       if (has_y) {
-        const F8 y = load8(aY + c);
+        const F8 y = c.load(aY);
         float2 yy = mul2(y.v[0], y.v[0]);
 #pragma unroll
         for (int e = 1; e < 4; ++e) yy = fma2(y.v[e], y.v[e], yy);
@@ -354,14 +399,14 @@ __global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant_
     F8 un[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * tpr + t) * 8;
+      const C8 c(i, t, tpr, p.D);
       se[i] = 0.f;
       r1[i] = rsqrtf((gl ? sg[i] : s3[2]) * p.inv_group + p.eps);
       un[i] = fill8(0.f);
-      if (!live || c >= p.D) continue;
-      F8 dx = has_dxn ? load8(aD + c) : fill8(0.f);
+      if (!live || !c.any()) continue;
+      F8 dx = has_dxn ? c.load(aD) : fill8(0.f);
       if (has_pre) {
-        const F8 x = load8(aX + c), dh = load8(aH + c), w = w_pre(c);
+        const F8 x = c.load(aX), dh = c.load(aH), w = w_pre(c);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 d = mul2(dh.v[e], pair(r2));
@@ -369,11 +414,11 @@ __global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant_
           dx.v[e] = fma2(d, w.v[e], fma2(x.v[e], pair(c2), dx.v[e]));
         }
       }
-      if (has_dx) store8(static_cast<T*>(p.dx) + (size_t)row * p.D + c, dx);
+      if (has_dx) c.store(static_cast<T*>(p.dx) + here, dx);
       if (has_y) {
-        const F8 w = w_post(c), sc = scale(c), y = load8(aY + c);
+        const F8 w = w_post(c), sc = scale(c), y = c.load(aY);
         F8 dg;
-        const F8 g = kAct != kNoGate ? load8(aG + c) : fill8(0.f);
+        const F8 g = kAct != kNoGate ? c.load(aG) : fill8(0.f);
         float2 s = pair(0.f);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -393,7 +438,7 @@ __global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant_
           s = fma2(un[i].v[e], y.v[e], s);
         }
         se[i] = s.x + s.y;
-        if (kAct != kNoGate) store8(static_cast<T*>(p.dgate) + (size_t)row * p.D + c, dg);
+        if (kAct != kNoGate) c.store(static_cast<T*>(p.dgate) + here, dg);
       }
     }
     if (gl) {
@@ -410,17 +455,17 @@ __global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant_
     if (has_y) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int c = (i * tpr + t) * 8;
-        if (!live || c >= p.D) continue;
+        const C8 c(i, t, tpr, p.D);
+        if (!live || !c.any()) continue;
         const float k = -r1[i] * r1[i] * r1[i] * se[i] * p.inv_group;
-        const F8 y = load8(aY + c);
+        const F8 y = c.load(aY);
 #pragma unroll
         for (int e = 0; e < 4; ++e) un[i].v[e] = fma2(y.v[e], pair(k), mul2(un[i].v[e], pair(r1[i])));
-        store8(static_cast<T*>(p.dy) + (size_t)row * p.D + c, un[i]);
+        c.store(static_cast<T*>(p.dy) + here, un[i]);
       }
     }
     __syncthreads();  // every thread has read the stage (and red1, red2)
-    if (tid == 0 && step + (long long)stages * gridDim.x < steps) load(step + (long long)stages * gridDim.x, st);
+    if (!kOdd && tid == 0 && step + (long long)stages * gridDim.x < steps) load(step + (long long)stages * gridDim.x, st);
   }
   // partial sums of this CTA, the row slots combined in slot order
   float* part = p.part + (size_t)blockIdx.x * 3 * p.D;
@@ -430,18 +475,18 @@ __global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant_
     if (slot != s) continue;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = (i * tpr + t) * 8;
-      if (c >= p.D) continue;
+      const C8 c(i, t, tpr, p.D);
+      if (!c.any()) continue;
       const F8* from[3] = {&apre[i], &apost[i], &ascale[i]};
 #pragma unroll
       for (int k = 0; k < 3; ++k) {
         F8 x = *from[k];
         if (s) {
-          const F8 y = load8(acc + k * p.D + c);
+          const F8 y = c.load(acc + k * p.D);
 #pragma unroll
           for (int e = 0; e < 4; ++e) x.v[e] = add2(y.v[e], x.v[e]);
         }
-        store8(acc + k * p.D + c, x);
+        c.store(acc + k * p.D, x);
       }
     }
   }
@@ -477,8 +522,8 @@ __global__ void __launch_bounds__(32 * kSlices) bn_reduce_kernel(const __grid_co
 }
 
 // ---------------------------------------------------------------------------------
-// Any D up to kBnMaxD and any group that divides it: a CTA per row, values one by one.
-// The rsqrt of each group stays in shared memory; inputs are read again for each step
+// Any D up to kBnMaxD and any group that divides it, for the groups that are neither the row
+// nor whole vectors of a power of two: a CTA per row, values one by one.  The rsqrt of each group stays in shared memory; inputs are read again for each step
 // (from L1 or L2).
 // ---------------------------------------------------------------------------------
 constexpr int kAnyT = 256;
@@ -623,6 +668,7 @@ int ceil_pow2(int x) {
 // Lanes per group of y's norm when groups lie inside a warp's vectors; 0: the whole row is
 // one group; -1: neither.
 int group_lanes(const BnArgs& p) {
+  if (p.y && p.group == 1) return -1;  // the gradient of one value alone has its own form
   if (!p.y || p.group == p.D) return 0;
   const int n = p.group / 8;
   return p.group % 8 == 0 && n <= 32 && (n & (n - 1)) == 0 ? n : -1;
@@ -643,8 +689,8 @@ void with_act(const BnArgs& p, F f) {
 
 template <typename T>
 cudaError_t fwd(const BnArgs& p, cudaStream_t st) {
-  const int gl = group_lanes(p), nvec = p.D / 8;
-  if (p.D % 8 || gl < 0) {
+  const int gl = group_lanes(p), nvec = (p.D + 7) / 8;
+  if (gl < 0) {
     const int smem = p.y ? p.D / p.group * 4 : 0;
     static SmemLimit limit;
     const cudaError_t e = limit.raise(bn_fwd_any_kernel<T>, kBnMaxGroups * 4);
@@ -653,8 +699,10 @@ cudaError_t fwd(const BnArgs& p, cudaStream_t st) {
     return cudaGetLastError();
   }
   // With many rows, four vectors a thread (two in fp32): fewer threads a row, more rows on
-  // an SM at a time.  With few, one, for the shortest way through a row.
-  int nv = p.rows >= 4 * 152 && nvec >= 64 ? (sizeof(T) == 2 && nvec >= 128 ? 4 : 2) : 1;
+  // an SM at a time.  With few, one, for the shortest way through a row, and where rows are not
+  // whole vectors, for their single loads (20000 rows of 1119 in bf16: 143 us with one, 190
+  // with four; 37317 of 222: 33 us, of which memory needs 12).
+  int nv = p.D % 8 == 0 && p.rows >= 4 * 152 && nvec >= 64 ? (sizeof(T) == 2 && nvec >= 128 ? 4 : 2) : 1;
   while (nvec > 512 * nv) nv *= 2;
   int tpr = ceil_pow2((nvec + nv - 1) / nv);
   tpr = tpr < 32 ? 32 : tpr;
@@ -662,9 +710,14 @@ cudaError_t fwd(const BnArgs& p, cudaStream_t st) {
   const unsigned grid = (unsigned)((p.rows + R - 1) / R);
   with_act(p, [&](auto act) {
     constexpr int kAct = decltype(act)::value;
-    if (nv == 1) bn_fwd_kernel<T, 1, kAct><<<grid, threads, 0, st>>>(p, tpr, gl);
-    else if (nv == 2) bn_fwd_kernel<T, 2, kAct><<<grid, threads, 0, st>>>(p, tpr, gl);
-    else bn_fwd_kernel<T, 4, kAct><<<grid, threads, 0, st>>>(p, tpr, gl);
+    auto launch = [&](auto odd) {
+      constexpr bool kOdd = decltype(odd)::value;
+      if (nv == 1) bn_fwd_kernel<T, 1, kAct, kOdd><<<grid, threads, 0, st>>>(p, tpr, gl);
+      else if (nv == 2) bn_fwd_kernel<T, 2, kAct, kOdd><<<grid, threads, 0, st>>>(p, tpr, gl);
+      else bn_fwd_kernel<T, 4, kAct, kOdd><<<grid, threads, 0, st>>>(p, tpr, gl);
+    };
+    if (p.D % 8) launch(Int<1>());
+    else launch(Int<0>());
   });
   return cudaGetLastError();
 }
@@ -673,7 +726,8 @@ template <typename T, int NV>
 cudaError_t bwd_fast(const BnArgs& p, const BnBwdPlan& pl, int gl, cudaStream_t st) {
   const int nin = (p.dh ? 2 : 0) + (p.dx_new ? 1 : 0) + (p.y ? 1 : 0) + (p.gate ? 1 : 0);
   const size_t stage = (size_t)nin * (pl.threads / pl.tpr) * p.D * sizeof(T), acc = (size_t)3 * p.D * 4;
-  int stages = (int)((size_t)pl.smem / stage);
+  const bool odd = p.D % 8 != 0;
+  int stages = odd ? 0 : (int)((size_t)pl.smem / stage);
   stages = stages > kBwdMaxStages ? kBwdMaxStages : stages;
   const size_t smem = stage * stages > acc ? stage * stages : acc;
   const bool base = p.dx_new && p.y && p.w_post;
@@ -686,12 +740,13 @@ cudaError_t bwd_fast(const BnArgs& p, const BnBwdPlan& pl, int gl, cudaStream_t 
       kernel<<<pl.ctas, pl.threads, smem, st>>>(p, pl.tpr, gl, stages);
       e = cudaGetLastError();
     };
-    static SmemLimit limits[3];
+    static SmemLimit limits[4];
+    if (odd) return launch(bn_bwd_kernel<T, NV, kAct, kAny, true>, limits[3]);
     if constexpr (kAct == kNoGate || kAct == BN_SILU) {  // the activations in use have their own kernels
-      if (args == kJoint) return launch(bn_bwd_kernel<T, NV, kAct, kJoint>, limits[0]);
-      if (args == kHeads) return launch(bn_bwd_kernel<T, NV, kAct, kHeads>, limits[1]);
+      if (args == kJoint) return launch(bn_bwd_kernel<T, NV, kAct, kJoint, false>, limits[0]);
+      if (args == kHeads) return launch(bn_bwd_kernel<T, NV, kAct, kHeads, false>, limits[1]);
     }
-    launch(bn_bwd_kernel<T, NV, kAct, kAny>, limits[2]);
+    launch(bn_bwd_kernel<T, NV, kAct, kAny, false>, limits[2]);
   });
   return e;
 }
@@ -728,8 +783,8 @@ cudaError_t bwd(const BnArgs& p, cudaStream_t st) {
 // gradients in the workspace).
 BnBwdPlan bn_bwd_plan(const BnArgs& p, bool bf16) {
   BnBwdPlan pl{};
-  const int nvec = p.D / 8, e = bf16 ? 2 : 4;
-  pl.nv = nvec <= 32 ? 1 : 2;
+  const int nvec = (p.D + 7) / 8, e = bf16 ? 2 : 4;
+  pl.nv = nvec <= (p.D % 8 ? 256 : 32) ? 1 : 2;
   pl.tpr = ceil_pow2((nvec + pl.nv - 1) / pl.nv);
   pl.tpr = pl.tpr < 32 ? 32 : pl.tpr;
   pl.threads = pl.tpr <= 256 ? 256 : 512;
@@ -737,7 +792,7 @@ BnBwdPlan bn_bwd_plan(const BnArgs& p, bool bf16) {
   const long long stage = 5LL * (pl.threads / pl.tpr) * p.D * e;
   const int per_sm = pl.threads == 256 && 2 * stage <= kBnBwdSmem ? 2 : 1;
   pl.smem = kBnBwdSmem / per_sm;
-  pl.fast = p.D % 8 == 0 && nvec <= 1024 && group_lanes(p) >= 0 && stage <= pl.smem;
+  pl.fast = nvec <= 1024 && group_lanes(p) >= 0 && stage <= pl.smem;
   const long long steps = pl.fast ? (p.rows + pl.threads / pl.tpr - 1) / (pl.threads / pl.tpr) : p.rows;
   const int most = pl.fast ? 152 * per_sm : kBnMaxParts;
   pl.ctas = (int)(steps < most ? steps : most);
