@@ -86,12 +86,26 @@ T* ptr(const at::Tensor& x) {
 }
 at::Tensor given_or_like(const at::Tensor& x, const at::Tensor& like) { return x.defined() ? x : at::empty_like(like); }
 
-void* stream_of(PyObject* s, int device) {
-  if (s == Py_None) return c10::cuda::getCurrentCUDAStream(device).stream();
-  void* p = PyLong_AsVoidPtr(s);
-  if (!p && PyErr_Occurred()) throw Raised{};
-  return p;
-}
+// Where a call runs: the device and stream, both current while it allocates.  Memory that the
+// caching allocator hands out belongs to the current stream; were it another one than the
+// call's, a result could take the place of what that stream still reads, and a workspace
+// could be handed on while the call still uses it.
+struct Target {
+  c10::cuda::CUDAGuard device;
+  c10::cuda::OptionalCUDAStreamGuard stream;
+  void* handle;
+  Target(PyObject* s, int index) : device(static_cast<c10::DeviceIndex>(index)) {
+    const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index));
+    handle = current.stream();
+    if (s == Py_None) return;
+    void* given = PyLong_AsVoidPtr(s);
+    if (!given && PyErr_Occurred()) throw Raised{};
+    if (given == handle) return;
+    handle = given;
+    stream.reset_stream(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(given),
+                                                         static_cast<c10::DeviceIndex>(index)));
+  }
+};
 void check_status(ll_status st, const char* where) {
   if (st == LL_OK) return;
   PyObject* e = PyObject_CallFunction(error_class, "is", static_cast<int>(st), where);
@@ -197,14 +211,13 @@ PyObject* py_lindecay_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     check(s_in, "state_in", l.state_sizes(), at::kFloat, l.device);
     check(s_out, "state_out", l.state_sizes(), at::kFloat, l.device);
     check(o_given, "o", v.sizes(), v.scalar_type(), l.device);
-    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(l.device));
+    const Target on(a[9], l.device);
     const at::Tensor ws = workspace_of(a[8], entry.fwd_bytes(&l.shape), l.device, "lindecay_fwd");
     const at::Tensor o = given_or_like(o_given, v);
-    void* st = stream_of(a[9], l.device);
     ll_status r;
     Py_BEGIN_ALLOW_THREADS
     r = entry.fwd(&l.shape, ptr(q), ptr(k), ptr(v), ptr<float>(log_a), ptr<int>(lengths), ptr<float>(s_in), ptr(o),
-                  ptr<float>(s_out), ptr(ws), bytes_of(ws), st);
+                  ptr<float>(s_out), ptr(ws), bytes_of(ws), on.handle);
     Py_END_ALLOW_THREADS
     check_status(r, "lindecay_fwd");
     return wrap(o);
@@ -223,14 +236,13 @@ PyObject* py_lindecay_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     check(s_in, "state_in", l.state_sizes(), at::kFloat, l.device);
     check(ds_out, "dstate_out", l.state_sizes(), at::kFloat, l.device);
     check(ds_in, "dstate_in", l.state_sizes(), at::kFloat, l.device);
-    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(l.device));
+    const Target on(a[10], l.device);
     const at::Tensor ws = workspace_of(a[9], entry.bwd_bytes(&l.shape), l.device, "lindecay_bwd");
     const at::Tensor dq = at::empty_like(q), dk = at::empty_like(k), dv = at::empty_like(v);
-    void* st = stream_of(a[10], l.device);
     ll_status r;
     Py_BEGIN_ALLOW_THREADS
     r = entry.bwd(&l.shape, ptr(q), ptr(k), ptr(v), ptr<float>(log_a), ptr<int>(lengths), ptr<float>(s_in), ptr(dO),
-                  ptr<float>(ds_out), ptr(dq), ptr(dk), ptr(dv), ptr<float>(ds_in), ptr(ws), bytes_of(ws), st);
+                  ptr<float>(ds_out), ptr(dq), ptr(dk), ptr(dv), ptr<float>(ds_in), ptr(ws), bytes_of(ws), on.handle);
     Py_END_ALLOW_THREADS
     check_status(r, "lindecay_bwd");
     return wrap_all({dq, dk, dv});
@@ -245,12 +257,11 @@ PyObject* py_lindecay_decode_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Lin l = lin_checked(q, k, v, log_a, 1);
     check(states, "states", l.state_sizes(), at::kFloat, l.device);
     check(o_given, "o_t", v.sizes(), v.scalar_type(), l.device);
-    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(l.device));
+    const Target on(a[6], l.device);
     const at::Tensor o = given_or_like(o_given, v);
-    void* st = stream_of(a[6], l.device);
     ll_status r;
     Py_BEGIN_ALLOW_THREADS
-    r = entry.step(&l.shape, ptr(q), ptr(k), ptr(v), ptr<float>(log_a), ptr(o), ptr<float>(states), st);
+    r = entry.step(&l.shape, ptr(q), ptr(k), ptr(v), ptr<float>(log_a), ptr(o), ptr<float>(states), on.handle);
     Py_END_ALLOW_THREADS
     check_status(r, "lindecay_decode_step");
     return wrap(o);
@@ -302,14 +313,13 @@ PyObject* py_blocknorm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
       if (!w_pre.defined() && !h_given.defined())
         refuse(PyExc_ValueError, "nothing to compute: neither y nor w_pre is given");
     }
-    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(device));
+    const Target on(a[11], device);
     const at::Tensor xn = y.defined() ? given_or_like(xn_given, first) : at::Tensor();
     const at::Tensor h = w_pre.defined() ? given_or_like(h_given, first) : h_given;
-    void* st = stream_of(a[11], device);
     ll_status r;
     Py_BEGIN_ALLOW_THREADS
     r = entry.bn_fwd(&s, ptr(x), ptr(y), ptr(gate), ptr<float>(w_post), ptr<float>(scale), ptr<float>(w_pre), ptr(xn),
-                     ptr(h), st);
+                     ptr(h), on.handle);
     Py_END_ALLOW_THREADS
     check_status(r, "blocknorm_fwd");
     return wrap_all({y.defined() ? xn : x, h});
@@ -339,17 +349,16 @@ PyObject* py_blocknorm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     check(scale, "scale", weights, at::kFloat, device);
     check(w_pre, "w_pre", weights, at::kFloat, device);
     const bool residual = a[11] == Py_None ? !y.defined() || scale.defined() || x_new.defined() : a[11] == Py_True;
-    const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(device));
+    const Target on(a[13], device);
     const at::Tensor ws = workspace_of(a[12], entry.bn_bytes(&s), device, "blocknorm_bwd");
     const auto like = [](const at::Tensor& x) { return x.defined() ? at::empty_like(x) : at::Tensor(); };
     const at::Tensor dx = residual ? at::empty_like(first) : at::Tensor(), dy = like(y), dgate = like(gate),
                      dw_post = like(w_post), dscale = like(scale), dw_pre = like(w_pre);
-    void* st = stream_of(a[13], device);
     ll_status r;
     Py_BEGIN_ALLOW_THREADS
     r = entry.bn_bwd(&s, ptr(dx_new), ptr(dh), ptr(x_new), ptr(y), ptr(gate), ptr<float>(w_post), ptr<float>(scale),
                      ptr<float>(w_pre), ptr(dx), ptr(dy), ptr(dgate), ptr<float>(dw_post), ptr<float>(dscale),
-                     ptr<float>(dw_pre), ptr(ws), bytes_of(ws), st);
+                     ptr<float>(dw_pre), ptr(ws), bytes_of(ws), on.handle);
     Py_END_ALLOW_THREADS
     check_status(r, "blocknorm_bwd");
     return wrap_all({dx, dy, dgate, dw_post, dscale, dw_pre});

@@ -358,3 +358,23 @@ def test_refusals(sml):
     with pytest.raises(sml.LogLinearError, match="LL_ERR_ALIGN"):
         sml.lindecay_fwd(*bad(2, odd))
     assert sml.loglinear_check_status() == 0
+
+
+def test_memory_of_a_call_on_a_given_stream(sml):
+    """A result allocated by a call on another stream does not take the place of memory that
+    the current stream still has to read."""
+    d = on_gpu(draw(1, 30000, 4, 1, 64, 64, torch.bfloat16, seed=7))
+    s = torch.cuda.Stream()
+    first = sml.lindecay_fwd(d["q"], d["k"], d["v"], d["log_a"])
+    torch.ones_like(d["v"]).sum(dtype=torch.float32)
+    torch.cuda._sleep(100)  # every kernel is loaded: nothing below waits for that
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    pending = torch.ones_like(d["v"])
+    torch.cuda._sleep(50_000_000)  # some 25 ms, ahead of the sum
+    total = pending.sum(dtype=torch.float32)
+    del pending
+    o = sml.lindecay_fwd(d["q"], d["k"], d["v"], d["log_a"], stream=s)
+    s.synchronize()
+    assert torch.equal(o, first)
+    assert float(total) == d["v"].numel()
