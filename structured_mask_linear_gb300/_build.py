@@ -75,7 +75,7 @@ def _native_command(out: str):
     paths = [sysconfig.get_paths()["include"], INCLUDE, os.path.join(cuda, "include")] + cpp_extension.include_paths()
     return ([cxx, "-shared", "-fPIC", "-O2", "-std=c++17", BINDING, "-o", out] + [f"-I{p}" for p in paths] +
             [f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f"-L{lib}", f"-Wl,-rpath,{lib}",
-             "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"])
+             "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"])
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

@@ -6,8 +6,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
-#include <ATen/ops/empty_like.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -84,7 +83,11 @@ template <typename T = void>
 T* ptr(const at::Tensor& x) {
   return x.defined() ? static_cast<T*>(x.data_ptr()) : nullptr;
 }
-at::Tensor given_or_like(const at::Tensor& x, const at::Tensor& like) { return x.defined() ? x : at::empty_like(like); }
+// A new contiguous tensor like x (undefined for undefined), without the dispatcher's steps.
+at::Tensor new_like(const at::Tensor& x) {
+  return x.defined() ? at::Tensor(at::detail::empty_cuda(x.sizes(), x.scalar_type(), x.device(), std::nullopt)) : at::Tensor();
+}
+at::Tensor given_or_like(const at::Tensor& x, const at::Tensor& like) { return x.defined() ? x : new_like(like); }
 
 // Where a call runs: the device and stream, both current while it allocates.  Memory that the
 // caching allocator hands out belongs to the current stream; were it another one than the
@@ -121,8 +124,9 @@ at::Tensor workspace_of(PyObject* given, size_t need, int device, const char* wh
   const at::Tensor& w = tensor(given, "workspace", true);
   if (!w.defined())
     return need <= 16 ? at::Tensor()
-                      : at::empty({static_cast<int64_t>(need)}, at::TensorOptions().dtype(at::kByte).device(
-                                                                     at::kCUDA, static_cast<c10::DeviceIndex>(device)));
+                      : at::Tensor(at::detail::empty_cuda({static_cast<int64_t>(need)}, at::kByte,
+                                                          c10::Device(at::kCUDA, static_cast<c10::DeviceIndex>(device)),
+                                                          std::nullopt));
   if (!w.is_cuda() || w.get_device() != device || !w.is_contiguous())
     refuse(PyExc_ValueError, "workspace must be a contiguous tensor on cuda:" + std::to_string(device));
   return w;
@@ -238,7 +242,7 @@ PyObject* py_lindecay_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     check(ds_in, "dstate_in", l.state_sizes(), at::kFloat, l.device);
     const Target on(a[10], l.device);
     const at::Tensor ws = workspace_of(a[9], entry.bwd_bytes(&l.shape), l.device, "lindecay_bwd");
-    const at::Tensor dq = at::empty_like(q), dk = at::empty_like(k), dv = at::empty_like(v);
+    const at::Tensor dq = new_like(q), dk = new_like(k), dv = new_like(v);
     ll_status r;
     Py_BEGIN_ALLOW_THREADS
     r = entry.bwd(&l.shape, ptr(q), ptr(k), ptr(v), ptr<float>(log_a), ptr<int>(lengths), ptr<float>(s_in), ptr(dO),
@@ -351,9 +355,8 @@ PyObject* py_blocknorm_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const bool residual = a[11] == Py_None ? !y.defined() || scale.defined() || x_new.defined() : a[11] == Py_True;
     const Target on(a[13], device);
     const at::Tensor ws = workspace_of(a[12], entry.bn_bytes(&s), device, "blocknorm_bwd");
-    const auto like = [](const at::Tensor& x) { return x.defined() ? at::empty_like(x) : at::Tensor(); };
-    const at::Tensor dx = residual ? at::empty_like(first) : at::Tensor(), dy = like(y), dgate = like(gate),
-                     dw_post = like(w_post), dscale = like(scale), dw_pre = like(w_pre);
+    const at::Tensor dx = residual ? new_like(first) : at::Tensor(), dy = new_like(y), dgate = new_like(gate),
+                     dw_post = new_like(w_post), dscale = new_like(scale), dw_pre = new_like(w_pre);
     ll_status r;
     Py_BEGIN_ALLOW_THREADS
     r = entry.bn_bwd(&s, ptr(dx_new), ptr(dh), ptr(x_new), ptr(y), ptr(gate), ptr<float>(w_post), ptr<float>(scale),
