@@ -2,6 +2,8 @@
 // is split into units of work, workspace layout.  Contracts are in include/loglinear.h.
 #include <cuda_runtime.h>
 
+#include <initializer_list>
+
 #include "lindecay.cuh"
 
 namespace {
@@ -39,6 +41,7 @@ ll_status check_seq_shape(const ll_shape* s) {
 struct Plan {
   LinArgs args;
   size_t off_seg[ll::kLinProbs], off_scratch, off_hand, off_flag, bytes;
+  double est;  // time, in chunks of a wide scan
 };
 
 // How the units become work items, by estimated time in eighths of what a chunk of a wide
@@ -51,7 +54,8 @@ struct Plan {
 //    start per item (kItem) and the prefix over the segments (kSeg each).
 // With many units the first needs no extra pass; with fewer than SMs only the second gives
 // every SM work.
-void cut_units(LinArgs& p, bool bf16) {
+// Returns the estimate, in such chunks.
+double cut_units(LinArgs& p, bool bf16) {
   constexpr double kState = 0.6, kLaunch = 4.0, kItem = 1.0, kSeg = 0.1;
   int units = 0, nh_tail = 1;
   long long line = 0, longest = 0;
@@ -98,7 +102,9 @@ void cut_units(LinArgs& p, bool bf16) {
   }
   // the wait for a part's state is bounded by seconds: not for sequences whose parts may take that
   const long long even = (line + kSms - 1) / kSms, turn = even > longest ? even : longest;
-  if (bf16 && units > kSms && units % kSms != 0 && p.NC <= (1 << 17) && turn / 8.0 + 1.0 < head + tail && all_sms()) {
+  double est = head + tail;
+  if (bf16 && units > kSms && units % kSms != 0 && p.NC <= (1 << 17) && turn / 8.0 + 1.0 < est && all_sms()) {
+    est = turn / 8.0 + 1.0;
     p.turn = turn;
     p.total = line / abreast;
     p.abreast = abreast;
@@ -117,6 +123,7 @@ void cut_units(LinArgs& p, bool bf16) {
     r.sunit0 = p.sitems;
     p.sitems += r.nsplit * r.nh * (p.nseg - 1);
   }
+  return est;
 }
 
 // Completes a plan whose scans' head counts, widths and directions are set.
@@ -139,7 +146,7 @@ void finish_plan(const ll_shape* s, Plan* pl) {
     p.pr[i].nh = p.pr[i].oh == p.H ? 1 : p.hpg;
     grouped = grouped || p.pr[i].nh > 1;
   }
-  cut_units(p, bf16);
+  pl->est = cut_units(p, bf16);
   size_t off = 0;
   for (int i = 0; i < p.nprob; ++i) {
     const LinProb& r = p.pr[i];
@@ -180,21 +187,34 @@ void plan_fwd(const ll_shape* s, const void* q, const void* k, const void* v, vo
   finish_plan(s, pl);
 }
 
-// The gradients' three scans: in one launch, or in two where the tensor-core kernels pad d_k
-// and d_v to different widths (dq and dk run over d_v, dv over d_k).  Returns the number of
-// launches; they run one after the other and share the workspace.
+// The gradients' three scans.  Where the tensor-core kernels pad d_k and d_v to different
+// widths (dq and dk run over d_v, dv over d_k) either in one launch, whose stages are laid out
+// for the wider (narrow chunks then take 15 % longer), or in two, each with its own remainder
+// after the last whole turn of the SMs, whichever is estimated to be shorter.  For d_k = 128,
+// d_v = 64, one and two launches: 13 and 25 us (2 x 500 tokens, 8 heads), 120 and 136 (8192, 16),
+// 439 and 421 (2 x 8192, 48 in pairs).  Returns the number of launches; they run one after the
+// other and share the workspace.
 int plan_bwd(const ll_shape* s, const void* q, const void* k, const void* v, const void* dO, void* dq, void* dk,
              void* dv, Plan* pl) {
+  constexpr double kMixed = 1.15, kLaunch = 2.0;
   const int H = s->heads, G = H / s->heads_per_group;
-  const int n = s->dtype == LL_BF16 && (s->d_k > 64) != (s->d_v > 64) ? 2 : 1;
-  pl[0].args = pl[1].args = LinArgs{};
-  pl[0].args.pr[0] = scan(dO, H, v, H, k, G, dq, G, s->d_v, s->d_k, 0);
-  pl[0].args.pr[1] = scan(v, H, dO, H, q, G, dk, G, s->d_v, s->d_k, 1);
-  (n == 2 ? pl[1].args.pr[0] : pl[0].args.pr[2]) = scan(k, G, q, G, dO, H, dv, H, s->d_k, s->d_v, 1);
-  pl[0].args.nprob = n == 2 ? 2 : 3;
-  pl[1].args.nprob = 1;
-  for (int i = 0; i < n; ++i) finish_plan(s, &pl[i]);
-  return n;
+  const LinProb pq = scan(dO, H, v, H, k, G, dq, G, s->d_v, s->d_k, 0),
+                pk = scan(v, H, dO, H, q, G, dk, G, s->d_v, s->d_k, 1),
+                pv = scan(k, G, q, G, dO, H, dv, H, s->d_k, s->d_v, 1);
+  auto plan = [&](Plan& x, std::initializer_list<LinProb> scans) {
+    x.args = LinArgs{};
+    for (const LinProb& r : scans) x.args.pr[x.args.nprob++] = r;
+    finish_plan(s, &x);
+  };
+  plan(pl[0], {pq, pk, pv});
+  if (s->dtype != LL_BF16 || (s->d_k > 64) == (s->d_v > 64)) return 1;
+  Plan a, b;
+  plan(a, {pq, pk});
+  plan(b, {pv});
+  if (pl[0].est * kMixed <= a.est + b.est + kLaunch) return 1;
+  pl[0] = a;
+  pl[1] = b;
+  return 2;
 }
 size_t bwd_bytes(const Plan* pl, int n) { return n == 2 && pl[1].bytes > pl[0].bytes ? pl[1].bytes : pl[0].bytes; }
 
