@@ -45,7 +45,8 @@ struct Plan {
 };
 
 // How the units become work items, by estimated time in eighths of what a chunk of a wide
-// scan (a > 64) takes on one SM (about 1.9 us):
+// scan (a > 64) takes on one SM (2 us in bf16; 8 us in fp32, where launches and starts weigh
+// less: 2 x 400 tokens, 8 heads of 64 59 -> 19.5 us, 4 x 1000, 16 of 64 133 -> 95):
 //  - wrapped: every SM gets an equal share of the line of units, or the longest unit's time
 //    where that is more.  Tensor cores only.
 //  - segmented: whole units in turn, the last incomplete turn's (all of them when there are
@@ -56,7 +57,7 @@ struct Plan {
 // every SM work.
 // Returns the estimate, in such chunks.
 double cut_units(LinArgs& p, bool bf16) {
-  constexpr double kState = 0.6, kLaunch = 4.0, kItem = 1.0, kSeg = 0.1;
+  const double kState = bf16 ? 0.6 : 0.4, kLaunch = bf16 ? 4.0 : 1.0, kItem = bf16 ? 1.0 : 0.5, kSeg = bf16 ? 0.1 : 0.05;
   int units = 0, nh_tail = 1;
   long long line = 0, longest = 0;
   int abreast = 8;  // divides the 152 SMs
