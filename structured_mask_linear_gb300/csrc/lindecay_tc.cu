@@ -26,11 +26,13 @@
 // them: what is left of a term is below 2^-15 of it, 4e-6 in the mean square.  R itself is
 // carried in fp32.
 //
-// Bound: shared memory.  An item of a = 128 moves 64 KB for S, 64 for Ob, 64 for D, 16 for Oa,
-// 80 for the loads, 48 for w Z, 32 for R's parts, 32 for the tile's way out and some 20 for
-// P's weights: 420 KB, 3300 cycles of an SM, against 2000 of tensor cores; 3500 are measured.
-// Hence Ob's and D's two parts side by side in one product of 128 columns where tensor memory
-// has the room (each reads its left operand once).
+// Bound: memory, where every SM holds a head's whole sequence (152 heads of 64 and 64, 8192
+// tokens: 105 us, 89 % of the copy rate; of 128 and 64: 151 us, 93 %); elsewhere the way of a
+// chunk through the roles, of which two are under way at a time: 2.1 to 2.3 us a chunk of a =
+// 128, with the tensor cores active for 37 % of it and shared memory's banks for 30 (4 x 8192
+// tokens, 48 heads in pairs: 188 us, 64 % of the copy rate).  Ob's and D's two parts lie side
+// by side in one product of 128 columns where tensor memory has the room: each then reads its
+// left operand once.
 //
 // Warp roles (640 threads, five warpgroups; each keeps to one part of the chain, so that the
 // parts of consecutive chunks overlap):
