@@ -86,22 +86,28 @@ struct Eight {
   __device__ __forceinline__ Eight(int i, int t, int tpr, int D) : c(kOdd ? i * 8 * tpr + t : (i * tpr + t) * 8), step(tpr), D(D) {}
   __device__ __forceinline__ bool any() const { return c < D; }
   __device__ __forceinline__ uint4 raw(const __nv_bfloat16* p) const {
-    if (!kOdd) return raw8(p + c);
-    uint32_t w[4];
+    if constexpr (!kOdd) {
+      return raw8(p + c);
+    } else {
+      uint32_t w[4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const unsigned short* q = reinterpret_cast<const unsigned short*>(p) + c + 2 * e * step;
-      const uint32_t lo = c + 2 * e * step < D ? q[0] : 0u, hi = c + (2 * e + 1) * step < D ? q[step] : 0u;
-      w[e] = lo | hi << 16;
+      for (int e = 0; e < 4; ++e) {
+        const unsigned short* q = reinterpret_cast<const unsigned short*>(p) + c + 2 * e * step;
+        const uint32_t lo = c + 2 * e * step < D ? q[0] : 0u, hi = c + (2 * e + 1) * step < D ? q[step] : 0u;
+        w[e] = lo | hi << 16;
+      }
+      return make_uint4(w[0], w[1], w[2], w[3]);
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
   }
   __device__ __forceinline__ RawF raw(const float* p) const {
-    if (!kOdd) return raw8(p + c);
-    float w[8];
+    if constexpr (!kOdd) {
+      return raw8(p + c);
+    } else {
+      float w[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = c + e * step < D ? p[c + e * step] : 0.f;
-    return {make_float4(w[0], w[1], w[2], w[3]), make_float4(w[4], w[5], w[6], w[7])};
+      for (int e = 0; e < 8; ++e) w[e] = c + e * step < D ? p[c + e * step] : 0.f;
+      return {make_float4(w[0], w[1], w[2], w[3]), make_float4(w[4], w[5], w[6], w[7])};
+    }
   }
   template <typename T>
   __device__ __forceinline__ F8 load(const T* p) const {
@@ -110,10 +116,13 @@ struct Eight {
   __device__ __forceinline__ F8 weight(const float* w) const { return w ? load(w) : fill8(1.f); }
   template <typename T>
   __device__ __forceinline__ void store(T* p, const F8& x) const {
-    if (!kOdd) return store8(p + c, x);
+    if constexpr (!kOdd) {
+      store8(p + c, x);
+    } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (c + e * step < D) ll_store(p, c + e * step, e & 1 ? x.v[e >> 1].y : x.v[e >> 1].x);
+      for (int e = 0; e < 8; ++e)
+        if (c + e * step < D) ll_store(p, c + e * step, e & 1 ? x.v[e >> 1].y : x.v[e >> 1].x);
+    }
   }
 };
 __device__ __forceinline__ float sum8(const F8& x) {
@@ -305,6 +314,7 @@ template <typename T, int NV, int kAct, int kArgs, bool kOdd>
 __global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant__ BnArgs p, int tpr, int gl, int stages) {
   extern __shared__ __align__(128) uint8_t sm[];
   __shared__ __align__(8) uint64_t full[kBwdMaxStages];
+  ptx::launch_dependents();
   __shared__ float red1[3 * (kBwdMaxT / 32)], red2[kBwdMaxT / 32];
   const int tid = threadIdx.x, t = tid & (tpr - 1), slot = tid / tpr, R = blockDim.x / tpr;
   const T* in[5] = {static_cast<const T*>(p.dh), static_cast<const T*>(p.x), static_cast<const T*>(p.dx_new),
@@ -468,6 +478,7 @@ __global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant_
     if (!kOdd && tid == 0 && step + (long long)stages * gridDim.x < steps) load(step + (long long)stages * gridDim.x, st);
   }
   // partial sums of this CTA, the row slots combined in slot order
+  const bool asked[3] = {p.dw_pre != nullptr, p.dw_post != nullptr, p.dscale != nullptr};
   float* part = p.part + (size_t)blockIdx.x * 3 * p.D;
   float* acc = reinterpret_cast<float*>(sm);  // 3 x D: the ring is free (every copy was waited for)
   for (int s = 0; s < R; ++s) {
@@ -480,6 +491,7 @@ __global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant_
       const F8* from[3] = {&apre[i], &apost[i], &ascale[i]};
 #pragma unroll
       for (int k = 0; k < 3; ++k) {
+        if (!asked[k]) continue;
         F8 x = *from[k];
         if (s) {
           const F8 y = c.load(acc + k * p.D);
@@ -491,7 +503,10 @@ __global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant_
     }
   }
   __syncthreads();
-  for (int c = tid; c < 3 * p.D; c += blockDim.x) part[c] = acc[c];
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    if (asked[k])
+      for (int c = tid; c < p.D; c += blockDim.x) part[k * p.D + c] = acc[k * p.D + c];
 }
 
 // Sums of the CTAs' partials, in order: 32 columns x 32 slices of the parts per CTA, so that
@@ -504,6 +519,7 @@ __global__ void __launch_bounds__(32 * kSlices) bn_reduce_kernel(const __grid_co
   int which = -1;
   for (int i = 0, n = (int)blockIdx.y; i < 3; ++i)
     if (outs[i] && n-- == 0) which = i;
+  ptx::wait_for_prerequisites();  // launched while the partials are still being made
   const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
   const int per = (nparts + kSlices - 1) / kSlices, p0 = sl * per;
   float x[kPerSlice], s = 0.f;
@@ -770,8 +786,16 @@ cudaError_t bwd(const BnArgs& p, cudaStream_t st) {
   note_launch();
   if (p.dw_pre || p.dw_post || p.dscale) {
     const int outs = (p.dw_pre ? 1 : 0) + (p.dw_post ? 1 : 0) + (p.dscale ? 1 : 0);
-    bn_reduce_kernel<<<dim3((p.D + 31) / 32, outs), 32 * kSlices, 0, st>>>(p, pl.ctas);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((p.D + 31) / 32, outs);
+    cfg.blockDim = dim3(32 * kSlices);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    if ((e = cudaLaunchKernelEx(&cfg, bn_reduce_kernel, p, pl.ctas)) != cudaSuccess) return e;
     note_launch();
   }
   return cudaSuccess;
