@@ -17,6 +17,8 @@ namespace {
 // and are issued eight at a time, a batch ahead.
 // ---------------------------------------------------------------------------------
 __global__ void __launch_bounds__(256) lin_scan_kernel(const __grid_constant__ LinArgs p) {
+  ptx::launch_dependents();
+  ptx::wait_for_prerequisites();  // launched while the totals are still being made
   const LinProb& r = p.pr[blockIdx.y];
   const int n4 = r.a * (kLinTile / 4);
   const long long e = (long long)blockIdx.x * 256 + threadIdx.x;
@@ -149,6 +151,8 @@ template <bool kStateOnly>
 __global__ void __launch_bounds__(kF, 1) lin_f32_kernel(const __grid_constant__ LinArgs p) {
   extern __shared__ float4 smem4[];
   F32Smem& sm = *reinterpret_cast<F32Smem*>(smem4);
+  if (kStateOnly) ptx::launch_dependents();
+  else ptx::wait_for_prerequisites();  // segments' start states
   const int tid = threadIdx.x, warp = tid >> 5, g = (tid & 31) >> 2, t4 = tid & 3;
   const int wm = (warp & 3) * 16, wn = (warp >> 2) * 8 * kNt;  // this warp's part of a 64 x 64 tile
   int head0 = 0;
@@ -402,14 +406,29 @@ __global__ void __launch_bounds__(kStepT) lin_step_kernel(LinStepArgs d) {
 
 }  // namespace
 
+// A launch that may start while the kernel before it ends.
+static cudaLaunchConfig_t dependent_launch(dim3 grid, int threads, int smem, cudaStream_t st, cudaLaunchAttribute* at) {
+  at->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at->val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
 cudaError_t launch_lin_scan(const LinArgs& p, cudaStream_t st) {
   long long most = 0;
   for (int i = 0; i < p.nprob; ++i) {
     const long long n = (long long)p.pr[i].nsplit * p.pr[i].nh * p.pr[i].a * (kLinTile / 4);
     most = n > most ? n : most;
   }
-  lin_scan_kernel<<<dim3((unsigned)((most + 255) / 256), p.nprob), 256, 0, st>>>(p);
-  cudaError_t e = cudaGetLastError();
+  cudaLaunchAttribute at[1];
+  const cudaLaunchConfig_t cfg = dependent_launch(dim3((unsigned)((most + 255) / 256), p.nprob), 256, 0, st, at);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, lin_scan_kernel, p);
   if (e == cudaSuccess) note_launch();
   return e;
 }
@@ -427,8 +446,10 @@ cudaError_t launch_lin_f32(LinArgs& p, cudaStream_t st) {
   }
   static SmemLimit limit;
   if ((e = limit.raise(lin_f32_kernel<false>, smem)) != cudaSuccess) return e;
-  lin_f32_kernel<false><<<p.items, kF, smem, st>>>(p);
-  if ((e = cudaGetLastError()) == cudaSuccess) note_launch();
+  cudaLaunchAttribute at[1];
+  cudaLaunchConfig_t cfg = dependent_launch(dim3(p.items), kF, smem, st, at);
+  if (p.nseg == 1) cfg.numAttrs = 0;
+  if ((e = cudaLaunchKernelEx(&cfg, lin_f32_kernel<false>, p)) == cudaSuccess) note_launch();
   return e;
 }
 
