@@ -82,6 +82,10 @@ __global__ void __launch_bounds__(256) lin_scan_kernel(const __grid_constant__ L
 //
 // Tile strides make the fragment loads free of bank conflicts: 4 mod 32 for operands that
 // run along a row with k, 8 mod 32 for those that run along a row with n.
+//
+// Bound: fragments.  Each step of 8 along k loads and splits eight values a lane for six
+// instructions, which alone would run at 294 TFLOP/s (measured): 18 us of the 80 us for a padded
+// batch of 3 x 1501 tokens, 8 heads of 128 and 64 (138 us with products on the CUDA cores).
 // ---------------------------------------------------------------------------------
 constexpr int kF = 512;
 constexpr int kC32 = kLinChunk32;
@@ -324,7 +328,8 @@ __global__ void __launch_bounds__(kF, 1) lin_f32_kernel(const __grid_constant__ 
 // lin_step: one token.  S <- g S + k vᵀ, o = Sᵀ q, one pass over the fp32 states, which is
 // all it costs (2 x 4 dk dv bytes per head against a few hundred for the rest).  A CTA
 // takes 32 columns of a head's state: its threads load them (8 float4 columns x 16 rows at
-// a time, up to 8 loads in flight a thread) before anything waits for q and k.
+// a time, up to 8 loads in flight a thread) before anything waits for q and k.  64 users of
+// 48 heads of 128 and 64: 33.6 us, 6.05 TB/s, 89 % of the copy rate; one user 2.1 us.
 // ---------------------------------------------------------------------------------
 constexpr int kStepT = 128;
 constexpr int kStepRows = kStepT / 8;
