@@ -80,29 +80,36 @@ __global__ void __launch_bounds__(256) lin_scan_kernel(const __grid_constant__ L
 // would need them there in 16 or 11 bits, both parts: twice the space) and are split in
 // registers, so the warp-level instruction (m16n8k8) is used.
 //
-// Tile strides make the fragment loads free of bank conflicts: 4 mod 32 for operands that
-// run along a row with k, 8 mod 32 for those that run along a row with n.
+// Tile strides make the fragment loads free of bank conflicts: 8 mod 32 for operands that
+// run along a row with k (two values at a time), 4 mod 32 for those that run along a row with
+// n.  Y does both and has the second: its two-value loads take two turns.
 //
-// Bound: fragments.  Each step of 8 along k loads and splits eight values a lane for six
-// instructions, which alone would run at 294 TFLOP/s (measured): 18 us of the 80 us for a padded
-// batch of 3 x 1501 tokens, 8 heads of 128 and 64 (138 us with products on the CUDA cores).
+// Bound: the instructions around the products.  Each step of 8 along k loads and splits eight
+// values a lane for six products; the schedulers issue in half of the cycles, the tensor cores
+// work in 30 % (their rate for this instruction: 294 TFLOP/s measured), the barriers between a
+// chunk's four products take most of the rest.  A padded batch of 3 x 1501 tokens, 8 heads of
+// 128 and 64: 78 us (138 with the products on the CUDA cores); 20000 tokens, 4 heads of 128 and
+// 128: 300 us.
 // ---------------------------------------------------------------------------------
 constexpr int kF = 512;
 constexpr int kC32 = kLinChunk32;
-constexpr int kLdX = 132, kLdZ = 72, kLdP = 68;
+constexpr int kLdX = 136, kLdY = 132, kLdZ = 68, kLdP = 72;
 struct F32Smem {
   float X[2][kC32 * kLdX];
-  float Y[2][kC32 * kLdX];
+  float Y[2][kC32 * kLdY];
   float Z[2][kC32 * kLdZ];
   float R[128 * kLdZ];
   float P[kC32 * kLdP];
   float pw[kC32 + 1];  // g^d
 };
 
-// x = hi + lo: hi is x rounded to tf32's 11 significant bits.
-__device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
-  hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
-  lo = __float_as_uint(x - __uint_as_float(hi));
+// x = hi + lo for a pair: hi is x rounded to tf32's 11 significant bits.
+__device__ __forceinline__ void split_tf32(float2 x, uint32_t& h0, uint32_t& l0, uint32_t& h1, uint32_t& l1) {
+  h0 = (__float_as_uint(x.x) + 0x1000u) & 0xffffe000u;
+  h1 = (__float_as_uint(x.y) + 0x1000u) & 0xffffe000u;
+  const float2 lo = ptx::fma2(make_float2(__uint_as_float(h0), __uint_as_float(h1)), make_float2(-1.f, -1.f), x);
+  l0 = __float_as_uint(lo.x);
+  l1 = __float_as_uint(lo.y);
 }
 __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
   asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -111,9 +118,11 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
 }
 // acc (16 x 16, two n-tiles of 8) += A B over k = k0 .. k1 - 1 (multiples of 8), by one warp:
-// A(m, k) = a[m sam + k sak], B(k, n) = b[k sbk + n sbn] wk(k).
+// A(m, k) = a[m sam + k sak], B(k, n) = b[k sbk + n sbn] wk(k); kA, kB: sak, sbk are 1.  The
+// instruction's k = t and t + 4 are the tile's k = 2t and 2t + 1, on both sides, so that they lie
+// next to each other in a row.
 constexpr int kNt = 2;
-template <typename W>
+template <bool kA, bool kB, typename W>
 __device__ __forceinline__ void warp_mma(float (&acc)[kNt][4], const float* a, int sam, int sak, const float* b, int sbk,
                                          int sbn, int k0, int k1, W wk) {
   const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
@@ -126,13 +135,17 @@ __device__ __forceinline__ void warp_mma(float (&acc)[kNt][4], const float* a, i
     for (int k = kb; k < ke; k += 8) {
       uint32_t ah[4], al[4], bh[kNt][2], bl[kNt][2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) split_tf32(a[(g + 8 * (i & 1)) * sam + (k + t + 4 * (i >> 1)) * sak], ah[i], al[i]);
-#pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float w = wk(k + t + 4 * i);
+        const float* p = a + (g + 8 * i) * sam + (k + 2 * t) * sak;
+        const float2 x = kA ? *reinterpret_cast<const float2*>(p) : make_float2(p[0], p[sak]);
+        split_tf32(x, ah[i], al[i], ah[2 + i], al[2 + i]);
+      }
+      const float w0 = wk(k + 2 * t), w1 = wk(k + 2 * t + 1);
 #pragma unroll
-        for (int j = 0; j < kNt; ++j)
-          split_tf32(w * b[(k + t + 4 * i) * sbk + (8 * j + g) * sbn], bh[j][i], bl[j][i]);
+      for (int j = 0; j < kNt; ++j) {
+        const float* p = b + (k + 2 * t) * sbk + (8 * j + g) * sbn;
+        const float2 x = kB ? *reinterpret_cast<const float2*>(p) : make_float2(p[0], p[sbk]);
+        split_tf32(make_float2(w0 * x.x, w1 * x.y), bh[j][0], bl[j][0], bh[j][1], bl[j][1]);
       }
 #pragma unroll
       for (int j = 0; j < kNt; ++j) mma_tf32(part[j], al, bh[j]);
@@ -188,7 +201,7 @@ __global__ void __launch_bounds__(kF, 1) lin_f32_kernel(const __grid_constant__ 
       const int a4 = a / 4;
       for (int e = tid; e < kC32 * a4; e += kF) {
         const int t = e / a4, c = e % a4 * 4;
-        float* y = sm.Y[s] + t * kLdX + c;
+        float* y = sm.Y[s] + t * kLdY + c;
         float* xx = sm.X[s] + t * kLdX + c;
         if (t < nv) {
           ptx::cp_async16(y, Yg + ((t0 + t) * r.yh + hy) * a + c);
@@ -247,7 +260,7 @@ __global__ void __launch_bounds__(kF, 1) lin_f32_kernel(const __grid_constant__ 
         clear();
         // S, only where some key of the warp's 16 x 16 part counts
         const bool some = wm < nv && wn < nv && (rev ? wn + 8 * kNt > wm : wn <= wm + 15);
-        if (some) warp_mma(acc, X + wm * kLdX, kLdX, 1, Y + wn * kLdX, 1, kLdX, 0, a, NoWeight());
+        if (some) warp_mma<true, true>(acc, X + wm * kLdX, kLdX, 1, Y + wn * kLdY, 1, kLdY, 0, a, NoWeight());
 #pragma unroll
         for (int j = 0; j < kNt; ++j)
 #pragma unroll
@@ -258,7 +271,7 @@ __global__ void __launch_bounds__(kF, 1) lin_f32_kernel(const __grid_constant__ 
           }
         // X R, its rows scaled, then P Z on top
         clear();
-        if (wm < nv && !zero) warp_mma(acc, X + wm * kLdX, kLdX, 1, sm.R + wn, kLdZ, 1, 0, a, NoWeight());
+        if (wm < nv && !zero) warp_mma<true, false>(acc, X + wm * kLdX, kLdX, 1, sm.R + wn, kLdZ, 1, 0, a, NoWeight());
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int row = wm + g + 8 * (e >> 1);
@@ -268,7 +281,8 @@ __global__ void __launch_bounds__(kF, 1) lin_f32_kernel(const __grid_constant__ 
         }
         __syncthreads();  // P complete; R has been read
         if (wm < nv)
-          warp_mma(acc, sm.P + wm * kLdP, kLdP, 1, Z + wn, kLdZ, 1, rev ? wm : 0, rev ? nk : min(nk, wm + 16), NoWeight());
+          warp_mma<true, false>(acc, sm.P + wm * kLdP, kLdP, 1, Z + wn, kLdZ, 1, rev ? wm : 0,
+                                rev ? nk : min(nk, wm + 16), NoWeight());
 #pragma unroll
         for (int j = 0; j < kNt; ++j)
 #pragma unroll
@@ -287,7 +301,8 @@ __global__ void __launch_bounds__(kF, 1) lin_f32_kernel(const __grid_constant__ 
       // R <- g^nv R + Yᵀ (w Z), 16 x 16 parts handed out to the warps
       const float dec = sm.pw[nv];
       const float* pw = sm.pw;
-      auto wz = [&](int t) { return t < nv ? pw[rev ? t + 1 : nv - 1 - t] : 0.f; };
+      // rows of Z past the length are zero: any weight will do there
+      auto wz = [&](int t) { return pw[rev ? t + 1 : max(nv - 1 - t, 0)]; };
       for (int tile = warp; (kStateOnly || !last) && tile < (a + 15) / 16 * (kLinTile / (8 * kNt)); tile += kF / 32) {
         const int m0 = tile / (kLinTile / (8 * kNt)) * 16, n0 = tile % (kLinTile / (8 * kNt)) * 8 * kNt;
         float* R = sm.R + (m0 + g) * kLdZ + n0 + 2 * t4;
@@ -295,8 +310,8 @@ __global__ void __launch_bounds__(kF, 1) lin_f32_kernel(const __grid_constant__ 
         for (int j = 0; j < kNt; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[j][e] = dec * R[8 * (e >> 1) * kLdZ + 8 * j + (e & 1)];
-        if (nk == kC32) warp_mma(acc, Y + m0, 1, kLdX, Z + n0, kLdZ, 1, 0, kC32, wz);
-        else warp_mma(acc, Y + m0, 1, kLdX, Z + n0, kLdZ, 1, 0, nk, wz);
+        if (nk == kC32) warp_mma<false, false>(acc, Y + m0, 1, kLdY, Z + n0, kLdZ, 1, 0, kC32, wz);
+        else warp_mma<false, false>(acc, Y + m0, 1, kLdY, Z + n0, kLdZ, 1, 0, nk, wz);
 #pragma unroll
         for (int j = 0; j < kNt; ++j)
 #pragma unroll
