@@ -1,5 +1,6 @@
-"""Linear attention with per-head decay, as layers: the operators under autograd, and a stack
-of blocks that trains, takes a prompt and generates token by token.
+"""Linear attention with per-head decay, as layers: the operators under autograd (first
+derivatives; a second one raises), and a stack of blocks that trains, takes a prompt and
+generates token by token.
 
 A block holds one norm before it, four projections, the attention, a norm of each head under
 the gate, the projection back, and a norm after it under a learned scale:
@@ -29,6 +30,25 @@ from torch.nn import functional as F
 from . import blocknorm_bwd, blocknorm_fwd, lindecay_bwd, lindecay_decode_step, lindecay_fwd
 
 
+class _FirstOrder(torch.autograd.Function):
+    """A backward's gradients, made part of the graph of what they depend on, where they refuse to
+    be differentiated.  The library's calls return tensors without history: with create_graph they
+    would pass for constants, and a loss over them would lose its gradient without a word."""
+
+    @staticmethod
+    def forward(ctx, name, n, *tensors):  # n gradients, then what they depend on
+        ctx.name = name
+        return tuple(None if t is None else t.clone() for t in tensors[:n])
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError(f"{ctx.name} has no second derivative: its gradients cannot be differentiated")
+
+
+def _first_order(name, grads, *inputs):
+    return _FirstOrder.apply(name, len(grads), *grads, *inputs) if torch.is_grad_enabled() else grads
+
+
 class _Lindecay(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, log_a, lengths, state_in):
@@ -45,8 +65,9 @@ class _Lindecay(torch.autograd.Function):
         dO = torch.zeros_like(v) if dO is None else dO.contiguous()
         dstate_out = None if dstate_out is None else dstate_out.contiguous()
         dstate_in = torch.empty_like(state_in) if ctx.needs_input_grad[5] else None
-        dq, dk, dv = lindecay_bwd(q, k, v, log_a, dO, lengths=lengths, state_in=state_in, dstate_out=dstate_out,
-                                  dstate_in=dstate_in)
+        grads = lindecay_bwd(q, k, v, log_a, dO, lengths=lengths, state_in=state_in, dstate_out=dstate_out,
+                             dstate_in=dstate_in)
+        dq, dk, dv, dstate_in = _first_order("lindecay", (*grads, dstate_in), q, k, v, state_in, dO, dstate_out)
         return dq, dk, dv, None, None, dstate_in
 
 
@@ -70,16 +91,19 @@ class _Blocknorm(torch.autograd.Function):
             return (None,) * 9
         g = blocknorm_bwd(None if dx_new is None else dx_new.contiguous(), y, w_post,
                           None if dh is None else dh.contiguous(), x_new, gate, scale, w_pre, **ctx.args)
-        return g.dy, g.dw_post, g.dx, g.dgate, g.dscale, g.dw_pre, None, None, None
+        g = _first_order("blocknorm", (g.dy, g.dw_post, g.dx, g.dgate, g.dscale, g.dw_pre), dx_new, dh, y, w_post,
+                         x_new, gate, scale, w_pre)
+        return (*g, None, None, None)
 
 
 def lindecay(q, k, v, log_a, lengths=None, state_in=None) -> Tuple[torch.Tensor, torch.Tensor]:
-    """lindecay_fwd under autograd: o and the final states.  log_a and lengths are constants."""
+    """lindecay_fwd under autograd (first derivatives): o and the final states.  log_a and lengths
+    are constants."""
     return _Lindecay.apply(q, k, v, log_a, lengths, state_in)
 
 
 def blocknorm(y=None, w_post=None, x=None, gate=None, scale=None, w_pre=None, group=None, act="silu", eps=1e-6):
-    """blocknorm_fwd under autograd: (x', h)."""
+    """blocknorm_fwd under autograd (first derivatives): (x', h)."""
     x_new, h = _Blocknorm.apply(y, w_post, x, gate, scale, w_pre, group, act, eps)
     return (x if y is None else x_new), h
 
