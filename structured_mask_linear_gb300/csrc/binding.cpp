@@ -88,6 +88,12 @@ at::Tensor new_like(const at::Tensor& x) {
   return x.defined() ? at::Tensor(at::detail::empty_cuda(x.sizes(), x.scalar_type(), x.device(), std::nullopt)) : at::Tensor();
 }
 at::Tensor given_or_like(const at::Tensor& x, const at::Tensor& like) { return x.defined() ? x : new_like(like); }
+// The caller's tensors that a call has written: where autograd keeps one of them for a backward,
+// its raised version says that it is no longer what it was.  (Inference tensors have none.)
+void written(std::initializer_list<at::Tensor> xs) {
+  for (const at::Tensor& x : xs)
+    if (x.defined() && !x.is_inference()) x.unsafeGetTensorImpl()->bump_version();
+}
 
 // Where a call runs: the device and stream, both current while it allocates.  Memory that the
 // caching allocator hands out belongs to the current stream; were it another one than the
@@ -224,6 +230,7 @@ PyObject* py_lindecay_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
                   ptr<float>(s_out), ptr(ws), bytes_of(ws), on.handle);
     Py_END_ALLOW_THREADS
     check_status(r, "lindecay_fwd");
+    written({o_given, s_out});
     return wrap(o);
   });
 }
@@ -249,6 +256,7 @@ PyObject* py_lindecay_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
                   ptr<float>(ds_out), ptr(dq), ptr(dk), ptr(dv), ptr<float>(ds_in), ptr(ws), bytes_of(ws), on.handle);
     Py_END_ALLOW_THREADS
     check_status(r, "lindecay_bwd");
+    written({ds_in});
     return wrap_all({dq, dk, dv});
   });
 }
@@ -268,6 +276,7 @@ PyObject* py_lindecay_decode_step(PyObject*, PyObject* const* a, Py_ssize_t n) {
     r = entry.step(&l.shape, ptr(q), ptr(k), ptr(v), ptr<float>(log_a), ptr(o), ptr<float>(states), on.handle);
     Py_END_ALLOW_THREADS
     check_status(r, "lindecay_decode_step");
+    written({o_given, states});
     return wrap(o);
   });
 }
@@ -326,6 +335,7 @@ PyObject* py_blocknorm_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
                      ptr(h), on.handle);
     Py_END_ALLOW_THREADS
     check_status(r, "blocknorm_fwd");
+    written({xn_given, h_given});
     return wrap_all({y.defined() ? xn : x, h});
   });
 }
