@@ -12,7 +12,9 @@
 //     dn  = dm act(gate),   dw_post = sum dn y r1
 //     un  = dn w_post,      dy = r1 (un - y r1² mean_group(un y))
 // All sums are fp32; values are rounded once, where they are stored.  h is the norm of x'
-// before x' is rounded; the gradients take x' as stored.
+// before x' is rounded; the gradients take x' as stored.  Only normalised values (y r1, x' r2)
+// are multiplied by a further rsqrt: its square or cube alone leaves fp32's range where a row
+// is zeros or tiny (eps = 1e-30: r1 = 1e15) or huge, while the gradient does not.
 //
 // Both directions are bound by memory: each activation is read once and written once.
 // 32768 rows of 4096 in bf16, every part: forward 230 us, 5.85 TB/s, 86 % of the copy rate;
@@ -407,7 +409,7 @@ __global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant_
       for (int i = 0; i < NV; ++i) sg[i] = lanes_sum(sg[i], gl);
     }
     row_sum(s3, tpr, red1);
-    const float r2 = rsqrtf(s3[0] * p.inv_D + p.eps), c2 = -r2 * r2 * r2 * s3[1] * p.inv_D;
+    const float r2 = rsqrtf(s3[0] * p.inv_D + p.eps), c2 = -(r2 * s3[1] * p.inv_D) * r2;
     float se[NV], r1[NV];
     F8 un[NV];
 #pragma unroll
@@ -422,9 +424,9 @@ __global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant_
         const F8 x = c.load(aX), dh = c.load(aH), w = w_pre(c);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float2 d = mul2(dh.v[e], pair(r2));
-          apre[i].v[e] = fma2(d, x.v[e], apre[i].v[e]);
-          dx.v[e] = fma2(d, w.v[e], fma2(x.v[e], pair(c2), dx.v[e]));
+          const float2 xn = mul2(x.v[e], pair(r2));
+          apre[i].v[e] = fma2(dh.v[e], xn, apre[i].v[e]);
+          dx.v[e] = fma2(mul2(dh.v[e], pair(r2)), w.v[e], fma2(xn, pair(c2), dx.v[e]));
         }
       }
       if (has_dx) c.store(static_cast<T*>(p.dx) + here, dx);
@@ -448,7 +450,7 @@ __global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant_
           }
           apost[i].v[e] = fma2(dn, yn, apost[i].v[e]);
           un[i].v[e] = mul2(dn, w.v[e]);
-          s = fma2(un[i].v[e], y.v[e], s);
+          s = fma2(un[i].v[e], yn, s);
         }
         se[i] = s.x + s.y;
         if (kAct != kNoGate) c.store(static_cast<T*>(p.dgate) + here, dg);
@@ -470,10 +472,11 @@ __global__ void __launch_bounds__(kBwdMaxT) bn_bwd_kernel(const __grid_constant_
       for (int i = 0; i < NV; ++i) {
         const C8 c(i, t, tpr, p.D);
         if (!live || !c.any()) continue;
-        const float k = -r1[i] * r1[i] * r1[i] * se[i] * p.inv_group;
+        const float k = -r1[i] * se[i] * p.inv_group;
         const F8 y = c.load(aY);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) un[i].v[e] = fma2(y.v[e], pair(k), mul2(un[i].v[e], pair(r1[i])));
+        for (int e = 0; e < 4; ++e)
+          un[i].v[e] = fma2(mul2(y.v[e], pair(r1[i])), pair(k), mul2(un[i].v[e], pair(r1[i])));
         c.store(static_cast<T*>(p.dy) + here, un[i]);
       }
     }
@@ -636,7 +639,7 @@ __global__ void __launch_bounds__(kAnyT) bn_bwd_any_kernel(const __grid_constant
       }
     a = block_sum(a, red);
     b = block_sum(b, red);
-    const float r2 = rsqrtf(a * p.inv_D + p.eps), c2 = r2 * r2 * b * p.inv_D;
+    const float r2 = rsqrtf(a * p.inv_D + p.eps), c2 = r2 * b * p.inv_D;
     if (Y)
       group_sums(p.D, p.group, s_y, red, [&](int c) {
         const float y = ll_load(Y, base + c);
@@ -644,7 +647,7 @@ __global__ void __launch_bounds__(kAnyT) bn_bwd_any_kernel(const __grid_constant
       });
     auto dx_of = [&](int c) {
       float dx = Dn ? ll_load(Dn, base + c) : 0.f;
-      if (H) dx += r2 * (ll_load(H, base + c) * (p.w_pre ? p.w_pre[c] : 1.f) - ll_load(X, base + c) * c2);
+      if (H) dx += r2 * (ll_load(H, base + c) * (p.w_pre ? p.w_pre[c] : 1.f) - ll_load(X, base + c) * r2 * c2);
       return dx;
     };
     auto un_of = [&](int c) {
@@ -655,7 +658,7 @@ __global__ void __launch_bounds__(kAnyT) bn_bwd_any_kernel(const __grid_constant
     if (Y) group_sums(p.D, p.group, s_e, red, [&](int c) { return un_of(c) * ll_load(Y, base + c); });
     for (int c = threadIdx.x; c < p.D; c += kAnyT) {
       const float dx = dx_of(c);
-      if (H) acc[c] += ll_load(H, base + c) * ll_load(X, base + c) * r2;
+      if (H) acc[c] += ll_load(H, base + c) * (ll_load(X, base + c) * r2);
       float dy = 0.f, dg = 0.f;
       if (Y) {
         const int k = c / p.group;
@@ -667,7 +670,7 @@ __global__ void __launch_bounds__(kAnyT) bn_bwd_any_kernel(const __grid_constant
         acc[2 * p.D + c] += dx * ac.x * n;
         dg = dm * n * ac.y;
         // a group of one: the two terms are equal but for eps, which is all that is left
-        dy = p.group == 1 ? r1 * r1 * r1 * p.eps * un_of(c) : r1 * (un_of(c) - y * r1 * r1 * s_e[k] * p.inv_group);
+        dy = p.group == 1 ? r1 * p.eps * r1 * (r1 * un_of(c)) : r1 * (un_of(c) - yn * (r1 * s_e[k] * p.inv_group));
       }
       if (p.dx) ll_store(static_cast<T*>(p.dx), base + c, dx);
       if (Gt) ll_store(static_cast<T*>(p.dgate), base + c, dg);
