@@ -545,7 +545,8 @@ __global__ void __launch_bounds__(32 * kSlices) bn_reduce_kernel(const __grid_co
 
 // ---------------------------------------------------------------------------------
 // Any D up to kBnMaxD and any group that divides it, for the groups that are neither the row
-// nor whole vectors of a power of two: a CTA per row, values one by one.  The rsqrt of each group stays in shared memory; inputs are read again for each step
+// nor whole vectors of a power of two, and those of one value: a CTA per row, values one by
+// one.  The rsqrt of each group stays in shared memory; inputs are read again for each step
 // (from L1 or L2).
 // ---------------------------------------------------------------------------------
 constexpr int kAnyT = 256;
@@ -647,7 +648,11 @@ __global__ void __launch_bounds__(kAnyT) bn_bwd_any_kernel(const __grid_constant
       });
     auto dx_of = [&](int c) {
       float dx = Dn ? ll_load(Dn, base + c) : 0.f;
-      if (H) dx += r2 * (ll_load(H, base + c) * (p.w_pre ? p.w_pre[c] : 1.f) - ll_load(X, base + c) * r2 * c2);
+      if (H) {
+        const float u = ll_load(H, base + c) * (p.w_pre ? p.w_pre[c] : 1.f);
+        // a single value: the two terms are equal but for eps, which is all that is left
+        dx += p.D == 1 ? r2 * p.eps * r2 * (r2 * u) : r2 * (u - ll_load(X, base + c) * r2 * c2);
+      }
       return dx;
     };
     auto un_of = [&](int c) {
@@ -669,7 +674,6 @@ __global__ void __launch_bounds__(kAnyT) bn_bwd_any_kernel(const __grid_constant
         acc[p.D + c] += dm * ac.x * yn;
         acc[2 * p.D + c] += dx * ac.x * n;
         dg = dm * n * ac.y;
-        // a group of one: the two terms are equal but for eps, which is all that is left
         dy = p.group == 1 ? r1 * p.eps * r1 * (r1 * un_of(c)) : r1 * (un_of(c) - yn * (r1 * s_e[k] * p.inv_group));
       }
       if (p.dx) ll_store(static_cast<T*>(p.dx), base + c, dx);
@@ -690,7 +694,7 @@ int ceil_pow2(int x) {
 // Lanes per group of y's norm when groups lie inside a warp's vectors; 0: the whole row is
 // one group; -1: neither.
 int group_lanes(const BnArgs& p) {
-  if (p.y && p.group == 1) return -1;  // the gradient of one value alone has its own form
+  if (p.D == 1 || (p.y && p.group == 1)) return -1;  // the gradient of one value alone has its own form
   if (!p.y || p.group == p.D) return 0;
   const int n = p.group / 8;
   return p.group % 8 == 0 && n <= 32 && (n & (n - 1)) == 0 ? n : -1;

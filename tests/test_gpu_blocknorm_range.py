@@ -108,3 +108,17 @@ def test_extreme_rows(sml, size, D, group, has, dtype):
     """rsqrt from 1e15 (of an epsilon alone) to 1e-15: its cube is outside of fp32, the gradient is
     not."""
     check(sml, 5, D, group, dtype, has, size)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("size", [1e-15, 1e-3, 1.0])
+def test_norm_of_a_single_value(sml, size, dtype):
+    """x rsqrt(x^2 + eps): what is left of its gradient is eps (x^2 + eps)^(-3/2)."""
+    check(sml, 40, 1, None, dtype, ("w_pre",), size, dx_new=False)
+
+
+def test_norm_of_a_single_value_at_the_usual_epsilon(sml):
+    g = torch.Generator().manual_seed(2)
+    x, dh, w = torch.randn((50, 1), generator=g), torch.randn((50, 1), generator=g), torch.full((1,), 1.25)
+    got = sml.blocknorm_bwd(None, dh=dh.to(DEV), x_new=x.to(DEV), w_pre=w.to(DEV), eps=1e-6)
+    near(got.dx, dh.double() * 1.25 * 1e-6 * (x.double().square() + 1e-6) ** -1.5, "dx")
