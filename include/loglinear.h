@@ -395,7 +395,7 @@ ll_status ssd_fwd(const ll_shape* shape, const void* q, const void* k, const voi
  */
 
 /* Bytes of device workspace lindecay_fwd needs (0: invalid shape; 16: none is used, NULL
- * will do). */
+ * will do), on whichever device, stream or part of its SMs the call is made. */
 size_t lindecay_fwd_workspace_bytes(const ll_shape* shape);
 
 /*
@@ -413,7 +413,7 @@ ll_status lindecay_fwd(const ll_shape* shape, const void* q, const void* k, cons
                        size_t workspace_bytes, void* stream);
 
 /* Bytes of device workspace lindecay_bwd needs (0: invalid shape; 16: none is used, NULL
- * will do). */
+ * will do), on whichever device, stream or part of its SMs the call is made. */
 size_t lindecay_bwd_workspace_bytes(const ll_shape* shape);
 
 /*

@@ -40,9 +40,29 @@ ll_status check_seq_shape(const ll_shape* s) {
 
 struct Plan {
   LinArgs args;
-  size_t off_seg[ll::kLinProbs], off_scratch, off_hand, off_flag, bytes;
-  double est;  // time, in chunks of a wide scan
+  size_t off_seg[ll::kLinProbs], off_scratch, off_hand, off_flag;
+  size_t bytes;  // workspace: for a wrapped plan also enough for the segmented one in its place
+  double est;    // time, in chunks of a wide scan
 };
+// The wrapped sharing of the same units, where it is estimated to be shorter.
+struct Wrap {
+  long long turn, total;  // turn 0: it is not
+  int abreast;
+};
+
+// Work items of a sharing (nwhole, nseg) of all units.
+void share_items(LinArgs& p, int units) {
+  p.items = p.nwhole + (units - p.nwhole) * p.nseg;
+  p.sitems = 0;
+  for (int i = 0; i < p.nprob; ++i) {
+    LinProb& r = p.pr[i];
+    const int w = p.nwhole - r.unit0;
+    r.split0 = w < 0 ? 0 : w > r.nunits ? r.nunits : w;
+    r.nsplit = r.nunits - r.split0;
+    r.sunit0 = p.sitems;
+    p.sitems += r.nsplit * r.nh * (p.nseg - 1);
+  }
+}
 
 // How the units become work items, by estimated time in eighths of what a chunk of a wide
 // scan (a > 64) takes on one SM (2 us in bf16; 8 us in fp32, where launches and starts weigh
@@ -55,8 +75,9 @@ struct Plan {
 //    start per item (kItem) and the prefix over the segments (kSeg each).
 // With many units the first needs no extra pass; with fewer than SMs only the second gives
 // every SM work.
-// Returns the estimate, in such chunks.
-double cut_units(LinArgs& p, bool bf16) {
+// Leaves the segmented sharing in p, and the wrapped one in *wrap if that is the shorter.  Returns
+// the shorter one's estimate, in such chunks.
+double cut_units(LinArgs& p, bool bf16, Wrap* wrap) {
   const double kState = bf16 ? 0.6 : 0.4, kLaunch = bf16 ? 4.0 : 1.0, kItem = bf16 ? 1.0 : 0.5, kSeg = bf16 ? 0.1 : 0.05;
   int units = 0, nh_tail = 1;
   long long line = 0, longest = 0;
@@ -101,34 +122,55 @@ double cut_units(LinArgs& p, bool bf16) {
       if (p.pr[i].unit0 < u + kSms && p.pr[i].unit0 + p.pr[i].nunits > u && p.pr[i].cost > most) most = p.pr[i].cost;
     head += (double)most / 8.0 * p.NC;
   }
+  p.turn = 0;
+  share_items(p, units);
   // the wait for a part's state is bounded by seconds: not for sequences whose parts may take that
   const long long even = (line + kSms - 1) / kSms, turn = even > longest ? even : longest;
-  double est = head + tail;
-  if (bf16 && units > kSms && units % kSms != 0 && p.NC <= (1 << 17) && turn / 8.0 + 1.0 < est && all_sms()) {
-    est = turn / 8.0 + 1.0;
-    p.turn = turn;
-    p.total = line / abreast;
-    p.abreast = abreast;
-    for (int i = 0; i < p.nprob; ++i) p.pr[i].pos0 /= abreast;
-    p.nwhole = units;
-    p.nseg = 1;
-    p.L = p.NC;
+  *wrap = Wrap{};
+  if (bf16 && units > kSms && units % kSms != 0 && p.NC <= (1 << 17) && turn / 8.0 + 1.0 < head + tail) {
+    *wrap = Wrap{turn, line / abreast, abreast};
+    return turn / 8.0 + 1.0;
   }
-  p.items = p.nwhole + (units - p.nwhole) * p.nseg;
-  p.sitems = 0;
+  return head + tail;
+}
+// p, as cut_units left it, shared out by *w.
+void wrap_units(LinArgs& p, const Wrap& w) {
+  int units = 0;
   for (int i = 0; i < p.nprob; ++i) {
-    LinProb& r = p.pr[i];
-    const int w = p.nwhole - r.unit0;
-    r.split0 = w < 0 ? 0 : w > r.nunits ? r.nunits : w;
-    r.nsplit = r.nunits - r.split0;
-    r.sunit0 = p.sitems;
-    p.sitems += r.nsplit * r.nh * (p.nseg - 1);
+    p.pr[i].pos0 /= w.abreast;
+    units += p.pr[i].nunits;
   }
-  return est;
+  p.turn = w.turn;
+  p.total = w.total;
+  p.abreast = w.abreast;
+  p.nwhole = units;
+  p.nseg = 1;
+  p.L = p.NC;
+  share_items(p, units);
 }
 
-// Completes a plan whose scans' head counts, widths and directions are set.
-void finish_plan(const ll_shape* s, Plan* pl) {
+// Places in the workspace; returns its size.
+size_t lay_out(Plan* pl, bool bf16, bool grouped) {
+  const LinArgs& p = pl->args;
+  size_t off = 0;
+  for (int i = 0; i < p.nprob; ++i) {
+    const LinProb& r = p.pr[i];
+    pl->off_seg[i] = off;
+    off += a256((size_t)r.nsplit * r.nh * p.nseg * r.a * ll::kLinTile * 4);
+  }
+  pl->off_scratch = off;
+  if (bf16 && grouped) off += a256((size_t)kSms * (p.sub + p.hpg) * ll::kLinChunk * ll::kLinTile * 4);
+  pl->off_hand = off;
+  if (p.turn > 0) off += a256((size_t)(kSms + 1) * p.hpg * ll::kLinChunk * ll::kLinTile * 4);
+  pl->off_flag = off;
+  if (p.turn > 0) off += a256(kSms * sizeof(unsigned));
+  return off;
+}
+
+// Completes a plan whose scans' head counts, widths and directions are set; may_wrap false: for a
+// stream that has only some of the SMs.  The size of the workspace goes by the shape alone, so
+// that it does for either sharing.
+void finish_plan(const ll_shape* s, Plan* pl, bool may_wrap) {
   // A group's heads take turns of 16 chunks, so that their fp32 sums (16 x 32 KB a CTA, 80
   // MB on 152 SMs) stay in the 126 MB L2.
   constexpr int kSub = 16;
@@ -147,20 +189,15 @@ void finish_plan(const ll_shape* s, Plan* pl) {
     p.pr[i].nh = p.pr[i].oh == p.H ? 1 : p.hpg;
     grouped = grouped || p.pr[i].nh > 1;
   }
-  pl->est = cut_units(p, bf16);
-  size_t off = 0;
-  for (int i = 0; i < p.nprob; ++i) {
-    const LinProb& r = p.pr[i];
-    pl->off_seg[i] = off;
-    off += a256((size_t)r.nsplit * r.nh * p.nseg * r.a * ll::kLinTile * 4);
-  }
-  pl->off_scratch = off;
-  if (bf16 && grouped) off += a256((size_t)kSms * (p.sub + p.hpg) * ll::kLinChunk * ll::kLinTile * 4);
-  pl->off_hand = off;
-  if (p.turn > 0) off += a256((size_t)(kSms + 1) * p.hpg * ll::kLinChunk * ll::kLinTile * 4);
-  pl->off_flag = off;
-  if (p.turn > 0) off += a256(kSms * sizeof(unsigned));
-  pl->bytes = off;
+  Wrap wrap;
+  pl->est = cut_units(p, bf16, &wrap);
+  pl->bytes = lay_out(pl, bf16, grouped);
+  if (wrap.turn == 0) return;
+  Plan w = *pl;
+  wrap_units(w.args, wrap);
+  const size_t need = lay_out(&w, bf16, grouped), both = need > pl->bytes ? need : pl->bytes;
+  if (may_wrap && all_sms()) *pl = w;
+  pl->bytes = both;
 }
 
 LinProb scan(const void* X, int xh, const void* Y, int yh, const void* Z, int zh, void* out, int oh, int a, int b,
@@ -185,7 +222,7 @@ void plan_fwd(const ll_shape* s, const void* q, const void* k, const void* v, vo
   pl->args = LinArgs{};
   pl->args.nprob = 1;
   pl->args.pr[0] = scan(q, G, k, G, v, H, o, H, s->d_k, s->d_v, 0);
-  finish_plan(s, pl);
+  finish_plan(s, pl, true);
 }
 
 // The gradients' three scans.  Where the tensor-core kernels pad d_k and d_v to different
@@ -205,7 +242,7 @@ int plan_bwd(const ll_shape* s, const void* q, const void* k, const void* v, con
   auto plan = [&](Plan& x, std::initializer_list<LinProb> scans) {
     x.args = LinArgs{};
     for (const LinProb& r : scans) x.args.pr[x.args.nprob++] = r;
-    finish_plan(s, &x);
+    finish_plan(s, &x, true);
   };
   plan(pl[0], {pq, pk, pv});
   if (s->dtype != LL_BF16 || (s->d_k > 64) == (s->d_v > 64)) return 1;
@@ -219,19 +256,30 @@ int plan_bwd(const ll_shape* s, const void* q, const void* k, const void* v, con
 }
 size_t bwd_bytes(const Plan* pl, int n) { return n == 2 && pl[1].bytes > pl[0].bytes ? pl[1].bytes : pl[0].bytes; }
 
-ll_status run(const ll_shape* s, Plan* pl, const float* log_a, const int* lengths, void* workspace, void* stream) {
+cudaError_t launch(const ll_shape* s, Plan* pl, const float* log_a, const int* lengths, void* workspace,
+                   cudaStream_t st) {
   LinArgs& p = pl->args;
   p.log_a = log_a;
   p.lengths = lengths;
-  p.status = ll::device_status_word();
-  if (!p.status) return LL_ERR_CUDA;
   char* ws = static_cast<char*>(workspace);
   for (int i = 0; i < p.nprob; ++i) p.pr[i].seg = reinterpret_cast<float*>(ws + pl->off_seg[i]);
   p.scratch = reinterpret_cast<float*>(ws + pl->off_scratch);
   p.hand = reinterpret_cast<float*>(ws + pl->off_hand);
   p.flag = reinterpret_cast<unsigned*>(ws + pl->off_flag);
+  return s->dtype == LL_BF16 ? ll::launch_lin_tc(p, kSms, st) : ll::launch_lin_f32(p, st);
+}
+ll_status run(const ll_shape* s, Plan* pl, const float* log_a, const int* lengths, void* workspace, void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = s->dtype == LL_BF16 ? ll::launch_lin_tc(p, kSms, st) : ll::launch_lin_f32(p, st);
+  pl->args.status = ll::device_status_word();
+  if (!pl->args.status) return LL_ERR_CUDA;
+  cudaError_t e = launch(s, pl, log_a, lengths, workspace, st);
+  if (e == cudaErrorCooperativeLaunchTooLarge) {
+    // the stream or the context has only some of the SMs (a green context, an MPS share): the
+    // segmented sharing, whose CTAs do not wait for one another
+    cudaGetLastError();
+    finish_plan(s, pl, false);
+    e = launch(s, pl, log_a, lengths, workspace, st);
+  }
   return e == cudaSuccess ? LL_OK : LL_ERR_CUDA;
 }
 
