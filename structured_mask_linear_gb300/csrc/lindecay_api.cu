@@ -124,10 +124,12 @@ double cut_units(LinArgs& p, bool bf16, Wrap* wrap) {
   }
   p.turn = 0;
   share_items(p, units);
-  // the wait for a part's state is bounded by seconds: not for sequences whose parts may take that
+  // The wait for a part's state is bounded by 2 s: not for units whose parts may take that (a
+  // chunk of every head that is summed takes up to 2.3 us; 2^17 of them 0.3 s).
+  constexpr long long kLongest = 8LL << 17;
   const long long even = (line + kSms - 1) / kSms, turn = even > longest ? even : longest;
   *wrap = Wrap{};
-  if (bf16 && units > kSms && units % kSms != 0 && p.NC <= (1 << 17) && turn / 8.0 + 1.0 < head + tail) {
+  if (bf16 && units > kSms && units % kSms != 0 && longest <= kLongest && turn / 8.0 + 1.0 < head + tail) {
     *wrap = Wrap{turn, line / abreast, abreast};
     return turn / 8.0 + 1.0;
   }

@@ -124,3 +124,12 @@ def test_binding_refuses_before_cuda(L):
         sml.lindecay_decode_step(z, z, z, torch.zeros(2), z)
     with pytest.raises(ValueError, match="must be on a CUDA device"):
         sml.blocknorm_fwd(z)
+
+
+def test_parts_are_handed_over_only_while_they_are_short(L):
+    """A CTA waits (for 2 s at most) until another one has left a part's state.  The part's time goes
+    by its chunks and by the heads that are summed over them: gradients of 8 heads a group hand
+    states over, which their workspace holds, up to 2^21 tokens, and beyond that no more."""
+    need = [L.lindecay_bwd_workspace_bytes(ctypes.byref(shape(batch=1, heads=128, heads_per_group=8, d_k=8, d_v=8, T=1 << e)))
+            for e in (20, 21, 22, 23)]
+    assert need[0] == need[1] > need[2] == need[3]
