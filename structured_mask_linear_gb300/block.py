@@ -98,7 +98,9 @@ class _Blocknorm(torch.autograd.Function):
 
 def lindecay(q, k, v, log_a, lengths=None, state_in=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """lindecay_fwd under autograd (first derivatives): o and the final states.  log_a and lengths
-    are constants."""
+    are constants: a log_a that asks for a gradient, which there is none of, is refused."""
+    if log_a.requires_grad and torch.is_grad_enabled():
+        raise ValueError("log_a is a constant of lindecay, which has no gradient for it: detach it")
     return _Lindecay.apply(q, k, v, log_a, lengths, state_in)
 
 

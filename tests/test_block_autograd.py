@@ -122,3 +122,15 @@ def test_a_second_derivative_by_one_input_is_refused(case):
     for t in x:
         with pytest.raises(RuntimeError, match="second derivative"):
             torch.autograd.grad(grads[0].sum(), t, allow_unused=True, retain_graph=True)
+
+
+def test_decays_that_ask_for_a_gradient_are_refused():
+    """They would get none.  Without a graph, or detached, they are the constants they are."""
+    x, _, _ = attention()
+    log_a = torch.full((4,), -0.5, dtype=torch.float64, requires_grad=True)
+    with pytest.raises(ValueError, match="log_a"):
+        block.lindecay(*x[:3], log_a)
+    o, _ = block.lindecay(*x[:3], log_a.detach())
+    assert o.requires_grad
+    with torch.no_grad():
+        assert torch.equal(block.lindecay(*x[:3], log_a)[0], o)
