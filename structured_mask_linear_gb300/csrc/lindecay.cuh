@@ -74,10 +74,11 @@ struct LinArgs {
   int nseg, L;
   int nwhole, items, sitems;  // work items of the output and of the state pass
   int sub;              // grouped outputs: chunks that one head runs before the next one does
+  int keep;             // states that wait for their heads' next turn: hpg, 0 where there is but one
   int nprob;
   const float* log_a;   // (H)
   const int* lengths;   // NULL or (B)
-  float* scratch;       // grouped outputs, per CTA: sub * 128 * 64 sums, hpg * 128 * 64 states
+  float* scratch;       // heads in turns, per CTA: sub * 128 * 64 sums, keep * 128 * 64 states
   unsigned* status;
   LinProb pr[kLinProbs];
 };

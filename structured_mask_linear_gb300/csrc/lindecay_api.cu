@@ -152,7 +152,7 @@ void wrap_units(LinArgs& p, const Wrap& w) {
 }
 
 // Places in the workspace; returns its size.
-size_t lay_out(Plan* pl, bool bf16, bool grouped) {
+size_t lay_out(Plan* pl, bool bf16, bool turns) {
   const LinArgs& p = pl->args;
   size_t off = 0;
   for (int i = 0; i < p.nprob; ++i) {
@@ -161,7 +161,8 @@ size_t lay_out(Plan* pl, bool bf16, bool grouped) {
     off += a256((size_t)r.nsplit * r.nh * p.nseg * r.a * ll::kLinTile * 4);
   }
   pl->off_scratch = off;
-  if (bf16 && grouped) off += a256((size_t)kSms * (p.sub + p.hpg) * ll::kLinChunk * ll::kLinTile * 4);
+  const int ctas = p.turn > 0 || p.items > kSms ? kSms : p.items;
+  if (bf16 && turns) off += a256((size_t)ctas * (p.sub + p.keep) * ll::kLinChunk * ll::kLinTile * 4);
   pl->off_hand = off;
   if (p.turn > 0) off += a256((size_t)(kSms + 1) * p.hpg * ll::kLinChunk * ll::kLinTile * 4);
   pl->off_flag = off;
@@ -185,19 +186,20 @@ void finish_plan(const ll_shape* s, Plan* pl, bool may_wrap) {
   p.chunk = bf16 ? ll::kLinChunk : ll::kLinChunk32;
   p.NC = (s->T + p.chunk - 1) / p.chunk;
   p.sub = kSub < p.NC ? kSub : p.NC;
-  bool grouped = false;
+  p.keep = p.NC > p.sub ? p.hpg : 0;
+  bool turns = false;  // a pair of heads runs side by side, more of them or an odd number in turns
   for (int i = 0; i < p.nprob; ++i) {
     p.pr[i].tiles = (p.pr[i].b + ll::kLinTile - 1) / ll::kLinTile;
     p.pr[i].nh = p.pr[i].oh == p.H ? 1 : p.hpg;
-    grouped = grouped || p.pr[i].nh > 1;
+    turns = turns || p.pr[i].nh > 2;
   }
   Wrap wrap;
   pl->est = cut_units(p, bf16, &wrap);
-  pl->bytes = lay_out(pl, bf16, grouped);
+  pl->bytes = lay_out(pl, bf16, turns);
   if (wrap.turn == 0) return;
   Plan w = *pl;
   wrap_units(w.args, wrap);
-  const size_t need = lay_out(&w, bf16, grouped), both = need > pl->bytes ? need : pl->bytes;
+  const size_t need = lay_out(&w, bf16, turns), both = need > pl->bytes ? need : pl->bytes;
   if (may_wrap && all_sms()) *pl = w;
   pl->bytes = both;
 }

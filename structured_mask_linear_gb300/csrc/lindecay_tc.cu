@@ -628,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
       // states of heads that wait for their turn, and of units that another CTA goes on with:
       // 16 float4s a row, consecutive rows side by side
       float4* keep = reinterpret_cast<float4*>(p.scratch) +
-                     ((size_t)blockIdx.x * (p.sub + p.hpg) + p.sub + w.hi) * (kC * kLinTile / 4) + row;
+                     ((size_t)blockIdx.x * (p.sub + p.keep) + p.sub + w.hi) * (kC * kLinTile / 4) + row;
       float4* hand = reinterpret_cast<float4*>(p.hand) + ((size_t)w.x.slot * p.hpg + w.hi) * (kC * kLinTile / 4) + row;
       holds = row < 64 * lin_blocks<KA>(r);
       if (!kStateOnly && w.first_block() && w.first_head() && w.x.from == kLinHand)
@@ -712,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
       const int rot = row & 7;
       uint8_t* stage = smem + S::kOut;
       float4* scr = reinterpret_cast<float4*>(p.scratch) +
-                    (size_t)blockIdx.x * (p.sub + p.hpg) * (kC * kLinTile / 4) + row;
+                    (size_t)blockIdx.x * (p.sub + p.keep) * (kC * kLinTile / 4) + row;
       uint32_t turn = 0;
       bool ok = true;
       for (Walk w(p, false); w.live(); w.next_run()) {

@@ -133,3 +133,17 @@ def test_parts_are_handed_over_only_while_they_are_short(L):
     need = [L.lindecay_bwd_workspace_bytes(ctypes.byref(shape(batch=1, heads=128, heads_per_group=8, d_k=8, d_v=8, T=1 << e)))
             for e in (20, 21, 22, 23)]
     assert need[0] == need[1] > need[2] == need[3]
+
+
+def test_workspace_of_summed_heads(L):
+    """Two heads a group run side by side and need no place for their sums; more take turns: 32 KB a
+    chunk of 128 tokens for each of the CTAs, at most 16 chunks, and 32 KB a head for the states
+    that wait where 16 chunks are not all."""
+    need = lambda **kw: L.lindecay_bwd_workspace_bytes(ctypes.byref(shape(d_k=64, d_v=64, **kw)))  # noqa: E731
+    tile = 128 * 64 * 4
+    assert need(batch=1, heads=4, heads_per_group=2, T=3) == 16
+    # items: dq and dk per group, dv per head
+    assert need(batch=1, heads=4, heads_per_group=4, T=3) == (1 + 1 + 4) * 1 * tile
+    assert need(batch=1, heads=6, heads_per_group=3, T=200) == (2 + 2 + 6) * 2 * tile
+    assert need(batch=152, heads=3, heads_per_group=3, T=2048) == 152 * 16 * tile
+    assert need(batch=152, heads=3, heads_per_group=3, T=2049) == 152 * (16 + 3) * tile
