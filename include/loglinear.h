@@ -404,7 +404,7 @@ size_t lindecay_fwd_workspace_bytes(const ll_shape* shape);
  *   log_a     (H) fp32
  *   lengths   NULL or (B) int32
  *   state_in  NULL or (B, H, d_k, d_v) fp32, the state before the first token
- *   o         (B, T, H, d_v) dtype, written
+ *   o         (B, T, H, d_v) dtype, written; may be v, overlaps neither q nor k
  *   state_out NULL or (B, H, d_k, d_v) fp32, written; may be state_in
  *   workspace >= lindecay_fwd_workspace_bytes(shape) bytes; contents do not matter
  */
@@ -424,6 +424,7 @@ size_t lindecay_bwd_workspace_bytes(const ll_shape* shape);
  *   dq, dk     (B, T, G, d_k) dtype, dv (B, T, H, d_v) dtype, written; the heads of a group
  *              add up in fp32, in order (the result does not vary between calls)
  *   dstate_in  NULL or (B, H, d_k, d_v) fp32, written; neither state_in nor dstate_out
+ * No output may overlap an input or another output.
  */
 ll_status lindecay_bwd(const ll_shape* shape, const void* q, const void* k, const void* v, const float* log_a,
                        const int* lengths, const float* state_in, const void* dO, const float* dstate_out, void* dq,

@@ -509,7 +509,7 @@ def lindecay_fwd(q, k, v, log_a, lengths=None, state_in=None, state_out=None, o=
     """o of S_t = exp(log_a[h]) S_{t-1} + k_t v_tᵀ, o_t = S_tᵀ q_t.  q, k: (B, T, G, d_k);
     v: (B, T, H, d_v), bf16 or fp32; log_a: (H,) fp32.  lengths: (B,) int32 tokens per row;
     state_in, state_out: (B, H, d_k, d_v) fp32 states before the first and after the last
-    token (state_out is written; it may be state_in)."""
+    token (state_out is written; it may be state_in).  o may be given, v itself among others."""
     return (_native_module or _native()).lindecay_fwd(q, k, v, log_a, lengths, state_in, state_out, o, workspace,
                                                       None if stream is None else _stream_ptr(stream))
 

@@ -42,6 +42,7 @@ ll_status blocknorm_fwd(const blocknorm_shape* s, const void* x, const void* y, 
   if (!x && !y) return LL_ERR_NULL;
   if (y ? !x_new : (!h || x_new || gate || w_post || scale)) return LL_ERR_NULL;
   if (!h && w_pre) return LL_ERR_NULL;
+  if (h && h == x_new) return LL_ERR_SHAPE;
   for (const void* q : {x, y, gate, (const void*)w_post, (const void*)scale, (const void*)w_pre, (const void*)x_new,
                         (const void*)h})
     if (!aligned16(q)) return LL_ERR_ALIGN;

@@ -310,6 +310,8 @@ ll_status lindecay_fwd(const ll_shape* s, const void* q, const void* k, const vo
   plan_fwd(s, q, k, v, o, &pl);
   if (pl.bytes > 0 && (!workspace || workspace_bytes < pl.bytes)) return LL_ERR_WORKSPACE;
   if (!aligned16(workspace)) return LL_ERR_ALIGN;
+  // other heads and columns still read q and k when an output is written
+  if (o == q || o == k) return LL_ERR_SHAPE;
   LinProb& r = pl.args.pr[0];
   r.init = state_in;
   r.init_rs = s->d_v;
@@ -334,12 +336,15 @@ ll_status lindecay_bwd(const ll_shape* s, const void* q, const void* k, const vo
   for (const void* x : {q, k, v, dO, (const void*)dq, (const void*)dk, (const void*)dv, (const void*)state_in,
                         (const void*)dstate_out, (const void*)dstate_in})
     if (!aligned16(x)) return LL_ERR_ALIGN;
-  // the scans run side by side: one may still read the states that another's end writes
+  // the scans run side by side: one may still read what another writes
   if (dstate_in && (dstate_in == state_in || dstate_in == dstate_out)) return LL_ERR_SHAPE;
   Plan pl[2];
   const int n = plan_bwd(s, q, k, v, dO, dq, dk, dv, pl);
   if (bwd_bytes(pl, n) > 0 && (!workspace || workspace_bytes < bwd_bytes(pl, n))) return LL_ERR_WORKSPACE;
   if (!aligned16(workspace)) return LL_ERR_ALIGN;
+  for (const void* g : {dq, dk, dv})
+    if (g == q || g == k || g == v || g == dO) return LL_ERR_SHAPE;
+  if (dq == dk || dq == dv || dk == dv) return LL_ERR_SHAPE;
   LinProb &pq = pl[0].args.pr[0], &pk = pl[0].args.pr[1], &pv = n == 2 ? pl[1].args.pr[0] : pl[0].args.pr[2];
   pq.init = state_in;
   pk.init = pv.init = dstate_out;

@@ -147,3 +147,17 @@ def test_workspace_of_summed_heads(L):
     assert need(batch=1, heads=6, heads_per_group=3, T=200) == (2 + 2 + 6) * 2 * tile
     assert need(batch=152, heads=3, heads_per_group=3, T=2048) == 152 * 16 * tile
     assert need(batch=152, heads=3, heads_per_group=3, T=2049) == 152 * (16 + 3) * tile
+
+
+def test_outputs_in_the_place_of_what_is_still_read(L):
+    """Refused, where a call would give wrong results without a word."""
+    s = ctypes.byref(shape(T=1, heads=2, heads_per_group=1, d_k=64, d_v=64))
+    at = [FAKE * (i + 1) for i in range(16)]
+    fwd = lambda o: L.lindecay_fwd(s, *at[:4], None, None, o, None, at[8], 0, None)  # noqa: E731
+    assert fwd(at[0]) == 2 and fwd(at[1]) == 2
+    bwd = lambda dq, dk, dv: L.lindecay_bwd(s, *at[:4], None, None, at[4], None, dq, dk, dv, None, at[8], 0, None)  # noqa: E731
+    places = at[5:8]
+    for i in range(3):
+        for taken in (*at[:3], at[4], places[(i + 1) % 3]):
+            assert bwd(*places[:i], taken, *places[i + 1:]) == 2
+    assert L.blocknorm_fwd(bn(), None, at[0], None, None, None, None, at[1], at[1], None) == 2
