@@ -11,12 +11,14 @@ the gate, the projection back, and a norm after it under a learned scale:
     x'         = x + scale * norm(u W_o) * w_post      blocknorm: both of these
     h'         = norm(x') * w_pre'                     in one pass, w_pre' of the next block
 
-q starts smaller by sqrt(d_k), so that a product q k v starts at a mean square of 1, and that is
-the head norm's epsilon.  A sequence's first outputs are (q_0 k_0) v_0
-alone, and where q_0 k_0 happens to be near zero a norm with a small epsilon would make one
-token's gradient the whole sum, and a rounding of q or k a large share of it (7 % of a weight's
-gradient in bf16, against 1 %).  Only the projections are library products; the rest is three kernels per block going forward and
-three calls going back.  Decays are constants of the model, as log_a.
+The norms' epsilons are arguments, to be those that a model was trained with.  For training from
+the start q begins smaller by sqrt(d_k), so that a product q k v begins at a mean square of 1,
+and that is the head norm's epsilon unless another is given.  A sequence's first outputs are
+(q_0 k_0) v_0 alone, and where q_0 k_0 happens to be near zero a norm with a small epsilon would
+make one token's gradient the whole sum, and a rounding of q or k a large share of it (7 % of a
+weight's gradient in bf16, against 1 %).  Only the projections are library products; the rest is
+three kernels per block going forward and three calls going back.  Decays are constants of the
+model, as log_a.
 """
 from __future__ import annotations
 
@@ -119,11 +121,12 @@ def head_decays(heads: int, shortest: float = 8.0, longest: float = 2048.0) -> t
 class DecayBlock(nn.Module):
     """One block's weights, and what it does between its two norms."""
 
-    def __init__(self, width: int, heads: int, groups: int, d_k: int, d_v: int, dtype=torch.bfloat16, device="cuda"):
+    def __init__(self, width: int, heads: int, groups: int, d_k: int, d_v: int, dtype=torch.bfloat16, device="cuda",
+                 head_eps: float = 1.0):
         super().__init__()
         if heads <= 0 or groups <= 0 or heads % groups:
             raise ValueError(f"heads ({heads}) must be a multiple of groups ({groups})")
-        self.heads, self.groups, self.d_k, self.d_v = heads, groups, d_k, d_v
+        self.heads, self.groups, self.d_k, self.d_v, self.head_eps = heads, groups, d_k, d_v, head_eps
 
         def product(n_out, n_in, shrink=1):
             w = torch.empty((n_out, n_in), dtype=dtype, device=device)
@@ -148,17 +151,20 @@ class DecayBlock(nn.Module):
 
     def back(self, o, g):
         """From the heads' outputs to the block's, ahead of the norm after it."""
-        u, _ = blocknorm(o.reshape(g.shape), self.w_head, gate=g, group=self.d_v, eps=1.0)
+        u, _ = blocknorm(o.reshape(g.shape), self.w_head, gate=g, group=self.d_v, eps=self.head_eps)
         return F.linear(u, self.w_o)
 
 
 class DecayStack(nn.Module):
-    """Blocks on a residual stream.  forward() for training and prompts, step() for a token."""
+    """Blocks on a residual stream.  forward() for training and prompts, step() for a token.  eps: of
+    the norms over the stream and over a block's output; head_eps: of the norm of each head."""
 
     def __init__(self, layers: int, width: int, heads: int, groups: int, d_k: int, d_v: int, dtype=torch.bfloat16,
-                 device="cuda"):
+                 device="cuda", eps: float = 1e-6, head_eps: float = 1.0):
         super().__init__()
-        self.blocks = nn.ModuleList(DecayBlock(width, heads, groups, d_k, d_v, dtype, device) for _ in range(layers))
+        self.eps = eps
+        self.blocks = nn.ModuleList(DecayBlock(width, heads, groups, d_k, d_v, dtype, device, head_eps)
+                                    for _ in range(layers))
         self.w_last = nn.Parameter(torch.ones(width, dtype=torch.float32, device=device))
 
     def _after(self, i):
@@ -167,21 +173,21 @@ class DecayStack(nn.Module):
     def forward(self, x, lengths: Optional[torch.Tensor] = None, states: Optional[List[torch.Tensor]] = None):
         """x (B, T, width), lengths (B,) int32 and the blocks' states before it (none: zero).
         Returns the stream under its last norm and the states after each row's length."""
-        _, h = blocknorm(x=x, w_pre=self.blocks[0].w_pre if len(self.blocks) else self.w_last)
+        _, h = blocknorm(x=x, w_pre=self.blocks[0].w_pre if len(self.blocks) else self.w_last, eps=self.eps)
         after = []
         for i, b in enumerate(self.blocks):
             q, k, v, g = b.project(h)
             o, s = lindecay(q, k, v, b.log_a, lengths, None if states is None else states[i])
             after.append(s)
-            x, h = blocknorm(b.back(o, g), b.w_post, x, scale=b.scale, w_pre=self._after(i))
+            x, h = blocknorm(b.back(o, g), b.w_post, x, scale=b.scale, w_pre=self._after(i), eps=self.eps)
         return h, after
 
     @torch.no_grad()
     def step(self, x_t, states: List[torch.Tensor]):
         """One token of every row: x_t (B, width); the states move on in place."""
-        _, h = blocknorm_fwd(x=x_t, w_pre=self.blocks[0].w_pre if len(self.blocks) else self.w_last)
+        _, h = blocknorm_fwd(x=x_t, w_pre=self.blocks[0].w_pre if len(self.blocks) else self.w_last, eps=self.eps)
         for i, b in enumerate(self.blocks):
             q, k, v, g = b.project(h)
             y = b.back(lindecay_decode_step(q, k, v, b.log_a, states[i]), g)
-            x_t, h = blocknorm_fwd(y, b.w_post, x_t, scale=b.scale, w_pre=self._after(i))
+            x_t, h = blocknorm_fwd(y, b.w_post, x_t, scale=b.scale, w_pre=self._after(i), eps=self.eps)
         return h
