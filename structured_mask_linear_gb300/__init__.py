@@ -34,6 +34,7 @@ import torch
 
 from ._build import LIB as _LIB_PATH
 from ._build import NATIVE as _NATIVE_PATH
+from ._build import native_missing as _native_missing
 
 LL_OK = 0
 STATUS_NAMES = {0: "LL_OK", 1: "LL_ERR_NULL", 2: "LL_ERR_SHAPE", 3: "LL_ERR_DTYPE",
@@ -485,8 +486,10 @@ def _native():
     with _lock:
         if _native_module is None:
             if not os.path.exists(_NATIVE_PATH):
+                need = _native_missing()
                 raise RuntimeError(f"{_NATIVE_PATH} is missing: run __graft_entry__.build() "
-                                   "(or python -m structured_mask_linear_gb300._build)")
+                                   "(or python -m structured_mask_linear_gb300._build)" +
+                                   (f", which needs {need}" if need else ""))
             spec = importlib.util.spec_from_file_location("_native", _NATIVE_PATH)
             module = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(module)

@@ -4,7 +4,7 @@ CPython module _native.so (csrc/binding.cpp) against the installed torch with g+
 Each translation unit compiles in parallel to an object file under _build/, then one
 nvcc link makes _build/libloglinear.so (CUDA runtime linked statically).  Rebuilds
 only when a source or header is newer than the library, the module also when torch has
-changed.
+changed.  Without the interpreter's headers the module is left out, with a warning.
 """
 from __future__ import annotations
 
@@ -13,6 +13,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -78,9 +79,17 @@ def _native_command(out: str):
              "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python"])
 
 
+def native_missing() -> str:
+    """What the CPython module cannot be built without and is not there; empty if nothing is."""
+    header = os.path.join(sysconfig.get_paths()["include"], "Python.h")
+    return "" if os.path.exists(header) else f"{header} (the interpreter's headers)"
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    native = None
-    if force or not native_up_to_date():
+    native, missing = None, native_missing()
+    if missing:  # the library does not need the module; the calls that do raise
+        warnings.warn(f"_native.so is not built: {missing} is missing", RuntimeWarning, stacklevel=2)
+    elif force or not native_up_to_date():
         os.makedirs(OUT_DIR, exist_ok=True)
         tmp = NATIVE + f".tmp{os.getpid()}"
         cmd = _native_command(tmp)
