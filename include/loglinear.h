@@ -381,8 +381,13 @@ ll_status ssd_fwd(const ll_shape* shape, const void* q, const void* k, const voi
  *
  * Shapes: ll_shape with any T >= 1 (2^30 at most); d_k and d_v multiples of 8 from 8 to 128;
  * batch * heads <= 2^20; chunk and levels are ignored.  q, k, v, o and their gradients have
- * shape->dtype; states (B, H, d_k, d_v), log_a (H) and their gradients are fp32.  bf16 runs
- * on tcgen05, fp32 in three tf32 products each (errors below 1e-6).
+ * shape->dtype; states (B, H, d_k, d_v), log_a (H) and their gradients are fp32.
+ *
+ * Precision, as errors relative in the 2-norm: fp32 calls (three tf32 products each) below
+ * 2^-19, 3 to 5e-7 as a rule.  bf16 calls (on tcgen05): outputs and gradients 2.1e-3 of which
+ * 1.7e-3 is their own rounding; final states and dstate_in, though fp32, below 2^-16, 4e-6 as
+ * a rule, since each token's decayed v enters its product as two bf16 parts (16 bits).  A
+ * decode step adds to the states in fp32.
  *
  * log_a is a constant of the model (no gradient is returned for it).  Values above 0 count
  * as 0 (no decay), values below -1000 as -1000 (gamma is 0 in fp32).

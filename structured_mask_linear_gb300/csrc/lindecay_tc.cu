@@ -14,23 +14,25 @@
 //     Oa = P Z                     128 x 64 x 128   (P = S g^|i-j|, masked, rounded to bf16)
 // and out_i = Oa_i + g^(i'+sh) Ob_i, R <- g^nv R + D.  Where an output sums over a group with
 // an even number of heads, a CTA takes two heads side by side: their items alternate, Oa
-// adds up over both, each has its own Ob and R (560 -> 424 us for the gradients of
-// 2 x 8192 tokens, 48 heads of 128 and 64 in pairs, against one head after the other with
-// fp32 sums in global memory; larger and odd groups still take their turns that way).
+// adds up over both, each has its own Ob and R (for the gradients of 2 x 8192 tokens, 48
+// heads of 128 and 64 in pairs, 408 us today, it took 560 -> 424 against one head after the
+// other with fp32 sums in global memory; larger and odd groups still take their turns that way).
 //
 // Roundings: X, Y, Z enter exactly.  P enters as bf16: an output averages over its terms, or
 // is one of them and then no less exact than its own rounding.  R enters Ob as two parts:
 // one alone put the largest errors, where a row is mostly its state_in, at 0.053 RMS of the
 // output, outside the package's bar of 0.05 (it costs 8 % at 4 x 8192 x 48 heads).  w_j Z_j
 // takes two parts because the states are fp32 outputs, and an error made in one chunk stays in
-// them: what is left of a term is below 2^-15 of it, 4e-6 in the mean square.  R itself is
-// carried in fp32.
+// them: what is left of a term is below 2^-15 of it, 4e-6 in the mean square.  (Splitting in
+// fp32 arithmetic leaves 2.4e-6 and takes 3 % longer; a third part 1.3e-7, and 7 to 14 % longer
+// with a <= 64, 30 % with 128, where its place in shared memory makes more turns of it.)  R
+// itself is carried in fp32.
 //
 // Bound: memory, where every SM holds a head's whole sequence (152 heads of 64 and 64, 8192
 // tokens: 105 us, 89 % of the copy rate; of 128 and 64: 151 us, 93 %); elsewhere the way of a
 // chunk through the roles, of which two are under way at a time: 2.1 to 2.3 us a chunk of a =
 // 128, with the tensor cores active for 37 % of it and shared memory's banks for 30 (4 x 8192
-// tokens, 48 heads in pairs: 188 us, 64 % of the copy rate).  Ob's and D's two parts lie side
+// tokens, 48 heads in pairs: 187 us, 65 % of the copy rate).  Ob's and D's two parts lie side
 // by side in one product of 128 columns where tensor memory has the room: each then reads its
 // left operand once.
 //
@@ -42,7 +44,7 @@
 //               the registers: 15 % slower)
 //   warps 12-15 w Z: the high and low parts, through two slots
 //   warp 16     TMA loads, two or three chunks ahead
-//   warp 17     the MMAs of S, one chunk ahead of
+//   warp 17     the MMAs of S, a chunk ahead of warp 18
 //   warp 18     the MMAs of D, Ob and Oa
 // The launch gives 96 registers a thread; the groups pass on what they do not need.
 //
@@ -808,7 +810,8 @@ __global__ void __launch_bounds__(kThreads, 1) lin_tc_kernel(const __grid_consta
     }
   } else if (group == 3) {
     ptx::regs_dec<kGrouped ? 64 : 80>();
-    // ---- w Z: four threads a token, 16 columns each, 32 tokens at a time --------------------
+    // ---- w Z: 32 tokens at a time, four threads a token and 16 columns each (in the narrow
+    // kernel, whose slots have room, 64 tokens, two threads and 32 columns) -------------------
     constexpr int kTh = kC / S::kTok, kV = 8 / kTh;  // threads a token, 16-byte pieces of each
     const int part = (row & (kTh - 1)) * kV;
     uint32_t it = 0;
