@@ -59,6 +59,8 @@ struct Place {
     }
   }
   __device__ __forceinline__ bool any() const { return at[0] >= 0; }
+  // whether pair n turns.  kVec: a lane's pairs all do or none does.
+  static __device__ __forceinline__ bool turns(int unit, int n, int rot) { return 8 * unit + (kVec ? 0 : 2 * n) < rot; }
   // where value e sits, -1 (kVec: with any() alone) for none
   __device__ __forceinline__ int of(int e) const {
     if constexpr (!kVec) return at[e];
@@ -224,6 +226,7 @@ struct Lane {
   const HrArgs& p;
   const Shared& sh;
   int slot, unit, hpw;  // a step's heads of a row; a lane's of them, and its place in the head
+  bool turns[kVec ? 1 : 4];  // which of its pairs do
   Place<kVec, kHalf> at;
   unsigned long long freq[4];
   long long row;
@@ -232,7 +235,26 @@ struct Lane {
 
   __device__ __forceinline__ Lane(const HrArgs& p, const Shared& s)
       : p(p), sh(s), slot(((threadIdx.x & 31) >> p.tph_log) & ((32 >> p.tph_log >> p.rpw_log) - 1)),
-        unit(threadIdx.x & ((1 << p.tph_log) - 1)), hpw(32 >> p.tph_log >> p.rpw_log), at(unit, p.d, p.rot) {}
+        unit(threadIdx.x & ((1 << p.tph_log) - 1)), hpw(32 >> p.tph_log >> p.rpw_log), at(unit, p.d, p.rot) {
+#pragma unroll
+    for (int n = 0; n < (kVec ? 1 : 4); ++n) turns[n] = Place<kVec, kHalf>::turns(unit, n, p.rot);
+  }
+  // The pairs that turn by t.  The others stay: a product with the sine of 0 would hand a value that is not
+  // finite on to its partner.
+  __device__ __forceinline__ void turn(Eight& v, const Turn& t) const {
+    if constexpr (kVec) {
+      if (turns[0]) turned(v, t);
+    } else {
+      const Eight was = v;
+      turned(v, t);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        if (turns[n]) continue;
+        (n % 2 ? v.p[n / 2].y : v.p[n / 2].x) = n % 2 ? was.p[n / 2].y : was.p[n / 2].x;
+        (n % 2 ? v.p[n / 2 + 2].y : v.p[n / 2 + 2].x) = n % 2 ? was.p[n / 2 + 2].y : was.p[n / 2 + 2].x;
+      }
+    }
+  }
   // Fills the shared part, for all.
   __device__ __forceinline__ void prepare(Shared& s) {
     for (int j = threadIdx.x; j < p.rot / 2; j += blockDim.x) s.freq[j] = turns_of(p.inv_freq[j]);
@@ -345,7 +367,7 @@ __global__ void __launch_bounds__(kHrWarps * 32, kHrFwdCtas) hr_fwd_kernel(HrArg
         const Eight w = l.weights(in_k);
 #pragma unroll
         for (int n = 0; n < 4; ++n) v.p[n] = mul2(v.p[n], mul2(w.p[n], both(r)));
-        if (kUsual || p.rot) turned(v, t);
+        if (kUsual || p.rot) l.turn(v, t);
         if (has) Held<T, kVec, kHalf>::store((in_k ? ko : qo) + (i0 + i) * step, l.at, v);
       }
     };
@@ -414,7 +436,7 @@ __global__ void __launch_bounds__(kHrWarps * 32, kHrBwdCtas) hr_bwd_kernel(HrArg
             v = x[i].get();
             u = y[i].get();
           }
-          if (kUsual || p.rot) turned(u, t);
+          if (kUsual || p.rot) l.turn(u, t);
           Eight g;
 #pragma unroll
           for (int n = 0; n < 4; ++n) g.p[n] = mul2(u.p[n], w.p[n]);

@@ -1,0 +1,43 @@
+"""GPU tests of the head norms with rotation on values that are not finite: they stay where they are,
+as far as the formula goes."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+LOST = [float("nan"), float("inf"), float("-inf")]
+
+
+@pytest.fixture(scope="module")
+def sml():
+    import structured_mask_linear_gb300 as m
+
+    m.lib()
+    return m
+
+
+def alike(a, b):
+    return (a == b) | (a.isnan() & b.isnan())
+
+
+# (72, 24): 9 lanes' worth in 16; (33, 6), (10, 2), (7, 2): value by value, an odd one left over
+DIMS = [(64, 16), (72, 24), (128, 64), (33, 6), (10, 2), (7, 2), (8, 0)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("layout", ["half", "inter"])
+@pytest.mark.parametrize("d,rot", DIMS)
+def test_past_the_rotated_part_a_value_is_its_own(sml, d, rot, layout, dtype):
+    """Without a norm what is not rotated goes out as it came, and its gradient too."""
+    g = torch.Generator().manual_seed(d)
+    q, dq = (torch.randn((3, 2, d), generator=g).to(dtype).to(DEV) for _ in range(2))
+    kw = dict(inv_freq=sml.rope_frequencies(rot) if rot else None, layout=layout, norm="none",
+              positions=torch.tensor([5, 0, 1 << 20], dtype=torch.int32, device=DEV) if rot else None)
+    base = sml.headrope_fwd(q, **kw)[0], sml.headrope_bwd(dq, q, **kw).dq
+    for n in range(rot, d):
+        x, dy = q.clone(), dq.clone()
+        x[1, 0, n] = dy[1, 0, n] = LOST[n % 3]
+        y, dx = sml.headrope_fwd(x, **kw)[0], sml.headrope_bwd(dy, q, **kw).dq
+        for got, was, want in ((y, base[0], x[1, 0, n]), (dx, base[1], dy[1, 0, n])):
+            same = alike(got, was)
+            assert alike(got[1, 0, n], want) and int((~same).sum()) == 1 and not same[1, 0, n], n
