@@ -440,8 +440,8 @@ __global__ void __launch_bounds__(kHrWarps * 32, kHrBwdCtas) hr_bwd_kernel(HrArg
           Eight g;
 #pragma unroll
           for (int n = 0; n < 4; ++n) g.p[n] = mul2(u.p[n], w.p[n]);
-          float r = 1.f, k = 0.f;
-          if (kUsual || p.norm != HR_NONE) {
+          float r = 1.f;
+          if (kUsual || p.norm != HR_NONE) {  // without a norm x has no part in dx, not even as 0 times an infinity
             float2 ss = mul2(v.p[0], v.p[0]), gx = mul2(g.p[0], v.p[0]);
 #pragma unroll
             for (int n = 1; n < 4; ++n) {
@@ -451,13 +451,12 @@ __global__ void __launch_bounds__(kHrWarps * 32, kHrBwdCtas) hr_bwd_kernel(HrArg
             float sums[2] = {sum_of(ss), sum_of(gx)};
             head_sums(sums, p.tph_log);
             r = inverse_norm(sums[0], p);
-            k = -(r * (r * (sums[1] * mean)));
+            const float k = -(r * (r * (sums[1] * mean)));
+#pragma unroll
+            for (int n = 0; n < 4; ++n) g.p[n] = mul2(fma2(v.p[n], both(k), g.p[n]), both(r));
           }
 #pragma unroll
-          for (int n = 0; n < 4; ++n) {
-            dw[side].p[n] = fma2(mul2(u.p[n], both(scale * r)), v.p[n], dw[side].p[n]);
-            g.p[n] = mul2(fma2(v.p[n], both(k), g.p[n]), both(r));
-          }
+          for (int n = 0; n < 4; ++n) dw[side].p[n] = fma2(mul2(u.p[n], both(scale * r)), v.p[n], dw[side].p[n]);
           if (has) Held<T, kVec, kHalf>::store(o0 + (i0 + i) * step, l.at, g);
         }
       }

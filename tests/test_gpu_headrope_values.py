@@ -41,3 +41,23 @@ def test_past_the_rotated_part_a_value_is_its_own(sml, d, rot, layout, dtype):
         for got, was, want in ((y, base[0], x[1, 0, n]), (dx, base[1], dy[1, 0, n])):
             same = alike(got, was)
             assert alike(got[1, 0, n], want) and int((~same).sum()) == 1 and not same[1, 0, n], n
+
+
+@pytest.mark.parametrize("d,rot", [(64, 16), (64, 0), (33, 6), (128, 128)])
+@pytest.mark.parametrize("weights", [False, True])
+def test_without_a_norm_x_has_no_part_in_its_gradient(sml, d, rot, weights):
+    """dx = R^-1 dy w: an infinity in x reaches the weight's gradient alone."""
+    g = torch.Generator().manual_seed(d)
+    q, dq = (torch.randn((3, 2, d), generator=g).to(DEV) for _ in range(2))
+    kw = dict(w_q=torch.rand(d, generator=g).to(DEV) if weights else None, norm="none",
+              inv_freq=sml.rope_frequencies(rot) if rot else None,
+              positions=torch.tensor([5, 0, 1 << 20], dtype=torch.int32, device=DEV) if rot else None)
+    base = sml.headrope_bwd(dq, q, **kw)
+    x = q.clone()
+    x[1, 0, d // 2], x[2, 1, 0], x[0, 0, d - 1] = LOST[0], LOST[1], LOST[2]
+    got = sml.headrope_bwd(dq, x, **kw)
+    assert torch.equal(got.dq, base.dq)
+    if weights:
+        keep = torch.ones(d, dtype=torch.bool)
+        keep[[0, d // 2, d - 1]] = False
+        assert torch.equal(got.dw_q[keep.to(DEV)], base.dw_q[keep.to(DEV)]) and not torch.isfinite(got.dw_q[~keep.to(DEV)]).any()
