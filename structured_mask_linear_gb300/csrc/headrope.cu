@@ -181,6 +181,16 @@ __device__ __forceinline__ void turned(Eight& v, const Turn& t) {
     v.p[n + 2] = fma2(a, t.s[n], mul2(b, t.c[n]));
   }
 }
+// The same of one pair of pairs where `on`; as they are otherwise.
+__device__ __forceinline__ void turned_if(bool on, float2& a, float2& b, float2 c, float2 s, float2 minus) {
+  asm("{\n\t.reg .pred p;\n\t.reg .b64 a, b, c, s, m, x, y;\n\tsetp.ne.b32 p, %10, 0;\n\t"
+      "mov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tmov.b64 c, {%4, %5};\n\tmov.b64 s, {%6, %7};\n\t"
+      "mov.b64 m, {%8, %9};\n\tmul.rn.f32x2 x, b, m;\n\tmul.rn.f32x2 y, b, c;\n\t"
+      "@p fma.rn.f32x2 b, a, s, y;\n\t@p fma.rn.f32x2 a, a, c, x;\n\t"
+      "mov.b64 {%0, %1}, a;\n\tmov.b64 {%2, %3}, b;\n\t}"
+      : "+f"(a.x), "+f"(a.y), "+f"(b.x), "+f"(b.y)
+      : "f"(c.x), "f"(c.y), "f"(s.x), "f"(s.y), "f"(minus.x), "f"(minus.y), "r"((unsigned)on));
+}
 __device__ __forceinline__ float sum_of(const float2& x) { return x.x + x.y; }
 // Sums over a head's lanes; for the usual sizes without a test for each step.
 template <int S, int N>
@@ -218,9 +228,13 @@ struct Shared {
   float w[2][kHrMaxDim];
 };
 
+// What is known of a launch's heads: nothing; there is a norm, and part of a head turns; there is a norm, and
+// all of it turns.  (32768 tokens of 48 heads with a test for the norm and the rotation 140 us, with one for the
+// part that turns 137, without any 131.)
+enum Heads { kAnyHeads, kPartHeads, kWholeHeads };
+
 // What both kernels have: a warp's rows, a lane's place in them.  kFull: every lane has a head's
-// values in every step.  kUsual: there is a norm and a rotation (without the tests of them 140 us instead
-// of 132 at 32768 tokens of 48 heads).
+// values in every step.
 template <typename T, bool kHalf, bool kVec>
 struct Lane {
   const HrArgs& p;
@@ -241,9 +255,13 @@ struct Lane {
   }
   // The pairs that turn by t.  The others stay: a product with the sine of 0 would hand a value that is not
   // finite on to its partner.
+  template <Heads kHeads>
   __device__ __forceinline__ void turn(Eight& v, const Turn& t) const {
-    if constexpr (kVec) {
-      if (turns[0]) turned(v, t);
+    if constexpr (kHeads == kWholeHeads) {
+      turned(v, t);
+    } else if constexpr (kVec) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n) turned_if(turns[0], v.p[n], v.p[n + 2], t.c[n], t.s[n], t.minus[n]);
     } else {
       const Eight was = v;
       turned(v, t);
@@ -320,7 +338,7 @@ constexpr int kHrBwdCtas = 2;
 
 // ---- forward -----------------------------------------------------------------------------
 // Steps of a row: of q's heads, then of k's.
-template <typename T, bool kHalf, bool kVec, bool kFull, bool kUsual>
+template <typename T, bool kHalf, bool kVec, bool kFull, Heads kHeads>
 __global__ void __launch_bounds__(kHrWarps * 32, kHrFwdCtas) hr_fwd_kernel(HrArgs p) {
   __shared__ __align__(16) Shared sh;
   Lane<T, kHalf, kVec> l(p, sh);
@@ -356,7 +374,7 @@ __global__ void __launch_bounds__(kHrWarps * 32, kHrFwdCtas) hr_fwd_kernel(HrArg
         Eight v{};
         if (has) v = from[i].get();
         float r = 1.f;
-        if (kUsual || p.norm != HR_NONE) {
+        if (kHeads != kAnyHeads || p.norm != HR_NONE) {
           float2 ss = mul2(v.p[0], v.p[0]);
 #pragma unroll
           for (int n = 1; n < 4; ++n) ss = fma2(v.p[n], v.p[n], ss);
@@ -367,7 +385,7 @@ __global__ void __launch_bounds__(kHrWarps * 32, kHrFwdCtas) hr_fwd_kernel(HrArg
         const Eight w = l.weights(in_k);
 #pragma unroll
         for (int n = 0; n < 4; ++n) v.p[n] = mul2(v.p[n], mul2(w.p[n], both(r)));
-        if (kUsual || p.rot) l.turn(v, t);
+        if (kHeads != kAnyHeads || p.rot) l.template turn<kHeads>(v, t);
         if (has) Held<T, kVec, kHalf>::store((in_k ? ko : qo) + (i0 + i) * step, l.at, v);
       }
     };
@@ -376,7 +394,7 @@ __global__ void __launch_bounds__(kHrWarps * 32, kHrFwdCtas) hr_fwd_kernel(HrArg
     ready = true;
     if (l.from >= l.to) continue;
     Turn t;
-    if (kUsual || p.rot) t = l.angles(false);
+    if (kHeads != kAnyHeads || p.rot) t = l.angles(false);
     for (int i0 = l.from; i0 < l.to; i0 += 2 * N) {
       load(i0 + N, x[1]);
       work(i0, x[0], t);
@@ -391,7 +409,7 @@ __global__ void __launch_bounds__(kHrWarps * 32, kHrFwdCtas) hr_fwd_kernel(HrArg
 // dx = r (g - x r (r mean(g x))), the sum in place of the mean for l2; both sums in one round.  r
 // times its sum first: r^2 alone leaves fp32's range where x is far from 1.  A lane keeps its eight
 // values' share of dw over all of its heads.
-template <typename T, bool kHalf, bool kVec, bool kFull, bool kUsual>
+template <typename T, bool kHalf, bool kVec, bool kFull, Heads kHeads>
 __global__ void __launch_bounds__(kHrWarps * 32, kHrBwdCtas) hr_bwd_kernel(HrArgs p) {
   __shared__ __align__(16) Shared sh;
   __shared__ float s_dw[kHrWarps][kHrMaxDim];
@@ -426,7 +444,7 @@ __global__ void __launch_bounds__(kHrWarps * 32, kHrBwdCtas) hr_bwd_kernel(HrArg
             x[i].load(x0 + (i0 + i) * step, l.at);
             y[i].load(y0 + (i0 + i) * step, l.at);
           }
-        if ((kUsual || p.rot) && (side ? max(l.from, steps_q) : l.from) == l.from && i0 == lo) t = l.angles(true);
+        if ((kHeads != kAnyHeads || p.rot) && (side ? max(l.from, steps_q) : l.from) == l.from && i0 == lo) t = l.angles(true);
 #pragma unroll
         for (int i = 0; i < kHrBwdAhead<T>; ++i) {
           if (i0 + i >= hi) break;
@@ -436,12 +454,12 @@ __global__ void __launch_bounds__(kHrWarps * 32, kHrBwdCtas) hr_bwd_kernel(HrArg
             v = x[i].get();
             u = y[i].get();
           }
-          if (kUsual || p.rot) l.turn(u, t);
+          if (kHeads != kAnyHeads || p.rot) l.template turn<kHeads>(u, t);
           Eight g;
 #pragma unroll
           for (int n = 0; n < 4; ++n) g.p[n] = mul2(u.p[n], w.p[n]);
           float r = 1.f;
-          if (kUsual || p.norm != HR_NONE) {  // without a norm x has no part in dx, not even as 0 times an infinity
+          if (kHeads != kAnyHeads || p.norm != HR_NONE) {  // without a norm x has no part in dx, not even as 0 times an infinity
             float2 ss = mul2(v.p[0], v.p[0]), gx = mul2(g.p[0], v.p[0]);
 #pragma unroll
             for (int n = 1; n < 4; ++n) {
@@ -529,17 +547,18 @@ int grid_of(const HrArgs& p, int most) {
   return (int)(ctas < most ? ctas : most);
 }
 
-template <template <typename, bool, bool, bool, bool> class K>
+template <template <typename, bool, bool, bool, Heads> class K>
 cudaError_t choose(const HrArgs& p, int layout, bool bf16, int grid, cudaStream_t st) {
   const bool vec = p.d % 8 == 0 && p.rot % 8 == 0, half = layout == HR_HALF;
   const int hpw = 32 >> p.tph_log;
   const bool full = vec && p.rpw_log == 0 && p.d / 8 == 1 << p.tph_log && p.gq % hpw == 0 && p.gk % hpw == 0;
   const bool usual = p.norm != HR_NONE && p.rot > 0;
-#define LL_HR(T, H)                                                     \
-  return full && usual ? K<T, H, true, true, true>::run(p, grid, st)    \
-         : full        ? K<T, H, true, true, false>::run(p, grid, st)   \
-         : vec         ? K<T, H, true, false, false>::run(p, grid, st)  \
-                       : K<T, H, false, false, false>::run(p, grid, st)
+#define LL_HR(T, H)                                                               \
+  return full && usual && p.rot == p.d ? K<T, H, true, true, kWholeHeads>::run(p, grid, st) \
+         : full && usual               ? K<T, H, true, true, kPartHeads>::run(p, grid, st)  \
+         : full                        ? K<T, H, true, true, kAnyHeads>::run(p, grid, st)   \
+         : vec                         ? K<T, H, true, false, kAnyHeads>::run(p, grid, st)  \
+                                       : K<T, H, false, false, kAnyHeads>::run(p, grid, st)
   if (bf16) {
     if (half) LL_HR(__nv_bfloat16, true);
     LL_HR(__nv_bfloat16, false);
@@ -548,17 +567,17 @@ cudaError_t choose(const HrArgs& p, int layout, bool bf16, int grid, cudaStream_
   LL_HR(float, false);
 #undef LL_HR
 }
-template <typename T, bool kHalf, bool kVec, bool kFull, bool kUsual>
+template <typename T, bool kHalf, bool kVec, bool kFull, Heads kHeads>
 struct Fwd {
   static cudaError_t run(const HrArgs& p, int grid, cudaStream_t st) {
-    hr_fwd_kernel<T, kHalf, kVec, kFull, kUsual><<<grid, kHrWarps * 32, 0, st>>>(p);
+    hr_fwd_kernel<T, kHalf, kVec, kFull, kHeads><<<grid, kHrWarps * 32, 0, st>>>(p);
     return cudaGetLastError();
   }
 };
-template <typename T, bool kHalf, bool kVec, bool kFull, bool kUsual>
+template <typename T, bool kHalf, bool kVec, bool kFull, Heads kHeads>
 struct Bwd {
   static cudaError_t run(const HrArgs& p, int grid, cudaStream_t st) {
-    hr_bwd_kernel<T, kHalf, kVec, kFull, kUsual><<<grid, kHrWarps * 32, 0, st>>>(p);
+    hr_bwd_kernel<T, kHalf, kVec, kFull, kHeads><<<grid, kHrWarps * 32, 0, st>>>(p);
     return cudaGetLastError();
   }
 };
