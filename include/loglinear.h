@@ -512,7 +512,8 @@ ll_status blocknorm_bwd(const blocknorm_shape* shape, const void* dx_new, const 
  * lengths: NULL, or (B) int32 on the device: row b holds lengths[b] tokens, clamped to [0, T].
  * What the tensors hold past them is not read; outputs there are written as zeros, and final
  * states are those after lengths[b] tokens (state_in itself for length 0).
- * r of -inf holds a state (a = 1, and n = 0 but for GS_NONE), inf decays it by exp(-decay).
+ * r of -inf holds a state (a = 1, and n = 0 but for GS_NONE), inf decays it by exp(-decay).  GS_RMS:
+ * where 1 - a^2 is below 2^-126, a decay of 0 among them, n and its slope count as 0.
  * The state and all arithmetic are fp32; h_t is rounded once, the state that goes on is not.
  * Results do not vary between calls.
  */

@@ -62,11 +62,12 @@ __device__ __forceinline__ float2 square_root(float2 x) {
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y.y) : "f"(x.y));
   return y;
 }
-// 1 / sqrt(x), 0 for 0; NaN stays NaN.
+// 1 / sqrt(x); x itself, as good as 0, below the smallest normal number, which the instruction takes for 0
+// (and whose inverse would make infinities); NaN stays NaN.
 __device__ __forceinline__ float inverse_root(float x) {
   float y;
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return x > 0.f ? y : x;
+  return x >= 1.17549435e-38f ? y : x;
 }
 // e^-x.  bf16: the exponent unit's own, 2^-22 relative and 2^-24 |x|, well below the inputs' step.
 template <typename T>
