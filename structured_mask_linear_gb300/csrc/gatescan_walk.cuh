@@ -217,8 +217,10 @@ struct Walk {
     __syncthreads();
     if (size > 1) cluster_sync();  // the others' shared memory and barriers are there from here on
   }
-  __device__ __forceinline__ ~Walk() {
-    if (size > 1) cluster_sync();  // nobody leaves while others may still write to it
+  // After the last step: nobody leaves while others may still write to it, and all have read the state that
+  // they began from, whose place the last one may take.
+  __device__ __forceinline__ void leave() {
+    if (size > 1) cluster_sync();
   }
 
   // The tokens from t0 (of tensor n from t0 - shift_n) of a step.  By TMA: one thread asks for them,
