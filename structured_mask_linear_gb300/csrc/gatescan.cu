@@ -136,7 +136,7 @@ struct Forward {
       consider<T, N, 2>(c, gs_fwd_kernel<T, kTma, M, kGate, 2>, p, dev, room[1]);
       consider<T, N, 4>(c, gs_fwd_kernel<T, kTma, M, kGate, 4>, p, dev, room[2]);
     }
-    if (c.t == 0) return cudaErrorInvalidConfiguration;
+    if (c.t == 0) return c.why != cudaSuccess ? c.why : cudaErrorInvalidConfiguration;
     if constexpr (kTma) {
       if (c.groups == 2) return launch<T, N, 2>(gs_fwd_kernel<T, kTma, M, kGate, 2>, p, c, x, true, st);
       if (c.groups == 4) return launch<T, N, 4>(gs_fwd_kernel<T, kTma, M, kGate, 4>, p, c, x, true, st);

@@ -163,7 +163,7 @@ struct Backward {
       consider<T, N, 2>(c, gs_bwd_kernel<T, kTma, M, kGate, 2>, p, dev, room[1]);
       consider<T, N, 4>(c, gs_bwd_kernel<T, kTma, M, kGate, 4>, p, dev, room[2]);
     }
-    if (c.t == 0) return cudaErrorInvalidConfiguration;
+    if (c.t == 0) return c.why != cudaSuccess ? c.why : cudaErrorInvalidConfiguration;
     if constexpr (kTma) {
       if (c.groups == 2) return launch<T, N, 2>(gs_bwd_kernel<T, kTma, M, kGate, 2>, p, c, x, true, st);
       if (c.groups == 4) return launch<T, N, 4>(gs_bwd_kernel<T, kTma, M, kGate, 4>, p, c, x, true, st);

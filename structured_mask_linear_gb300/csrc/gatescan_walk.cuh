@@ -334,29 +334,23 @@ void launch_config(int size, unsigned grid, int smem, cudaStream_t st, cudaLaunc
   cfg.numAttrs = size > 1 ? 1 : 0;
 }
 template <typename K>
-int clusters_at_once(K kernel, int size, int smem, int dev, Room& room) {
-  std::atomic<int>* kept = dev < 64 ? &room.clusters[dev][size] : nullptr;
-  if (kept)
-    if (const int n = kept->load(std::memory_order_acquire)) return n - 1;
-  int n = 0;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
-  if (e == cudaSuccess && size > 1) {
-    cudaLaunchConfig_t cfg;
-    cudaLaunchAttribute attr;
-    launch_config(size, (unsigned)size, smem, nullptr, cfg, &attr);
-    e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
-  } else if (e == cudaSuccess) {
-    int per_sm = 0, sms = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kGsWarps * 32, (size_t)smem);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    n = per_sm * sms;
-  }
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    n = 0;
-  }
-  if (kept) kept->store(n + 1, std::memory_order_release);
-  return n;
+cudaError_t clusters_at_once(K kernel, int size, int smem, int dev, Room& room, int& clusters) {
+  return ask_once(dev < 64 ? &room.clusters[dev][size] : nullptr, clusters, [&](int& n) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (e == cudaSuccess && size > 1) {
+      cudaLaunchConfig_t cfg;
+      cudaLaunchAttribute attr;
+      launch_config(size, (unsigned)size, smem, nullptr, cfg, &attr);
+      e = cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+    } else if (e == cudaSuccess) {
+      int per_sm = 0, sms = 0;
+      e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kGsWarps * 32, (size_t)smem);
+      if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+      n = per_sm * sms;
+    }
+    if (e != cudaSuccess) cudaGetLastError();  // reported, or the layout goes without this size
+    return e;
+  });
 }
 
 // Map over (D, T, B) with a box of a unit's channels and a chunk of tokens.
@@ -381,22 +375,25 @@ constexpr double kMore = 0.42, kRound = 0.01, kGroup = 0.05;
 
 struct Choice {
   int groups, size, steps, units;
-  double t;  // 0: none yet
+  double t;         // 0: none yet
+  cudaError_t why;  // an error of a size that could not be asked about
 };
 template <typename T, int N, int G, typename K>
 void consider(Choice& best, K kernel, const GsArgs& p, int dev, Room& room) {
   const int chunks = (p.T + kChunk<T, N, G> - 1) / kChunk<T, N, G>, wide = kGsWidth / G;
   const int units = p.B * ((p.D + wide - 1) / wide);
   for (int size = 1; size <= kGsMaxCluster && (size == 1 || size <= chunks); ++size) {
-    const int n = clusters_at_once(kernel, size, smem_bytes<T, N, G>(size), dev, room);
-    if (n < 1) continue;
+    int n = 0;
+    const cudaError_t e = clusters_at_once(kernel, size, smem_bytes<T, N, G>(size), dev, room, n);
+    if (e != cudaSuccess) best.why = e;
+    if (e != cudaSuccess || n < 1) continue;
     const int steps = (chunks + size - 1) / size;
     auto turn = [&](int clusters) {  // in steps of a CTA alone
       const int on_sm = (clusters * size + 151) / 152;
       return steps * (1.0 + kMore * (on_sm - 1)) * (1.0 + kRound * size) * (1.0 + kGroup * (G - 1));
     };
     const double t = units / n * turn(n) + (units % n ? turn(units % n) : 0.0);
-    if (best.t == 0 || t < best.t) best = Choice{G, size, steps, units, t};
+    if (best.t == 0 || t < best.t) best = Choice{G, size, steps, units, t, best.why};
   }
 }
 template <typename T, int N, int G, typename K>

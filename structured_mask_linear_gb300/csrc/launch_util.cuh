@@ -1,4 +1,5 @@
-// Host helper: a kernel's dynamic shared memory limit, raised once per device.
+// Host helpers: a kernel's dynamic shared memory limit, raised once per device; what a device is asked
+// once; launches that may start early.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -23,6 +24,20 @@ struct SmemLimit {
     return e;
   }
 };
+
+// What `ask(answer)` finds, asked once and then kept in `slot` (NULL: not kept; 0: not asked yet, so the answer
+// + 1).  Only an answer is kept: after an error the next call asks again.
+template <typename F>
+cudaError_t ask_once(std::atomic<int>* slot, int& answer, F ask) {
+  if (slot)
+    if (const int n = slot->load(std::memory_order_acquire)) {
+      answer = n - 1;
+      return cudaSuccess;
+    }
+  const cudaError_t e = ask(answer);
+  if (e == cudaSuccess && slot) slot->store(answer + 1, std::memory_order_release);
+  return e;
+}
 
 // A launch that may start before the kernel ahead of it on the stream has ended; the kernel waits
 // for that one itself (griddepcontrol.wait) before it reads what it wrote.
