@@ -1,5 +1,5 @@
-"""Blocks of decoders, as layers: the operators under autograd (first derivatives; a second one
-raises), and a stack of blocks that trains, takes a prompt and generates token by token.
+"""Blocks of decoders, as layers: the operators under autograd (first derivatives, backward; a second one
+and forward mode raise), and a stack of blocks that trains, takes a prompt and generates token by token.
 
 A block holds one norm before it, projections, a mixer of tokens, a norm of each head under the
 gate, the projection back, and a norm after it under a learned scale:
@@ -31,6 +31,7 @@ from typing import List, Optional, Sequence, Tuple
 
 import torch
 from torch import nn
+from torch.autograd import forward_ad
 from torch.nn import functional as F
 
 from . import (blocknorm_bwd, blocknorm_fwd, ffgate_bwd, ffgate_fwd, gatescan_bwd, gatescan_decode_step, gatescan_fwd,
@@ -54,6 +55,16 @@ class _FirstOrder(torch.autograd.Function):
 
 def _first_order(name, grads, *inputs):
     return _FirstOrder.apply(name, len(grads), *grads, *inputs) if torch.is_grad_enabled() else grads
+
+
+def _constant(*tensors):
+    """Whether nothing can be derived from a call on these: grad mode is off, and none carries a tangent, which
+    no_grad leaves to it (and which the functions below refuse)."""
+    if torch.is_grad_enabled():
+        return False
+    # outside of forward mode, where every token of a generation is, there is no need to ask each tensor
+    return getattr(forward_ad, "_current_level", 0) < 0 or all(
+        t is None or forward_ad.unpack_dual(t).tangent is None for t in tensors)
 
 
 class _Lindecay(torch.autograd.Function):
@@ -174,7 +185,7 @@ def headrope(q, k=None, w_q=None, w_k=None, inv_freq=None, positions=None, layou
     are constants: an inv_freq that asks for a gradient, which there is none of, is refused."""
     if inv_freq is not None and inv_freq.requires_grad and torch.is_grad_enabled():
         raise ValueError("inv_freq is a constant of headrope, which has no gradient for it: detach it")
-    if not torch.is_grad_enabled():
+    if _constant(q, k, w_q, w_k, inv_freq):
         return headrope_fwd(q, k, w_q=w_q, w_k=w_k, inv_freq=inv_freq, positions=positions, layout=layout, norm=norm, eps=eps,
                             scale_q=scale_q, scale_k=scale_k)
     return _Headrope.apply(q, k, w_q, w_k, inv_freq, positions,
@@ -183,7 +194,7 @@ def headrope(q, k=None, w_q=None, w_k=None, inv_freq=None, positions=None, layou
 
 def ffgate(x, w_gate, w_up, act="silu"):
     """ffgate_fwd under autograd (first derivatives)."""
-    if not torch.is_grad_enabled():
+    if _constant(x, w_gate, w_up):
         return ffgate_fwd(x, w_gate, w_up, act=act)
     return _Ffgate.apply(x, w_gate, w_up, act)
 
@@ -198,7 +209,7 @@ def lindecay(q, k, v, log_a, lengths=None, state_in=None) -> Tuple[torch.Tensor,
 
 def blocknorm(y=None, w_post=None, x=None, gate=None, scale=None, w_pre=None, group=None, act="silu", eps=1e-6):
     """blocknorm_fwd under autograd (first derivatives): (x', h)."""
-    if not torch.is_grad_enabled():
+    if _constant(y, w_post, x, gate, scale, w_pre):
         return blocknorm_fwd(y, w_post, x, gate, scale, w_pre, group=group, act=act, eps=eps)
     x_new, h = _Blocknorm.apply(y, w_post, x, gate, scale, w_pre, group, act, eps)
     return (x if y is None else x_new), h
@@ -384,7 +395,7 @@ class DecayStack(nn.Module):
         how many tokens each row has before this one; rotary asks for them."""
         if self.rotary and positions is None:
             raise ValueError("a stack with rotary heads needs each row's position")
-        _, h = blocknorm_fwd(x=x_t, w_pre=self.blocks[0].w_pre if len(self.blocks) else self.w_last, eps=self.eps)
+        _, h = blocknorm(x=x_t, w_pre=self.blocks[0].w_pre if len(self.blocks) else self.w_last, eps=self.eps)
         for i, b in enumerate(self.blocks):
             o, g = b.mix_token(h, states[i], positions)
             x_t, h = self._joint(i, b.back(o, g), x_t)
