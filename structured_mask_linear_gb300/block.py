@@ -34,7 +34,7 @@ from torch import nn
 from torch.autograd import forward_ad
 from torch.nn import functional as F
 
-from . import (blocknorm_bwd, blocknorm_fwd, ffgate_bwd, ffgate_fwd, gatescan_bwd, gatescan_decode_step, gatescan_fwd,
+from . import (MIXES, blocknorm_bwd, blocknorm_fwd, ffgate_bwd, ffgate_fwd, gatescan_bwd, gatescan_decode_step, gatescan_fwd,
                headrope_bwd, headrope_fwd, lindecay_bwd, lindecay_decode_step, lindecay_fwd, rope_frequencies)
 
 
@@ -304,6 +304,8 @@ class ScanBlock(nn.Module):
         super().__init__()
         if heads <= 0 or channels % heads:
             raise ValueError(f"channels ({channels}) must be a multiple of heads ({heads})")
+        if mix not in MIXES:
+            raise ValueError(f"mix must be one of {sorted(MIXES)}, got {mix!r}")
         self.channels, self.d_v, self.head_eps, self.mixing = channels, channels // heads, head_eps, mix
         product = lambda n_out, n_in, shrink=1: _product(n_out, n_in, dtype, device, shrink)  # noqa: E731
         weight = lambda n, value: _weight(n, value, device)  # noqa: E731
@@ -340,20 +342,24 @@ def _feed_forward(block, width, ff, act, product, weight):
 
 class DecayStack(nn.Module):
     """Blocks on a residual stream.  forward() for training and prompts, step() for a token.  eps: of
-    the norms over the stream and over a block's output; head_eps: of the norm of each head.
+    the norms over the stream and over a block's output; head_eps: of the norm of each head, in blocks of
+    both kinds (none given: 1 in DecayBlocks, 1e-6 in ScanBlocks).
     rotary, qk_norm, ff: of every block, as DecayBlock has them; recurrent: which blocks (by index)
-    are ScanBlocks, of `channels` channels (width unless given)."""
+    are ScanBlocks, of `channels` channels (width unless given) with n(a) as `mix` says."""
 
     def __init__(self, layers: int, width: int, heads: int, groups: int, d_k: int, d_v: int, dtype=torch.bfloat16,
-                 device="cuda", eps: float = 1e-6, head_eps: float = 1.0, rotary: int = 0, qk_norm: str = "none", ff: int = 0,
-                 ff_act: str = "silu", recurrent: Sequence[int] = (), channels: int = 0, base: float = 10000.0):
+                 device="cuda", eps: float = 1e-6, head_eps: Optional[float] = None, rotary: int = 0, qk_norm: str = "none", ff: int = 0,
+                 ff_act: str = "silu", recurrent: Sequence[int] = (), channels: int = 0, base: float = 10000.0,
+                 mix: str = "rms"):
         super().__init__()
         if any(not 0 <= i < layers for i in recurrent):
             raise ValueError(f"recurrent blocks {tuple(recurrent)} are not among {layers}")
         self.eps, self.rotary = eps, rotary
         self.blocks = nn.ModuleList(
-            ScanBlock(width, channels or width, heads, dtype, device, ff=ff, ff_act=ff_act) if i in recurrent else
-            DecayBlock(width, heads, groups, d_k, d_v, dtype, device, head_eps, rotary, qk_norm, ff, ff_act, base)
+            ScanBlock(width, channels or width, heads, dtype, device, 1e-6 if head_eps is None else head_eps, mix, ff, ff_act)
+            if i in recurrent else
+            DecayBlock(width, heads, groups, d_k, d_v, dtype, device, 1.0 if head_eps is None else head_eps, rotary, qk_norm, ff,
+                       ff_act, base)
             for i in range(layers))
         self.w_last = nn.Parameter(torch.ones(width, dtype=torch.float32, device=device))
 
