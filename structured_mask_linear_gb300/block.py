@@ -382,9 +382,12 @@ class DecayStack(nn.Module):
     def forward(self, x, lengths: Optional[torch.Tensor] = None, states: Optional[List[torch.Tensor]] = None,
                 start: Optional[torch.Tensor] = None):
         """x (B, T, width), lengths (B,) int32 and the blocks' states before it (none: zero).
-        start (B,) int32: each row's first position, for rotary (none: 0).
+        start (B,) int32: each row's first position, for rotary, which asks for it where states are given
+        (none: 0).
         Returns the stream under its last norm and the states after each row's length."""
         positions = None
+        if self.rotary and states is not None and start is None:
+            raise ValueError("a stack with rotary heads that goes on from states needs each row's first position")
         if self.rotary and start is not None:
             positions = start[:, None] + torch.arange(x.shape[1], dtype=torch.int32, device=x.device)
         _, h = blocknorm(x=x, w_pre=self.blocks[0].w_pre if len(self.blocks) else self.w_last, eps=self.eps)
