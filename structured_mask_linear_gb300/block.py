@@ -233,11 +233,11 @@ def _weight(n, value, device):
 class DecayBlock(nn.Module):
     """One block's weights, and what it does between its two norms.  rotary: how many values of
     each head of q and k turn with the position; qk_norm ("rms" or "l2"): a norm of those heads
-    before, with weights.  ff: width of its feed-forward half."""
+    before, with weights and the epsilon qk_eps.  ff: width of its feed-forward half."""
 
     def __init__(self, width: int, heads: int, groups: int, d_k: int, d_v: int, dtype=torch.bfloat16, device="cuda",
                  head_eps: float = 1.0, rotary: int = 0, qk_norm: str = "none", ff: int = 0, ff_act: str = "silu",
-                 base: float = 10000.0):
+                 base: float = 10000.0, qk_eps: float = 1e-6):
         super().__init__()
         if heads <= 0 or groups <= 0 or heads % groups:
             raise ValueError(f"heads ({heads}) must be a multiple of groups ({groups})")
@@ -250,7 +250,7 @@ class DecayBlock(nn.Module):
         self.w_pre, self.w_head = weight(width, 1.0), weight(heads * d_v, 1.0)
         self.w_post, self.scale = weight(width, 1.0), weight(width, 0.5)
         self.register_buffer("log_a", head_decays(heads).to(device))
-        self.qk_norm, self.rotary = qk_norm, rotary
+        self.qk_norm, self.qk_eps, self.rotary = qk_norm, qk_eps, rotary
         if qk_norm != "none":  # q begins smaller by sqrt(d_k), as without the norm
             self.w_q_norm, self.w_k_norm = weight(d_k, d_k ** -0.5 if qk_norm == "rms" else 1.0), weight(d_k, 1.0)
         if rotary:
@@ -273,7 +273,8 @@ class DecayBlock(nn.Module):
         if self.qk_norm == "none" and not self.rotary:
             return q, k
         w_q, w_k = (None, None) if self.qk_norm == "none" else (self.w_q_norm, self.w_k_norm)
-        return headrope(q, k, w_q, w_k, self.inv_freq if self.rotary else None, positions, norm=self.qk_norm)
+        return headrope(q, k, w_q, w_k, self.inv_freq if self.rotary else None, positions, norm=self.qk_norm,
+                        eps=self.qk_eps)
 
     def mix(self, h, lengths, state, positions):
         """The heads' outputs, the gate, and the states after."""
@@ -344,13 +345,13 @@ class DecayStack(nn.Module):
     """Blocks on a residual stream.  forward() for training and prompts, step() for a token.  eps: of
     the norms over the stream and over a block's output; head_eps: of the norm of each head, in blocks of
     both kinds (none given: 1 in DecayBlocks, 1e-6 in ScanBlocks).
-    rotary, qk_norm, ff: of every block, as DecayBlock has them; recurrent: which blocks (by index)
+    rotary, qk_norm, qk_eps, ff: of every block, as DecayBlock has them; recurrent: which blocks (by index)
     are ScanBlocks, of `channels` channels (width unless given) with n(a) as `mix` says."""
 
     def __init__(self, layers: int, width: int, heads: int, groups: int, d_k: int, d_v: int, dtype=torch.bfloat16,
                  device="cuda", eps: float = 1e-6, head_eps: Optional[float] = None, rotary: int = 0, qk_norm: str = "none", ff: int = 0,
                  ff_act: str = "silu", recurrent: Sequence[int] = (), channels: int = 0, base: float = 10000.0,
-                 mix: str = "rms"):
+                 mix: str = "rms", qk_eps: float = 1e-6):
         super().__init__()
         if any(not 0 <= i < layers for i in recurrent):
             raise ValueError(f"recurrent blocks {tuple(recurrent)} are not among {layers}")
@@ -359,7 +360,7 @@ class DecayStack(nn.Module):
             ScanBlock(width, channels or width, heads, dtype, device, 1e-6 if head_eps is None else head_eps, mix, ff, ff_act)
             if i in recurrent else
             DecayBlock(width, heads, groups, d_k, d_v, dtype, device, 1.0 if head_eps is None else head_eps, rotary, qk_norm, ff,
-                       ff_act, base)
+                       ff_act, base, qk_eps)
             for i in range(layers))
         self.w_last = nn.Parameter(torch.ones(width, dtype=torch.float32, device=device))
 

@@ -33,3 +33,17 @@ def test_options_reach_every_block(asked, recurrent):
 def test_an_unknown_mix_is_refused():
     with pytest.raises(ValueError, match="mix"):
         stack(torch.float32, mix="mean")
+
+
+@pytest.mark.parametrize("qk_norm", ["rms", "l2"])
+def test_the_epsilon_of_the_norms_of_q_and_k(qk_norm):
+    """Of the size of what it is added to."""
+    from decoder_ref import headrope
+
+    net, h = stack(torch.float32, layers=1, recurrent=(), qk_norm=qk_norm, qk_eps=0.75), draw(2, 9, torch.float32)
+    b, d = net.blocks[0], double(net).blocks[0]
+    p = torch.arange(9, dtype=torch.int32).expand(2, 9).contiguous()
+    with torch.no_grad():
+        got = b.place(*b.project(h.to(DEV))[:2], p.to(DEV))
+    for x, y, w in zip(got, d.project(h.double())[:2], (d.w_q_norm, d.w_k_norm)):
+        assert rel(x, headrope(y, w, b.inv_freq.double().cpu(), p, "half", qk_norm, 0.75)) <= OUT[torch.float32]
