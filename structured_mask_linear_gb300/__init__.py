@@ -699,11 +699,12 @@ def headrope_fwd(q, k=None, w_q=None, w_k=None, inv_freq=None, positions=None, l
 
 
 def headrope_bwd(dq_out, q, dk_out=None, k=None, w_q=None, w_k=None, inv_freq=None, positions=None, layout="half",
-                 norm="rms", eps=1e-6, scale_q=1.0, scale_k=1.0, workspace=None, stream=None):
-    """Gradients of sum(dq_out * q') + sum(dk_out * k') of headrope_fwd, from its inputs."""
+                 norm="rms", eps=1e-6, scale_q=1.0, scale_k=1.0, workspace=None, stream=None, dq=None, dk=None):
+    """Gradients of sum(dq_out * q') + sum(dk_out * k') of headrope_fwd, from its inputs.  dq and dk may be
+    given, dq_out and dk_out themselves among others."""
     return HeadropeGrads(*(_native_module or _native()).headrope_bwd(
         dq_out, q, dk_out, k, w_q, w_k, inv_freq, positions, _code(LAYOUTS, "layout", layout),
-        _code(HEAD_NORMS, "norm", norm), eps, scale_q, scale_k, workspace,
+        _code(HEAD_NORMS, "norm", norm), eps, scale_q, scale_k, dq, dk, workspace,
         None if stream is None else _stream_ptr(stream)))
 
 

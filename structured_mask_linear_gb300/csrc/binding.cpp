@@ -573,18 +573,22 @@ PyObject* py_headrope_fwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 PyObject* py_headrope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 15, [&]() -> PyObject* {
+  return guarded(n, 17, [&]() -> PyObject* {
     const at::Tensor &dqo = tensor(a[0], "dq_out", false), &q = tensor(a[1], "q", false), &dko = tensor(a[2], "dk_out", true),
                      &k = tensor(a[3], "k", true), &w_q = tensor(a[4], "w_q", true), &w_k = tensor(a[5], "w_k", true),
-                     &inv_freq = tensor(a[6], "inv_freq", true), &positions = tensor(a[7], "positions", true);
+                     &inv_freq = tensor(a[6], "inv_freq", true), &positions = tensor(a[7], "positions", true),
+                     &dq_given = tensor(a[13], "dq", true), &dk_given = tensor(a[14], "dk", true);
     const Heads l = heads_checked(q, k, w_q, w_k, inv_freq, positions, a + 8);
     check(dqo, "dq_out", q.sizes(), q.scalar_type(), l.device);
     if (k.defined() != dko.defined()) refuse(PyExc_ValueError, "k and dk_out go together");
     if (k.defined()) check(dko, "dk_out", k.sizes(), q.scalar_type(), l.device);
-    const Target on(a[14], l.device);
+    check(dq_given, "dq", q.sizes(), q.scalar_type(), l.device);
+    if (dk_given.defined() && !k.defined()) refuse(PyExc_ValueError, "dk is given without k");
+    if (k.defined()) check(dk_given, "dk", k.sizes(), q.scalar_type(), l.device);
+    const Target on(a[16], l.device);
     const bool sums = w_q.defined() || w_k.defined();
-    const at::Tensor ws = sums ? workspace_of(a[13], entry.hr_bytes(&l.shape), l.device, "headrope_bwd") : at::Tensor();
-    const at::Tensor dq = new_like(q), dk = new_like(k), dw_q = new_like(w_q), dw_k = new_like(w_k);
+    const at::Tensor ws = sums ? workspace_of(a[15], entry.hr_bytes(&l.shape), l.device, "headrope_bwd") : at::Tensor();
+    const at::Tensor dq = given_or_like(dq_given, q), dk = given_or_like(dk_given, k), dw_q = new_like(w_q), dw_k = new_like(w_k);
     ll_status st;
     Py_BEGIN_ALLOW_THREADS
     st = entry.hr_bwd(&l.shape, ptr(dqo), ptr(dko), ptr(q), ptr(k), ptr<float>(w_q), ptr<float>(w_k),
@@ -592,6 +596,7 @@ PyObject* py_headrope_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
                       ptr(ws), bytes_of(ws), on.handle);
     Py_END_ALLOW_THREADS
     check_status(st, "headrope_bwd");
+    written({dq_given, dk_given});
     return wrap_all({dq, dk, dw_q, dw_k});
   });
 }
