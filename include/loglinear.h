@@ -528,7 +528,7 @@ typedef struct {
 
 /*
  * The whole sequence.  i, lengths, state_in, state_out may be NULL.  h may be x, r or i;
- * state_out may be state_in.
+ * state_out may be state_in; otherwise no output may overlap an input or another output.
  */
 ll_status gatescan_fwd(const gatescan_shape* shape, const void* x, const void* r, const void* i, const float* decay,
                        const int* lengths, const float* state_in, void* h, float* state_out, void* stream);
@@ -552,7 +552,7 @@ ll_status gatescan_bwd(const gatescan_shape* shape, const void* dh, const void* 
 
 /*
  * One token of every row; shape->T is ignored.  x_t, r_t, i_t (NULL: none), h_t (B, dim) dtype;
- * states (B, dim) fp32, read and updated in place.  h_t may be x_t, r_t or i_t.
+ * states (B, dim) fp32, read and updated in place.  h_t may be x_t, r_t or i_t; nothing else may overlap.
  */
 ll_status gatescan_decode_step(const gatescan_shape* shape, const void* x_t, const void* r_t, const void* i_t,
                                const float* decay, float* states, void* h_t, void* stream);
@@ -589,7 +589,7 @@ typedef struct {
   ll_dtype dtype;
 } headrope_shape;
 
-/* q_out and k_out are written; each may be its own input. */
+/* q_out and k_out are written; each may be its own input, and may overlap nothing else. */
 ll_status headrope_fwd(const headrope_shape* shape, const void* q, const void* k, const float* w_q, const float* w_k,
                        const float* inv_freq, const int* positions, void* q_out, void* k_out, void* stream);
 
@@ -598,7 +598,7 @@ size_t headrope_bwd_workspace_bytes(const headrope_shape* shape);
 
 /*
  * Gradients of sum(dq_out * q_out) + sum(dk_out * k_out), from the forward's inputs.
- *   dq, dk      written; each may be its own dq_out or dk_out
+ *   dq, dk      written; each may be its own dq_out or dk_out, and may overlap nothing else
  *   dw_q, dw_k  NULL, or (dim) fp32, each with its weight, written; summed in a fixed order
  *   workspace   with dw_q or dw_k; contents do not matter
  */

@@ -11,6 +11,11 @@ namespace {
 using ll::GsArgs;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool among(const void* o, std::initializer_list<const void*> others) {
+  for (const void* q : others)
+    if (o && o == q) return true;
+  return false;
+}
 
 ll_status check_shape(const gatescan_shape* s, bool seq) {
   if (!s) return LL_ERR_NULL;
@@ -45,6 +50,7 @@ ll_status gatescan_fwd(const gatescan_shape* s, const void* x, const void* r, co
   for (const void* q : {x, r, i, (const void*)decay, (const void*)lengths, (const void*)state_in, (const void*)h,
                         (const void*)state_out})
     if (!aligned16(q)) return LL_ERR_ALIGN;
+  if (among(h, {decay, lengths, state_in, state_out}) || among(state_out, {x, r, i, decay, lengths})) return LL_ERR_SHAPE;
   GsArgs p = base_args(s);
   p.x = x;
   p.r = r;
@@ -115,6 +121,7 @@ ll_status gatescan_decode_step(const gatescan_shape* s, const void* x_t, const v
   if (!x_t || !r_t || !decay || !states || !h_t) return LL_ERR_NULL;
   for (const void* q : {x_t, r_t, i_t, (const void*)decay, (const void*)states, (const void*)h_t})
     if (!aligned16(q)) return LL_ERR_ALIGN;
+  if (among(states, {x_t, r_t, i_t, decay, h_t}) || among(h_t, {decay})) return LL_ERR_SHAPE;
   const ll::GsStepArgs p{(long long)s->batch * s->dim, s->dim, x_t, r_t, i_t, decay, states, h_t};
   const cudaError_t e = ll::launch_gs_step(p, s->mix, s->dtype == LL_BF16, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? LL_OK : LL_ERR_CUDA;

@@ -9,6 +9,13 @@
 namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// Whether an output takes the place of what all rows read.
+bool over_shared(std::initializer_list<const void*> outs, std::initializer_list<const void*> shared) {
+  for (const void* o : outs)
+    for (const void* q : shared)
+      if (o && o == q) return true;
+  return false;
+}
 
 ll_status check_shape(const headrope_shape* s) {
   if (!s) return LL_ERR_NULL;
@@ -52,6 +59,7 @@ ll_status headrope_fwd(const headrope_shape* s, const void* q, const void* k, co
   for (const void* x : {q, k, (const void*)w_q, (const void*)w_k, (const void*)inv_freq, (const void*)positions,
                         (const void*)q_out, (const void*)k_out})
     if (!aligned16(x)) return LL_ERR_ALIGN;
+  if (over_shared({q_out, k_out}, {w_q, w_k, inv_freq, positions})) return LL_ERR_SHAPE;
   ll::HrArgs p = base_args(s);
   p.q = q;
   p.k = k;
@@ -82,6 +90,9 @@ ll_status headrope_bwd(const headrope_shape* s, const void* dq_out, const void* 
                         (const void*)positions, (const void*)dq, (const void*)dk, (const void*)dw_q, (const void*)dw_k,
                         (const void*)workspace})
     if (!aligned16(x)) return LL_ERR_ALIGN;
+  if (over_shared({dq, dk, dw_q, dw_k}, {w_q, w_k, inv_freq, positions}) || over_shared({dw_q, dw_k}, {dq, dk, dq_out, dk_out, q, k}) ||
+      (dw_q && dw_q == dw_k))
+    return LL_ERR_SHAPE;
   if ((dw_q || dw_k) && (!workspace || workspace_bytes < headrope_bwd_workspace_bytes(s))) return LL_ERR_WORKSPACE;
   ll::HrArgs p = base_args(s);
   p.q = q;
