@@ -402,7 +402,7 @@ __global__ void __cluster_dims__(kGroup, 1, 1) __launch_bounds__(kFfThreads, 1)
         if (col + 8 * h >= r.cols) break;  // a multiple of 8
         float m[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m[j] = ff_act(g[8 * h + j], p.act) * u[8 * h + j];
+        for (int j = 0; j < 8; ++j) m[j] = ff_act<T>(g[8 * h + j], p.act) * u[8 * h + j];
         put_eight<T>(p.m, at + 8 * h, m);
         if (p.gate) {
           put_eight<T>(p.gate, at + 8 * h, g + 8 * h);
@@ -481,8 +481,8 @@ __global__ void __cluster_dims__(kGroup, 1, 1) __launch_bounds__(kFfThreads, 1)
           for (int c = 0; c < 2; ++c) put(r, r.out_up, v[1] + 32 * c, c, col, row);
         }
         if (O::kHalf) {
-          ff_gated<32>(v[0], v[1], p.act);
-          ff_gated<32>(v[0] + 32, v[1] + 32, p.act);
+          ff_gated<T, 32>(v[0], v[1], p.act);
+          ff_gated<T, 32>(v[0] + 32, v[1] + 32, p.act);
         }
 #pragma unroll
         for (int c = 0; c < 2; ++c) put(r, r.out, v[0] + 32 * c, c, col, row);
@@ -521,7 +521,7 @@ __global__ void __cluster_dims__(kGroup, 1, 1) __launch_bounds__(kFfThreads, 1)
             ptx::tmem_ld32(d + 128 + from + 32 * c, u);
             ptx::tmem_ld_wait();
             if (c == 1 && r.out_gate < 0) release();
-            ff_gated<32>(g, u, p.act);
+            ff_gated<T, 32>(g, u, p.act);
             put(r, r.out, g, c, col, row);
           }
           if (r.out_gate >= 0) {  // what the backward needs
@@ -664,7 +664,7 @@ __global__ void __launch_bounds__(256) ff_act_bwd_kernel(const T* dm, const T* g
         if (sizeof(T) == 4) return __uint_as_float(w[j % 4]);
         return __uint_as_float(j & 1 ? w[j / 2] & 0xffff0000u : w[j / 2] << 16);
       };
-      const float2 f = ff_act_and_slope(value(g), act);
+      const float2 f = ff_act_and_slope<T>(value(g), act);
       a[j] = value(d) * value(u) * f.y;
       b[j] = value(d) * f.x;
     }
@@ -707,7 +707,7 @@ __global__ void __launch_bounds__(256) ff_join_kernel(const __grid_constant__ Ff
         put(j.up, v[1]);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[0][i] = ff_act(v[0][i], j.act) * v[1][i];
+      for (int i = 0; i < 4; ++i) v[0][i] = ff_act<T>(v[0][i], j.act) * v[1][i];
     }
     put(r.out, v[0]);
   }

@@ -1,52 +1,68 @@
-// The gated feed-forward block's activations and their derivatives, in fp32.
+// The gated feed-forward block's activations and their derivatives, in fp32.  T: the type of what comes of
+// them, whose steps say how exact the exponentials have to be.
 #pragma once
+
+#include <cuda_bf16.h>
 
 #include "../../include/loglinear.h"
 
 namespace ll {
 
-__device__ __forceinline__ float ff_sigmoid(float x) {
-  float e, y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + e));
+__device__ __forceinline__ float ff_reciprocal(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+template <typename T>
+__device__ __forceinline__ float ff_sigmoid(float x) {
+  if constexpr (sizeof(T) == 2) {
+    // the exponent unit's own, |x| 2^-24 relative: well below a step of bf16
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.4426950408889634f));
+    return ff_reciprocal(1.f + e);
+  } else {
+    const float e = expf(-fabsf(x)), s = ff_reciprocal(1.f + e);
+    return x >= 0.f ? s : e * s;
+  }
+}
+template <typename T>
 __device__ __forceinline__ float ff_act(float x, int act) {
   switch (act) {
-    case FF_SILU: return x * ff_sigmoid(x);
-    case FF_SIGMOID: return ff_sigmoid(x);
+    case FF_SILU: return x * ff_sigmoid<T>(x);
+    case FF_SIGMOID: return ff_sigmoid<T>(x);
     case FF_GELU: return 0.5f * x * erfcf(x * -0.70710678118654752f);
     default: return x;
   }
 }
 // g = act(g) u.  The choice comes first: made for every value among its instructions it took longer than they.
-template <int N>
+template <typename T, int N>
 __device__ __forceinline__ void ff_gated(float* g, const float* u, int act) {
   auto each = [&](auto f) {
 #pragma unroll
     for (int j = 0; j < N; ++j) g[j] = f(g[j]) * u[j];
   };
   switch (act) {
-    case FF_SILU: each([](float x) { return ff_act(x, FF_SILU); }); break;
-    case FF_SIGMOID: each([](float x) { return ff_act(x, FF_SIGMOID); }); break;
-    case FF_GELU: each([](float x) { return ff_act(x, FF_GELU); }); break;
+    case FF_SILU: each([](float x) { return ff_act<T>(x, FF_SILU); }); break;
+    case FF_SIGMOID: each([](float x) { return ff_act<T>(x, FF_SIGMOID); }); break;
+    case FF_GELU: each([](float x) { return ff_act<T>(x, FF_GELU); }); break;
     default: each([](float x) { return x; });
   }
 }
 // act(x) and its derivative.
+template <typename T>
 __device__ __forceinline__ float2 ff_act_and_slope(float x, int act) {
   switch (act) {
     case FF_SILU: {
-      const float s = ff_sigmoid(x);
-      return make_float2(x * s, s * fmaf(x, 1.f - s, 1.f));
+      const float g = ff_sigmoid<T>(x);
+      return make_float2(x * g, g * fmaf(x, 1.f - g, 1.f));
     }
     case FF_SIGMOID: {
-      const float s = ff_sigmoid(x);
-      return make_float2(s, s * (1.f - s));
+      const float g = ff_sigmoid<T>(x);
+      return make_float2(g, g * (1.f - g));
     }
     case FF_GELU: {
-      const float c = 0.5f * erfcf(x * -0.70710678118654752f);
-      return make_float2(x * c, fmaf(x * 0.3989422804014327f, __expf(-0.5f * x * x), c));
+      const float c = 0.5f * erfcf(x * -0.70710678118654752f), z = -0.5f * x * x;
+      return make_float2(x * c, fmaf(x * 0.3989422804014327f, sizeof(T) == 2 ? __expf(z) : expf(z), c));
     }
     default: return make_float2(x, 1.f);
   }

@@ -36,7 +36,7 @@ __device__ __forceinline__ void finish(const FfStream& p, long long row, int f, 
     if constexpr (sizeof(T) == 2) static_cast<__nv_bfloat16*>(x)[at] = __float2bfloat16_rn(v);
     else static_cast<float*>(x)[at] = v;
   };
-  put(p.m, ff_act(g, p.act) * u);
+  put(p.m, ff_act<T>(g, p.act) * u);
   if (p.gate) {
     put(p.gate, g);
     put(p.up, u);
