@@ -65,3 +65,16 @@ def test_values(sml, act, dtype, rows, F, D):
     m = sml.ffgate_fwd(*(t.to(dtype).to(DEV) for t in (x, w_gate, w_up)), act=act).double().cpu()
     want = value_and_slope(gate.double(), act)[0]
     assert ((m - want).abs() <= tol(act, dtype) * want.abs() + LEAST).all(), float(((m - want) / want.abs().clamp(min=1e-30)).abs().max())
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("act", ["silu", "sigmoid", "gelu"])
+def test_slopes(sml, act, dtype):
+    rows, F = 300, 256
+    gate = draw(rows, F, act, dtype, 3).to(dtype).to(DEV)
+    one, eye = torch.ones_like(gate), torch.eye(F, dtype=dtype, device=DEV)
+    got = sml.ffgate_bwd(one, torch.zeros_like(gate), eye, torch.zeros_like(eye), gate, one, act=act, need=(1, 0, 0)).dx
+    _, want, size = value_and_slope(gate.double().cpu(), act)
+    # bf16 rounds the slope (half a step of it), fp32 its terms
+    bound = 2.0 ** -8 * want.abs() + 2.0 ** -16 * size if dtype == BF else tol(act, dtype) * size
+    assert ((got.double().cpu() - want).abs() <= bound + LEAST).all(), float(((got.double().cpu() - want) / size).abs().max())
