@@ -563,13 +563,13 @@ ll_status gatescan_decode_step(const gatescan_shape* shape, const void* x_t, con
  * norm: x * rsqrt(mean of x^2 + eps) (HR_RMS), x * rsqrt(sum of x^2 + eps) (HR_L2) or x (HR_NONE);
  * w (dim) fp32, shared by the heads, or NULL.  R turns the first `rot` values by pairs: pair n by
  * position * inv_freq[n] radians, (x_n, x_{n + rot/2}) (HR_HALF) or (x_2n, x_2n+1)
- * (HR_INTERLEAVED); the rest of the head stays.  Angles are exact modulo a turn to 2^-30 radians
- * at every position.
+ * (HR_INTERLEAVED); the rest of the head stays.  Angles are reduced modulo a turn to 2^-28 radians at
+ * every position, and what is left, an eighth of a turn at most, is held in fp32 (2^-25 radians).
  *   rows     1 to 2^31 - 1 tokens;  q (rows, q_heads, dim), k (rows, k_heads, dim) dtype
  *   q_heads  1 to 65536;  k_heads 0 (k is NULL) to 65536
  *   dim      1 to 256;  rot even, 0 to dim (multiples of 8 of both run faster)
  *   positions (rows) int32, may be negative; NULL: row % T, a batch of sequences from 0
- *   inv_freq  (rot / 2) fp32, finite
+ *   inv_freq  (rot / 2) fp32, below 2^63 in size
  *   eps      0 to 1 (with 0, a head whose mean or sum of squares is below 2^-126 counts as that)
  */
 enum { HR_HALF = 0, HR_INTERLEAVED = 1 };

@@ -14,7 +14,9 @@
 // registers hold, 170.
 //
 // Angles: position times frequency modulo a turn, as 64-bit integers (the frequency in 2^-64 turns),
-// so a position of a million is as exact as one of ten; the sine and cosine of what is left of the nearest quarter turn are fp32's own.
+// so a position of a million is as exact as one of ten: a unit of the frequency for each of up to 2^31 positions
+// and the low half that is left out are 1.5 steps of 2^-32 turns, 2^-28.7 radians.  What is left of the nearest
+// quarter turn is rounded to fp32 (2^-25.3 radians), and its sine and cosine are fp32's own.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -143,7 +145,7 @@ struct Held {
 
 // ---- angles ------------------------------------------------------------------------------
 // inv_freq (radians a position) in 2^-64 turns a position, modulo a turn: its mantissa times
-// floor(2^128 / (2 pi)), shifted by its exponent.
+// floor(2^128 / (2 pi)), shifted by its exponent.  From 2^64 on that constant has too few digits.
 __device__ __forceinline__ unsigned long long turns_of(float inv_freq) {
   const unsigned bits = __float_as_uint(inv_freq), field = (bits >> 23) & 255u;
   const unsigned long long m = field ? (bits & 0x7fffffu) | 0x800000u : bits & 0x7fffffu;
