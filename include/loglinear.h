@@ -506,7 +506,8 @@ ll_status blocknorm_bwd(const blocknorm_shape* shape, const void* dx_new, const 
  *     h_t = a_t h_{t-1} + u_t
  * n(a) keeps the state's size whatever the decay: sqrt(1 - a^2) (GS_RMS: a unit variance stays
  * one), 1 - a (GS_LERP: a moving average) or 1 (GS_NONE).  Without i its sigmoid is 1.
- *   batch  1 to 2^20;  T 1 to 2^30;  dim 1 to 2^20 channels (an even number runs faster)
+ *   batch  1 to 2^20;  T 1 to 2^30;  dim 1 to 2^20 channels (sequences run faster
+ *     with multiples of 8 in bf16 and of 4 in fp32, single tokens with even numbers)
  *   x, r, i, h and their gradients (B, T, dim) dtype;  decay (dim) fp32, finite; values below 0
  *   count as 0, and their gradient is 0;  states (B, dim) fp32
  * lengths: NULL, or (B) int32 on the device: row b holds lengths[b] tokens, clamped to [0, T].
@@ -515,7 +516,8 @@ ll_status blocknorm_bwd(const blocknorm_shape* shape, const void* dx_new, const 
  * r of -inf holds a state (a = 1, and n = 0 but for GS_NONE), inf decays it by exp(-decay).  GS_RMS:
  * where 1 - a^2 is below 2^-126, a decay of 0 among them, n and its slope count as 0.
  * The state and all arithmetic are fp32; h_t is rounded once, the state that goes on is not.
- * Results do not vary between calls.
+ * Results do not vary between calls of the same sizes; in another batch a row may be shared out
+ * otherwise, and its states rounded otherwise.
  */
 enum { GS_RMS = 0, GS_LERP = 1, GS_NONE = 2 };
 typedef struct {
@@ -612,12 +614,13 @@ ll_status headrope_bwd(const headrope_shape* shape, const void* dq_out, const vo
  *   x (rows, dim), w_gate and w_up (ff, dim), m (rows, ff), gradients like what they are of: dtype
  *   act   of the gate: identity, silu, sigmoid or gelu (0.5 z (1 + erf(z / sqrt 2)))
  * bf16: products of bf16 values summed in fp32, everything after them in fp32, rounded once; the
- * backward rounds the gradients of gate and up to bf16 before its products.  fp32: forward products
- * of fp32 values up to 8 rows; with more, rows of x and of the weights are two fp16 parts of values
- * scaled by their row's largest, three products each (22 bits of a value; one below 2^-18 of its
- * row's largest is within 2^-40 of that).  Backward three bf16 parts (24 bits), six products.  An
- * infinity (backward also a value beyond bf16's range) can come out as NaN in its row or column.
- * Results do not vary between calls.
+ * backward rounds the gradients of gate and up to bf16 before its products, which take nothing wider.
+ * fp32: forward products of fp32 values up to 8 rows; with more, rows of x and of the weights are two
+ * fp16 parts of values scaled by their row's largest, three products each: a value is within 2^-23
+ * of itself or 2^-39 of its row's largest, whichever is more, so that one 2^-30 of the largest has 9
+ * bits.  Backward three bf16 parts (24 bits, whatever the row), six products.  An infinity (backward
+ * also a value beyond bf16's range) can come out as NaN in its row or column.
+ * Results do not vary between calls of the same sizes on the same kind of GPU.
  */
 enum { FF_IDENTITY = 0, FF_SILU = 1, FF_SIGMOID = 2, FF_GELU = 3 };
 typedef struct {

@@ -15,10 +15,10 @@
 // derivative, a pass over memory of its own, are some 70.
 //
 // fp32 runs through the same kernel.  Forward every row of x and of the weights is summed over, so it may be
-// scaled: two fp16 parts (hi + lo, 22 bits of a value and more of the row's largest) make three products,
-// the one left out below 2^-22.  Backward the same operand is summed along both its sides, so there are
-// no scales: three bf16 parts (24 bits, over all of fp32's range), six products, what is left out below
-// 2^-24.  Forward with three parts took 60 us of 1003 x 1024 x 2816, with two 40 (fp32 operands' split by
+// scaled: two fp16 parts (hi + lo, 2^-23 of a value or 2^-39 of the row's largest) make three products, the
+// one left out below 2^-22.  Backward the gradients of gate and up are summed along both their sides (x and the
+// weights along one), so one scale a row would not do: all are three bf16 parts (24 bits, over all of fp32's
+// range), six products, what is left out below 2^-24.  Forward with three parts took 60 us of 1003 x 1024 x 2816, with two 40 (fp32 operands' split by
 // itself 9: 4 bytes read and 4 written a value).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -584,8 +584,10 @@ __global__ void __launch_bounds__(256) ff_split_kernel(const __grid_constant__ F
     put_parts<8>(static_cast<__nv_bfloat16*>(s.to[i]), at, n, v);
   }
 }
-// Rows as two fp16 parts of values scaled by a power of two that brings the largest to 2^14 .. 2^15: what
-// is lost is 2^-22 of a value, and for values below 2^-18 of their row's largest 2^-40 of that.  The scale
+// Rows as two fp16 parts of values scaled by a power of two that brings the largest to 2^14 .. 2^15.  What
+// is lost is half a step of the low part: 2^-23 of a value, and at least half of fp16's smallest step, 2^-25,
+// which is 2^-39 of a largest value of 2^14.  (Three bf16 parts lose 2^-24 of any value; with them 1003 x 1024 x
+// 2816 took 60 us instead of 41.)  The scale
 // goes back as two factors of half its exponent each, so that no product of factors leaves fp32's range.
 // W warps a row, 16 values a lane: read once up to 4096 values, or twice, the second time from the caches.
 template <int W, bool kOnce>
