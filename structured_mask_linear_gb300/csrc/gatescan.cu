@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(kGsWarps * 32, 4)
     gs_fwd_kernel(const __grid_constant__ GsArgs p, const __grid_constant__ GsMaps<2 + kGate> maps) {
   constexpr int N = 2 + kGate, L = kTokens<T, N, G>;
   extern __shared__ __align__(128) unsigned char raw[];
-  Walk<T, N, G> w(*reinterpret_cast<Shared<T, N, G>*>(raw), p);
+  Walk<T, N, G, 2> w(*reinterpret_cast<Shared<T, N, G>*>(raw), p);
   const float2 decay = not_below_0(w.pair_of(p.decay, 0));
   float2 carry = w.pair_of(p.state_in, w.b);
   const void* const from[3] = {p.r, p.x, p.i};
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kGsWarps * 32, 4)
     A = exp_minus<float>(A);
     w.s.group[step & 1][threadIdx.x] = make_float4(A.x, A.y, H.x, H.y);
     __syncthreads();
-    if (kTma && step + 2 < w.steps) w.template fetch<kTma>(maps, from, stage, t0 + 2 * stride, -1);
+    if (kTma && step + 2 < w.asked) w.template fetch<kTma>(maps, from, stage, t0 + 2 * stride, -1);
     float2 h = w.enter(step, w.group, carry);
     T* out = static_cast<T*>(p.h) + ((size_t)w.b * p.T + t) * p.D + w.c;
     if (there >= L) {

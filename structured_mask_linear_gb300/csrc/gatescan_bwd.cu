@@ -14,7 +14,7 @@ __global__ void __launch_bounds__(kGsWarps * 32, sizeof(T) == 2 ? 4 : 2)
     gs_bwd_kernel(const __grid_constant__ GsArgs p, const __grid_constant__ GsMaps<4 + kGate> maps) {
   constexpr int N = 4 + kGate, L = kTokens<T, N, G>;
   extern __shared__ __align__(128) unsigned char raw[];
-  Walk<T, N, G> w(*reinterpret_cast<Shared<T, N, G>*>(raw), p);
+  Walk<T, N, G, 1> w(*reinterpret_cast<Shared<T, N, G>*>(raw), p);
   const int turn = w.kGroups - 1 - w.group;  // place in the scan
   ptx::griddep_launch_dependents();
   const float2 given = w.pair_of(p.decay, 0), decay = not_below_0(given), minus = mul2(decay, both(-1.f));
@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kGsWarps * 32, sizeof(T) == 2 ? 4 : 2)
     w.s.group[step & 1][turn * w.kLanes + w.lane] = make_float4(A.x, A.y, H.x, H.y);
     __syncthreads();
     // the stage of the step before: all have left it
-    if (kTma && step + 1 < w.steps) w.template fetch<kTma>(maps, from, stage ^ 1, t0 - stride, 3);
+    if (kTma && step + 1 < w.asked) w.template fetch<kTma>(maps, from, stage ^ 1, t0 - stride, 3);
     float2 c = w.enter(step, turn, carry);
     const size_t last = ((size_t)w.b * p.T + t + L - 1) * p.D + w.c;
     T *ox = static_cast<T*>(p.dx) + last, *orr = static_cast<T*>(p.dr) + last, *oi = kGate ? static_cast<T*>(p.di) + last : nullptr;

@@ -148,18 +148,17 @@ constexpr int smem_bytes(int cluster) {
   return (int)sizeof(Shared<T, N, G>) + (cluster > 1 ? 2 * cluster * (32 / G) * 16 : 0);
 }
 
-// Bounded wait (2 s) for a phase; `lost` after one that ran out, and no later one is waited for.
-__device__ __forceinline__ void wait(uint64_t* bar, unsigned parity, bool& lost, unsigned* status) {
-  if (ptx::mbar_try_wait(bar, parity) || lost) return;
+// Bounded wait (2 s) for a phase.
+__device__ __forceinline__ bool waited(uint64_t* bar, unsigned parity, unsigned* status) {
   const uint64_t t0 = ptx::globaltimer_ns();
   while (true) {
 #pragma unroll 1
     for (int i = 0; i < 64; ++i)
-      if (ptx::mbar_try_wait(bar, parity)) return;
+      if (ptx::mbar_try_wait(bar, parity)) return true;
     if (ptx::globaltimer_ns() - t0 > 2000000000ull) break;
   }
-  lost = true;
   atomicExch(status, kStatusTimeout);
+  return false;
 }
 
 __device__ __forceinline__ unsigned cluster_rank() {
@@ -182,14 +181,16 @@ __device__ __forceinline__ void tell(unsigned rank, float4* p, float4 v, uint64_
 }
 
 // ---- a CTA's walk ------------------------------------------------------------------------
-// Which sequence and channels a CTA has, its place among the CTAs that share them, its steps.
-template <typename T, int N, int G>
+// Which sequence and channels a CTA has, its place among the CTAs that share them, its steps.  kAhead: how many
+// steps ahead their tokens are asked for.
+template <typename T, int N, int G, int kAhead>
 struct Walk {
   static constexpr int L = kTokens<T, N, G>, kGroups = kGsWarps * G, kLanes = 32 / G, kWide = kGsWidth / G, kRows = L * kGroups;
   Shared<T, N, G>& s;
   const GsArgs& p;
   unsigned rank, size;
   int b, c0, c, len, steps;
+  int asked;        // no step from here on is asked for: all of them but after a wait that ran out
   int lane, group;  // place in a group, and the group's in the CTA: in time order forward
   bool lost;
 
@@ -204,7 +205,7 @@ struct Walk {
     c = c0 + 2 * lane;
     len = p.T;
     if (p.lengths) len = max(0, min(p.T, __ldg(p.lengths + b)));
-    steps = p.steps;
+    asked = steps = p.steps;
     lost = false;
     if (threadIdx.x == 0) {
 #pragma unroll
@@ -217,10 +218,26 @@ struct Walk {
     __syncthreads();
     if (size > 1) cluster_sync();  // the others' shared memory and barriers are there from here on
   }
+  // For a phase of step's; `later`: the fetch within the step is behind it.  After a wait that ran out nothing is
+  // waited for, asked for or told any more.
+  __device__ __forceinline__ void wait(uint64_t* bar, int step, bool later) {
+    if (ptx::mbar_try_wait(bar, (unsigned)(step >> 1) & 1u) || lost) return;
+    if (waited(bar, (unsigned)(step >> 1) & 1u, p.status)) return;
+    lost = true;
+    asked = min(steps, step + kAhead + later);
+  }
   // After the last step: nobody leaves while others may still write to it, and all have read the state that
-  // they began from, whose place the last one may take.
+  // they began from, whose place the last one may take.  After a wait that ran out the tokens that were asked
+  // for land first, and the others' maps (within another such wait for each stage, and 0.1 ms).
   __device__ __forceinline__ void leave() {
-    if (size > 1) cluster_sync();
+    if (lost && threadIdx.x == 0)
+      for (int i = max(asked - 2, 0); i < asked; ++i) waited(&s.full[i & 1], (unsigned)(i >> 1) & 1u, p.status);
+    if (size > 1) {
+      cluster_sync();
+      if (lost)
+        for (const uint64_t t0 = ptx::globaltimer_ns(); ptx::globaltimer_ns() - t0 < 100000;) {
+        }
+    }
   }
 
   // The tokens from t0 (of tensor n from t0 - shift_n) of a step.  By TMA: one thread asks for them,
@@ -248,7 +265,7 @@ struct Walk {
   }
   template <bool kTma>
   __device__ __forceinline__ void arrived(int step) {
-    if (kTma) wait(&s.full[step & 1], (unsigned)(step >> 1) & 1u, lost, p.status);
+    if (kTma) wait(&s.full[step & 1], step, false);
     else __syncthreads();
   }
   __device__ __forceinline__ float2 token(int stage, int n, int k) const {
@@ -276,8 +293,8 @@ struct Walk {
     float2 in = carry;
     if (size > 1) {
       float4* told = s.cta + (buf * size) * kLanes;
-      if (threadIdx.x == 0) ptx::mbar_arrive_expect_tx(&s.told[buf], size * kLanes * 16);
-      if ((unsigned)group < size) {  // each group tells some of the CTAs
+      if (threadIdx.x == 0 && !lost) ptx::mbar_arrive_expect_tx(&s.told[buf], size * kLanes * 16);
+      if ((unsigned)group < size && !lost) {  // each group tells some of the CTAs
         float2 A = both(1.f), H = both(0.f);
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
@@ -288,7 +305,7 @@ struct Walk {
         for (unsigned r = group; r < size; r += kGroups)
           tell(r, told + rank * kLanes + lane, make_float4(A.x, A.y, H.x, H.y), &s.told[buf]);
       }
-      wait(&s.told[buf], (unsigned)(step >> 1) & 1u, lost, p.status);
+      wait(&s.told[buf], step, true);
       for (unsigned r = 0; r < size; ++r) {
         if (r == rank) in = carry;
         carry = applied(told[r * kLanes + lane], carry);
