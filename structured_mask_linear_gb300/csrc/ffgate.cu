@@ -267,7 +267,7 @@ __global__ void __cluster_dims__(kGroup, 1, 1) __launch_bounds__(kFfThreads, 1)
       const int part_bytes = first_operand ? a_bytes : b_bytes;
       const uint32_t bar0 = in_first(bars.full);
       uint32_t s = 0, phase = 1;  // the wait for an empty stage passes in the first turn
-      bool ok = true;
+      bool ok = true, turned = false;
       ptx::griddep_wait();  // operands may come from the kernel ahead; all else here waits for them
       for (int t = first; ok && t < p.tiles; t += stride) {
         const Tile x = tile_at(p, t);
@@ -303,12 +303,21 @@ __global__ void __cluster_dims__(kGroup, 1, 1) __launch_bounds__(kFfThreads, 1)
           if (++s == stages) {
             s = 0;
             phase ^= 1;
+            turned = true;
           }
           if (++k == kblocks) {
             k = 0;
             map = &maps.m[second];
           }
         }
+      }
+      // What was asked for lands before the CTAs end, whatever their other roles gave up (bounded, 2 s in all; each
+      // stage's bytes count in the first CTA, for both): the stages before s in this turn, the others in the one
+      // before it.
+      if (first_operand && rank == 0) {
+        bool landed = true;
+        for (uint32_t i = 0; landed && i < (uint32_t)stages; ++i)
+          if (i < s || turned) landed = ff_wait(&bars.full[i], i < s ? phase ^ 1 : phase, p.status);
       }
     }
   } else if (warp == 1 && rank == 0) {
