@@ -98,35 +98,75 @@ long long most_blocks(const FfArgs& p) {
   }
   return all + most;
 }
+void share(FfProb& r, int splits) {
+  r.share = ceil_div(r.pairs * r.kblocks, splits);
+  r.splits = ceil_div(r.pairs * r.kblocks, r.share);
+}
+// The most items that a tile may be shared by: 152 of the problem, with kLeast blocks at least.
+int most_splits(const FfProb& r, double block) {
+  const int tiles = r.tiles_m * r.tiles_n, blocks = r.pairs * r.kblocks;
+  if (tiles > 76 || (blocks - kLeast) * block < kJoinUs) return 1;
+  const int most = 152 / tiles < blocks / kLeast ? 152 / tiles : blocks / kLeast;
+  return most < 1 ? 1 : most;
+}
 // Numbers the items.  A tile's sum is shared by several where the launch would otherwise wait for it
-// (a single tile of 30 rows over 2 x 10384 values 540 us): by as many, up to 152 items of the
-// problem, as leave the least to the busiest pair, and where that saves more than joining the sums costs.
-// Returns the bytes of their sums.
+// (a single tile of 30 rows over 2 x 10384 values 540 us): by as many as leave the least to the busiest pair,
+// and where that saves more than joining the sums costs.  Found from two starts, a problem after the other: from
+// whole sums, and from shares of one size, since both weights' gradients are alike and a launch that shares one of
+// them still waits for the other (8192 x 64 x 64 41.8 -> 16.9 us, fp32 215 -> 33; 4096 x 256 x 512 27 -> 21 and 119 ->
+// 42; 1003 x 1024 x 2816, with one more sum shared, 30.1 -> 31.0).  Returns the bytes of the sums.
 size_t share_out(FfArgs& p, double block) {
-  auto split = [](FfProb& r, int splits) {
-    r.share = ceil_div(r.pairs * r.kblocks, splits);
-    r.splits = ceil_div(r.pairs * r.kblocks, r.share);
-  };
-  for (int i = 0; i < p.probs; ++i) split(p.prob[i], 1);
-  const long long whole = most_blocks(p);
+  int most[ll::kFfProbs], found[ll::kFfProbs], longest = 0;
   for (int i = 0; i < p.probs; ++i) {
     FfProb& r = p.prob[i];
-    const int tiles = r.tiles_m * r.tiles_n, blocks = r.pairs * r.kblocks;
-    if (tiles > 76 || (blocks - kLeast) * block < kJoinUs) continue;
-    int best = 1;
-    long long least = most_blocks(p);
-    for (int splits = 2; splits * tiles <= 152 && splits * kLeast <= blocks; splits += (splits + 3) / 4) {
-      split(r, splits);
-      const long long most = most_blocks(p);
-      if (most < least) {
-        least = most;
-        best = splits;
+    share(r, 1);
+    most[i] = most_splits(r, block);
+    found[i] = 1;
+    if (most[i] > 1 && r.share > longest) longest = r.share;
+  }
+  const long long whole = most_blocks(p);
+  long long least = whole;
+  // from the splits that there are, of `now` blocks
+  auto refine = [&](long long now) {
+    for (int i = 0; i < p.probs; ++i) {
+      FfProb& r = p.prob[i];
+      int best = r.splits;
+      for (int splits = 2; splits <= most[i]; splits += (splits + 3) / 4) {
+        share(r, splits);
+        const long long blocks = most_blocks(p);
+        if (blocks < now) {
+          now = blocks;
+          best = splits;
+        }
+      }
+      share(r, best);
+    }
+    if (now >= least) return;
+    least = now;
+    for (int i = 0; i < p.probs; ++i) found[i] = p.prob[i].splits;
+  };
+  if (longest) refine(whole);
+  if (longest && p.probs > 1) {
+    auto even = [&](int size) {
+      for (int i = 0; i < p.probs; ++i) {
+        const int splits = ceil_div(p.prob[i].pairs * p.prob[i].kblocks, size);
+        share(p.prob[i], splits < most[i] ? splits : most[i]);
+      }
+      return most_blocks(p);
+    };
+    int best = longest;
+    long long blocks = even(longest);
+    for (int size = longest; size >= kLeast; size -= (size + 3) / 4) {
+      const long long now = even(size);
+      if (now < blocks) {
+        blocks = now;
+        best = size;
       }
     }
-    split(r, best);
+    refine(even(best));
   }
-  if ((whole - most_blocks(p)) * block < kJoinUs)
-    for (int i = 0; i < p.probs; ++i) split(p.prob[i], 1);
+  const bool pays = (whole - least) * block >= kJoinUs;
+  for (int i = 0; i < p.probs; ++i) share(p.prob[i], pays ? found[i] : 1);
   size_t bytes = 0;
   p.tiles = 0;
   for (int i = 0; i < p.probs; ++i) {
@@ -147,7 +187,8 @@ struct Work {
   // workspace: operands that the call makes, bf16 (fp32 calls: in parts), and sums of split tiles
   size_t x, w_gate, w_up, scale, dgate, dup, part, bytes;
 };
-Work work_of(const ffgate_shape* s, bool bwd, bool dx, bool dw_gate, bool dw_up) {
+// plan: not for a bound on the bytes alone (backward).
+Work work_of(const ffgate_shape* s, bool bwd, bool dx, bool dw_gate, bool dw_up, bool plan = true) {
   Work w{};
   FfArgs& p = w.args;
   if (!bwd) {
@@ -169,7 +210,16 @@ Work work_of(const ffgate_shape* s, bool bwd, bool dx, bool dw_gate, bool dw_up)
   if (dw_gate) add_dw(kDwGate);
   if (dw_up) add_dw(kDwUp);
   if (!dx_first) add_dx();
-  const size_t parts = share_out(p, block_us(s->dtype == LL_F32, bwd));
+  const double block = block_us(s->dtype == LL_F32, bwd);
+  size_t parts = 0;
+  if (plan) {
+    parts = share_out(p, block);
+  } else {  // whatever the plan: room for the most items
+    for (int i = 0; i < p.probs; ++i) {
+      const int most = most_splits(p.prob[i], block);
+      if (most > 1) parts += a256((size_t)most * p.prob[i].rows * p.prob[i].cols * 4);
+    }
+  }
 
   const bool f32 = s->dtype == LL_F32;
   // Few rows of bf16: a stage has no more of them than there are, so that more of the weights is under way
@@ -314,13 +364,8 @@ ll_status ffgate_fwd(const ffgate_shape* s, const void* x, const void* w_gate, c
 
 size_t ffgate_bwd_workspace_bytes(const ffgate_shape* s) {
   if (check_shape(s) != LL_OK) return 0;
-  // room for whichever gradients are asked for: fewer of them may have their sums shared out further
-  size_t most = 0;
-  for (int need = 1; need < 8; ++need) {
-    const size_t n = work_of(s, true, need & 1, need & 2, need & 4).bytes;
-    most = n > most ? n : most;
-  }
-  return most;
+  // room for whichever gradients are asked for, and however their sums are shared
+  return work_of(s, true, true, true, true, false).bytes;
 }
 
 ll_status ffgate_bwd(const ffgate_shape* s, const void* dm, const void* x, const void* w_gate, const void* w_up,
