@@ -109,13 +109,18 @@ int most_splits(const FfProb& r, double block) {
   const int most = 152 / tiles < blocks / kLeast ? 152 / tiles : blocks / kLeast;
   return most < 1 ? 1 : most;
 }
+// The least items, so that no sum of bf16 products is longer than 131072 values: the tensor cores cut their sums off
+// where fp32 would round, 8e-10 a value of a random sum towards 0, which is 1e-4 of it then (a bf16 result's own
+// rounding is 1.7e-3 of it).  fp32 adds up short runs.
+constexpr int kLongest = 2048;
+int least_splits(const FfProb& r, bool f32) { return f32 ? 1 : ceil_div(r.pairs * r.kblocks, kLongest); }
 // Numbers the items.  A tile's sum is shared by several where the launch would otherwise wait for it
 // (a single tile of 30 rows over 2 x 10384 values 540 us): by as many as leave the least to the busiest pair,
 // and where that saves more than joining the sums costs.  Found from two starts, a problem after the other: from
 // whole sums, and from shares of one size, since both weights' gradients are alike and a launch that shares one of
 // them still waits for the other (8192 x 64 x 64 41.8 -> 16.9 us, fp32 215 -> 33; 4096 x 256 x 512 27 -> 21 and 119 ->
 // 42; 1003 x 1024 x 2816, with one more sum shared, 30.1 -> 31.0).  Returns the bytes of the sums.
-size_t share_out(FfArgs& p, double block) {
+size_t share_out(FfArgs& p, double block, bool f32) {
   int most[ll::kFfProbs], found[ll::kFfProbs], longest = 0;
   for (int i = 0; i < p.probs; ++i) {
     FfProb& r = p.prob[i];
@@ -166,7 +171,10 @@ size_t share_out(FfArgs& p, double block) {
     refine(even(best));
   }
   const bool pays = (whole - least) * block >= kJoinUs;
-  for (int i = 0; i < p.probs; ++i) share(p.prob[i], pays ? found[i] : 1);
+  for (int i = 0; i < p.probs; ++i) {
+    const int splits = pays ? found[i] : 1, floor = least_splits(p.prob[i], f32);
+    share(p.prob[i], splits > floor ? splits : floor);
+  }
   size_t bytes = 0;
   p.tiles = 0;
   for (int i = 0; i < p.probs; ++i) {
@@ -210,18 +218,18 @@ Work work_of(const ffgate_shape* s, bool bwd, bool dx, bool dw_gate, bool dw_up,
   if (dw_gate) add_dw(kDwGate);
   if (dw_up) add_dw(kDwUp);
   if (!dx_first) add_dx();
-  const double block = block_us(s->dtype == LL_F32, bwd);
+  const bool f32 = s->dtype == LL_F32;
+  const double block = block_us(f32, bwd);
   size_t parts = 0;
   if (plan) {
-    parts = share_out(p, block);
+    parts = share_out(p, block, f32);
   } else {  // whatever the plan: room for the most items
     for (int i = 0; i < p.probs; ++i) {
-      const int most = most_splits(p.prob[i], block);
+      const int a = most_splits(p.prob[i], block), b = least_splits(p.prob[i], f32), most = a > b ? a : b;
       if (most > 1) parts += a256((size_t)most * p.prob[i].rows * p.prob[i].cols * 4);
     }
   }
 
-  const bool f32 = s->dtype == LL_F32;
   // Few rows of bf16: a stage has no more of them than there are, so that more of the weights is under way
   // (64 x 4096 x 11008 41 -> 37 us; with weights still in L2 and 512 values a row 6.3 -> 5.4, 2048 no less).
   // fp32 gains nothing by it (the runs' adding up bounds it).
