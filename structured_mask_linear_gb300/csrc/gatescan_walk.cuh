@@ -89,7 +89,7 @@ __device__ __forceinline__ float2 rest_of(float2 e, float2 s) {
 }
 
 // m = 1 - a = 1 - e^-z for z >= 0.  Below 0.7 it is z times a polynomial in z (Chebyshev fit of
-// (1 - e^-z)/z, 1e-8 relative), since the difference would lose the small m that long memories live
+// (1 - e^-z)/z, 4e-8 relative with these coefficients), since the difference would lose the small m that long memories live
 // from.  a = 1 - m is as exact as fp32 holds it.
 template <typename T>
 __device__ __forceinline__ float2 loss_of(float2 z) {

@@ -6,8 +6,8 @@
 // and two pairs go through an instruction.  A warp takes a token and walks its heads, for which
 // angles are made once, with the next heads' values on their way.
 //
-// 32768 tokens of 24 + 24 heads of 128 132 us (6.1 TB/s, 90 % of a copy's rate), gradients of 16396
-// tokens of 32 + 8 heads 94 us (5.4, 79 %; 128 registers leave 16 warps an SM).  On the way there: two
+// 32768 tokens of 24 + 24 heads of 128 131 us (6.2 TB/s, 91 % of a copy's rate), gradients of 16396
+// tokens of 32 + 8 heads, half of each turned, 94 us (5.4, 79 %; 128 registers leave 16 warps an SM).  On the way there: two
 // values a lane and a product each, with a test for every head, 184 and 164 us; packed pairs 154 and
 // 106; weights without bank conflicts and sums without a test a step 140 and 96; pointers that step from
 // head to head instead of being made of the head's number 176; four heads on their way, more than
@@ -256,11 +256,14 @@ struct Lane {
     for (int n = 0; n < (kVec ? 1 : 4); ++n) turns[n] = Place<kVec, kHalf>::turns(unit, n, p.rot);
   }
   // The pairs that turn by t.  The others stay: a product with the sine of 0 would hand a value that is not
-  // finite on to its partner.
-  template <Heads kHeads>
+  // finite on to its partner.  Forward by predicates (139.8 us for 32768 tokens of 48 half-turned heads, 141.9 as a
+  // branch, 132.6 with those products), backward as a branch (94.0 for the gradients of 16396 of 40, 94.6, 92.6).
+  template <Heads kHeads, bool kBranch>
   __device__ __forceinline__ void turn(Eight& v, const Turn& t) const {
     if constexpr (kHeads == kWholeHeads) {
       turned(v, t);
+    } else if constexpr (kVec && kBranch) {
+      if (turns[0]) turned(v, t);
     } else if constexpr (kVec) {
 #pragma unroll
       for (int n = 0; n < 2; ++n) turned_if(turns[0], v.p[n], v.p[n + 2], t.c[n], t.s[n], t.minus[n]);
@@ -387,7 +390,7 @@ __global__ void __launch_bounds__(kHrWarps * 32, kHrFwdCtas) hr_fwd_kernel(HrArg
         const Eight w = l.weights(in_k);
 #pragma unroll
         for (int n = 0; n < 4; ++n) v.p[n] = mul2(v.p[n], mul2(w.p[n], both(r)));
-        if (kHeads != kAnyHeads || p.rot) l.template turn<kHeads>(v, t);
+        if (kHeads != kAnyHeads || p.rot) l.template turn<kHeads, false>(v, t);
         if (has) Held<T, kVec, kHalf>::store((in_k ? ko : qo) + (i0 + i) * step, l.at, v);
       }
     };
@@ -456,7 +459,7 @@ __global__ void __launch_bounds__(kHrWarps * 32, kHrBwdCtas) hr_bwd_kernel(HrArg
             v = x[i].get();
             u = y[i].get();
           }
-          if (kHeads != kAnyHeads || p.rot) l.template turn<kHeads>(u, t);
+          if (kHeads != kAnyHeads || p.rot) l.template turn<kHeads, true>(u, t);
           Eight g;
 #pragma unroll
           for (int n = 0; n < 4; ++n) g.p[n] = mul2(u.p[n], w.p[n]);

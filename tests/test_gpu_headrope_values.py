@@ -61,3 +61,36 @@ def test_without_a_norm_x_has_no_part_in_its_gradient(sml, d, rot, weights):
         keep = torch.ones(d, dtype=torch.bool)
         keep[[0, d // 2, d - 1]] = False
         assert torch.equal(got.dw_q[keep.to(DEV)], base.dw_q[keep.to(DEV)]) and not torch.isfinite(got.dw_q[~keep.to(DEV)]).any()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("layout", ["half", "inter"])
+@pytest.mark.parametrize("norm", ["rms", "l2"])
+@pytest.mark.parametrize("d,rot", [(128, 64), (128, 128), (64, 16), (80, 40), (33, 6)])
+def test_under_a_norm(sml, d, rot, norm, layout, dtype):
+    """An infinity makes its head's inverse norm 0: the others become 0, and it NaN, with the value that it turns
+    with.  An infinite dy past the rotated part reaches its own weight's gradient and its head alone."""
+    from decoder_ref import headrope
+
+    g = torch.Generator().manual_seed(d)
+    q, dq = (torch.randn((3, 4, d), generator=g).to(dtype) for _ in range(2))
+    p = torch.tensor([5, 3, 1 << 20], dtype=torch.int32)
+    w, f = 1 + 0.3 * torch.rand(d, generator=g), sml.rope_frequencies(rot, device="cpu")
+    kw = dict(w_q=w.to(DEV), inv_freq=f.to(DEV), positions=p.to(DEV), layout=layout, norm=norm)
+    for n in {0, rot // 2, rot - 1, rot % d, (rot + 4) % d, d - 1}:
+        x = q.clone()
+        x[1, 2, n] = LOST[1 + n % 2]
+        y = sml.headrope_fwd(x.to(DEV), **kw)[0].cpu()
+        want = headrope(x.double(), w.double(), f, p, layout, norm, 1e-6)
+        assert torch.equal(y.isnan(), want.isnan()) and int(y.isnan().sum()) == (2 if n < rot else 1), n
+        assert not y[1, 2].nan_to_num().any() and torch.isfinite(y[[0, 2]]).all()
+    base = sml.headrope_bwd(dq.to(DEV), q.to(DEV), **kw)
+    for n in range(rot, d, 5):
+        dy = dq.clone()
+        dy[1, 2, n] = LOST[n % 3]
+        got = sml.headrope_bwd(dy.to(DEV), q.to(DEV), **kw)
+        other = torch.ones((3, 4), dtype=torch.bool)
+        other[1, 2] = False
+        assert torch.equal(got.dq[other.to(DEV)], base.dq[other.to(DEV)]) and not torch.isfinite(got.dq[1, 2]).any(), n
+        own = torch.arange(d, device=DEV) == n
+        assert not torch.isfinite(got.dw_q[own]).any() and torch.equal(got.dw_q[~own], base.dw_q[~own]), n
