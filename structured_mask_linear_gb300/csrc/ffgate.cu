@@ -10,8 +10,8 @@
 // Wu: a thread has a gate and its up value in one row, and only their product goes out.  With few
 // rows the tiles are narrower, so that every pair has one (ffgate_api.cu).
 //
-// 8192 x 4096 x 11008 856 us under the power cap (1.73 PFLOP/s, what a library product sustains) and 725
-// in a burst; gradients of 8192 x 2048 x 5632 508 us, of which the products of dm with the activation's
+// 8192 x 4096 x 11008 850 to 876 us under the power cap (1.69 to 1.74 PFLOP/s; a library product sustains 1.73) and
+// 725 in a burst; gradients of 8192 x 2048 x 5632 490 to 523 us, of which the products of dm with the activation's
 // derivative, a pass over memory of its own, are some 70.
 //
 // fp32 runs through the same kernel.  Forward every row of x and of the weights is summed over, so it may be
@@ -659,6 +659,9 @@ __global__ void __launch_bounds__(256) ff_halves_kernel(const __grid_constant__ 
     }
   }
 }
+// The gradients of gate and up, as the products take them: in bf16 rounded to one part, which makes the weights'
+// and x's gradients off by 2.3e-3 of their norm instead of 1.7e-3: two independent roundings instead of one.  A second
+// part would be twice the products, another 437 us at 8192 x 2048 x 5632.
 template <typename T>
 __global__ void __launch_bounds__(256) ff_act_bwd_kernel(const T* dm, const T* gate, const T* up, __nv_bfloat16* dgate,
                                                          __nv_bfloat16* dup, long long n, int act) {

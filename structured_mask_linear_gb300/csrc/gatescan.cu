@@ -8,11 +8,12 @@
 // (a_t, u_t) in registers; the CTAs write their maps into one another's shared memory; then each knows
 // what enters its tokens and the next step, and applies it.
 //
-// At 4 x 8192 x 2560 138 us forward (4.9 TB/s, 72 % of a copy's rate) and 253 backward (5.3, 78 %); 100003
-// tokens of 2048 channels 397 (4.1, 61 %).  What bounds it: 35 instructions a value forward on 16
-// warps an SM, a quarter of their time in the special functions' unit (three exponentials, two
-// reciprocals, a root), and the maps' way round, some 1300 cycles a step that only the SM's other CTAs
-// fill.  Measured on the way there (the first of these): chunks of a sequence handed on through flags
+// At 4 x 8192 x 2560 139 us forward (4.8 TB/s, 71 % of a copy's rate) and 254 backward (5.3, 78 %), in fp32 222
+// and 444 (both 89 %); 100003 tokens of 2048 channels 398 (4.1, 61 %).  What bounds bf16: waiting.  35
+// instructions a value forward (77 us of the 139 if they were issued without a pause) on 16 warps an SM,
+// the special functions' unit 38 % busy (three exponentials, two reciprocals, a root), and the maps' way round,
+// some 1300 cycles a step that only the SM's other CTAs fill.  Rows that are not whole 16 bytes are copied value by
+// value between barriers: 4 x 8192 x 2562 706 and 1203 us.  Measured on the way there (the first of these): chunks of a sequence handed on through flags
 // in global memory 402 us; clusters with a barrier for every step (it waits for the stores to global
 // memory too) and loads into registers 243; tokens by TMA and maps by asynchronous stores 174; four
 // CTAs of four warps instead of two of eight 141.  Both sigmoids by one reciprocal of their product
