@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(kGsWarps * 32, 4)
       }
     }
   }
-  w.leave();
+  w.template leave<kTma>();
   if (p.state_out && w.rank == 0 && w.group == 0) w.put_pair(p.state_out, w.b, carry);
 }
 

@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kGsWarps * 32, sizeof(T) == 2 ? 4 : 2)
       }
     }
   }
-  w.leave();
+  w.template leave<kTma>();
   if (p.dstate_in && w.rank == 0 && turn == 0) w.put_pair(p.dstate_in, w.b, carry);
   if (p.part) {
     __syncthreads();

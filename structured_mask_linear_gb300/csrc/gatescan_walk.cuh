@@ -229,8 +229,9 @@ struct Walk {
   // After the last step: nobody leaves while others may still write to it, and all have read the state that
   // they began from, whose place the last one may take.  After a wait that ran out the tokens that were asked
   // for land first, and the others' maps (within another such wait for each stage, and 0.1 ms).
+  template <bool kTma>
   __device__ __forceinline__ void leave() {
-    if (lost && threadIdx.x == 0)
+    if (kTma && lost && threadIdx.x == 0)
       for (int i = max(asked - 2, 0); i < asked; ++i) waited(&s.full[i & 1], (unsigned)(i >> 1) & 1u, p.status);
     if (size > 1) {
       cluster_sync();
