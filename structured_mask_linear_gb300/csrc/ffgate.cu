@@ -661,9 +661,11 @@ __global__ void __launch_bounds__(256) ff_halves_kernel(const __grid_constant__ 
 }
 // The gradients of gate and up, as the products take them: in bf16 rounded to one part, which makes the weights'
 // and x's gradients off by 2.3e-3 of their norm instead of 1.7e-3: two independent roundings instead of one.  A second
-// part would be twice the products, another 437 us at 8192 x 2048 x 5632.
+// part would be twice the products, another 437 us at 8192 x 2048 x 5632.  (bf16 in 32 registers, so that all 16 CTAs
+// of an SM run in two full turns: in 40 the SMs were done apart, and the pairs of CTAs of the products behind them
+// began apart, 504 -> 546 us for 8831 x 552 x 10768.)
 template <typename T>
-__global__ void __launch_bounds__(256) ff_act_bwd_kernel(const T* dm, const T* gate, const T* up, __nv_bfloat16* dgate,
+__global__ void __launch_bounds__(256, sizeof(T) == 2 ? 8 : 5) ff_act_bwd_kernel(const T* dm, const T* gate, const T* up, __nv_bfloat16* dgate,
                                                          __nv_bfloat16* dup, long long n, int act) {
   constexpr int V = sizeof(T) == 2 ? 8 : 4;
   ptx::griddep_launch_dependents();
